@@ -4,7 +4,8 @@
  * The library packs tokenized sequences as one radix tree per training row
  * (a host packer) and runs causal tree attention over the packed rows on a
  * GB300 (sm_103a): tile classification, forward (O, LSE) and backward
- * (dQ, dK, dV).  Sources, by page and section:
+ * (dQ, dK, dV), and the operators before and after it.  Sources, by page and
+ * section:
  *
  *   [P1] "Prefix tree packing" (furtherai.github.io/blog/posts/prefix-tree-packing):
  *        tree-build section (the recursive walk, minimum shared-segment length,
@@ -516,6 +517,197 @@ stp_status stp_gdn_fwd_train(const stp_gdn_desc* desc, const void* plan, const v
 stp_status stp_gdn_bwd(const stp_gdn_desc* desc, const void* plan, const void* d_plan, const void* x,
                        const float* conv_w, const float* g, const float* beta, const float* d_o, float* dx,
                        float* dconv_w, float* dg, float* dbeta, void* d_ws, void* stream);
+
+/*
+ * Norm and rotation of queries and keys, one pass ([P1] materialization
+ * section: position ids are depths, so that a token of a packed row is
+ * rotated as in its own sequence).  For every head vector x of a token at
+ * position t, with w = w_q for queries and w_k for keys:
+ *   n = x w / sqrt(mean(x^2) + eps)
+ *   (y_a, y_b) = (n_a cos f t - n_b sin f t, n_a sin f t + n_b cos f t)
+ * over the pairs (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1) when
+ * interleaved, with f = inv_freq[i]; channels from rotary_dim on pass as n.
+ * Sums and products are float32, each output is rounded once; the angle is
+ * reduced exactly, at any position.
+ */
+typedef struct {
+  int32_t n_tokens;    /* N >= 0 (rows of a batch back to back)                  */
+  int32_t n_q_heads;   /* Hq in [1, 4096]                                        */
+  int32_t n_kv_heads;  /* Hkv in [1, 4096]                                       */
+  int32_t head_dim;    /* D, a multiple of 16 in [16, 512]                       */
+  int32_t rotary_dim;  /* rotated channels, a multiple of 16 in [0, D]           */
+  int32_t interleaved; /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1) */
+  int32_t dtype;       /* STP_BF16 or STP_FP32, of every tensor but the weights  */
+  float eps;           /* in [0, 1]                                              */
+  int64_t q_stride;    /* elements between tokens of q and dx_q: at least Hq * D, */
+  int64_t k_stride;    /* of k and dx_k: at least Hkv * D; multiples of 16 bytes */
+} stp_qk_desc;
+
+/* Device workspace of stp_qk_norm_rope_bwd: 2432 bytes per channel of a head. */
+stp_status stp_qk_norm_rope_workspace_size(const stp_qk_desc* desc, size_t* ws_bytes);
+
+/*
+ *   q, k            device, token rows q_stride / k_stride elements apart (a
+ *                   fused projection's output is read in place)
+ *   w_q, w_k        device float32 [D], or NULL for ones
+ *   inv_freq        HOST double [rotary_dim / 2], radians per position; read
+ *                   during the call (NULL only when rotary_dim is 0)
+ *   d_position_ids  device int32 [N]
+ *   q_out, k_out    device [N, Hq, D] and [N, Hkv, D], contiguous, as
+ *                   stp_attn_fwd takes them.  q_out may be q, and k_out k,
+ *                   where that tensor is contiguous.
+ * Tensors are 16-byte aligned.  No workspace and no device checks.
+ * Errors: STP_EINVAL, STP_EUNSUPPORTED (descriptor), STP_ECUDA.
+ */
+stp_status stp_qk_norm_rope_fwd(const stp_qk_desc* desc, const void* q, const void* k, const float* w_q,
+                                const float* w_k, const double* inv_freq, const int32_t* d_position_ids,
+                                void* q_out, void* k_out, void* stream);
+
+/*
+ * Backward, from the forward's inputs: with g the inverse rotation of d_q (d_k)
+ * and r = 1 / sqrt(mean(x^2) + eps),
+ *   dw = sum over tokens and heads of g x r,   dx = r (g w - x r^2 mean(g w x)).
+ *   d_q, d_k    device [N, Hq, D] and [N, Hkv, D], contiguous
+ *   dx_q, dx_k  device, strided like q and k (parts of a fused gradient; what
+ *               lies between is not touched); may be q and k themselves
+ *   dw_q, dw_k  device float32 [D], written in full (of the scale in use also
+ *               where the weight is NULL)
+ *   d_ws        device, stp_qk_norm_rope_workspace_size bytes, 256-byte aligned
+ * Every sum is taken in a fixed order: repeated calls give the same bits.
+ */
+stp_status stp_qk_norm_rope_bwd(const stp_qk_desc* desc, const void* q, const void* k, const float* w_q,
+                                const float* w_k, const double* inv_freq, const int32_t* d_position_ids,
+                                const void* d_q, const void* d_k, void* dx_q, void* dx_k, float* dw_q, float* dw_k,
+                                void* d_ws, void* stream);
+
+/*
+ * Tree attention with a sliding window and visible first tokens ([P1]
+ * attention section, for layers that see only near tokens).  Distances are
+ * taken along a token's own path, where position ids are depths: query i sees
+ *   V(i) = { j : j <= i, subtree_end[j] >= i,
+ *            position[i] - position[j] < window  or  position[j] < n_sink },
+ * exactly what the sequence alone would see under the same window.  Outputs,
+ * types, layouts, workspaces and errors are those of stp_classify,
+ * stp_attn_fwd and stp_attn_bwd; window >= 1 and n_sink >= 0 (STP_EINVAL), and
+ * all three calls of a batch take the same two.
+ *   d_position_ids  device int32 [R, T] as written by stp_plan_write, 16-byte
+ *                   aligned; a value outside [0, 2^30) sets tile_meta's device
+ *                   error word
+ * stp_count_window_tile_pairs is the exact number of non-empty tile pairs
+ * (host arrays; a window lists fewer than the whole tree), for
+ * stp_attn_desc.max_tile_pairs.
+ */
+stp_status stp_count_window_tile_pairs(const int32_t* subtree_end, const int32_t* position_ids, int32_t n_rows,
+                                       int32_t row_len, int32_t window, int32_t n_sink, int64_t* n_pairs);
+stp_status stp_classify_window(const stp_attn_desc* desc, int32_t window, int32_t n_sink,
+                               const int32_t* d_subtree_end, const int32_t* d_position_ids, void* d_tile_meta,
+                               void* stream);
+stp_status stp_attn_window_fwd(const stp_attn_desc* desc, int32_t window, int32_t n_sink, const void* q,
+                               const void* k, const void* v, const int32_t* d_subtree_end,
+                               const int32_t* d_position_ids, const void* d_tile_meta, void* o, float* lse,
+                               void* d_ws, void* stream);
+stp_status stp_attn_window_bwd(const stp_attn_desc* desc, int32_t window, int32_t n_sink, const void* q,
+                               const void* k, const void* v, const void* o, const float* lse, const void* d_o,
+                               const int32_t* d_subtree_end, const int32_t* d_position_ids, const void* d_tile_meta,
+                               void* dq, void* dk, void* dv, void* d_ws, void* stream);
+
+/*
+ * Statistics of rows of logits: the log-probability of a given token, the
+ * entropy, and the most likely tokens ([P1] materialization section: packed
+ * rows carry per-token logprobs of their trainable tokens; position x scores
+ * token x + 1).  With z = scale * logits[n] and lse = ln sum_v exp(z_v):
+ *   logprob[n] = z_target - lse,   entropy[n] = lse - sum_v exp(z_v - lse) z_v,
+ *   top_id[n], top_logprob[n]: the top_k largest logits, descending, ties to
+ *   the smaller id, and their z - lse; logits of -inf are not listed, and
+ *   missing entries are id -1 with -inf.
+ * Logits of -inf have probability 0 and add nothing.  A row of nothing else
+ * has lse = logprob = -inf and entropy 0; one that holds NaN or +inf has NaN
+ * in lse, logprob, entropy and top_logprob.  All sums are float32.
+ */
+typedef struct {
+  int32_t n_rows;  /* N >= 0                                                    */
+  int32_t vocab;   /* V in [1, 2^24]                                            */
+  int64_t stride;  /* elements between rows of logits (and of d_logits), >= V   */
+  int32_t dtype;   /* STP_BF16 or STP_FP32, of logits and d_logits              */
+  float scale;     /* positive, e.g. 1 / temperature                            */
+  int32_t top_k;   /* in [0, 32]                                                */
+} stp_stats_desc;
+
+/* Device workspace of stp_token_stats_fwd (its error word). */
+stp_status stp_token_stats_workspace_size(const stp_stats_desc* desc, size_t* ws_bytes);
+
+/*
+ *   logits       device [N, V], rows stride elements apart; rows of any
+ *                alignment of their type
+ *   d_targets    device int32 [N]: the token to score; negative: the row is
+ *                not read, and gets logprob = entropy = lse = 0 and no tokens
+ *   logprob, entropy, lse       device float32 [N]
+ *   top_id, top_logprob         device int32 / float32 [N, top_k] (may be NULL
+ *                               when top_k is 0)
+ *   d_ws         device, 256-byte aligned; its first word is the device error
+ *                word: a target >= V sets it, and gives logprob NaN
+ */
+stp_status stp_token_stats_fwd(const stp_stats_desc* desc, const void* logits, const int32_t* d_targets,
+                               float* logprob, float* entropy, float* lse, int32_t* top_id, float* top_logprob,
+                               void* d_ws, void* stream);
+
+/*
+ * Gradient of sum_n d_logprob[n] logprob[n] + d_entropy[n] entropy[n]:
+ *   d_logits_v = scale (d_logprob ([v = target] - p_v) - d_entropy p_v (ln p_v + entropy))
+ * with p = exp(z - lse); lse and entropy are the forward's.  d_entropy may be
+ * NULL (zero).  d_logits (strided like logits, may be logits itself) is
+ * written for every row: zeros where the target is negative or not below V.
+ */
+stp_status stp_token_stats_bwd(const stp_stats_desc* desc, const void* logits, const int32_t* d_targets,
+                               const float* lse, const float* entropy, const float* d_logprob,
+                               const float* d_entropy, void* d_logits, void* stream);
+
+/*
+ * Distillation from a teacher's top logits, on rows of the student's logits.
+ * With z = scale * logits[n], p = softmax(z) over the vocabulary, and q the
+ * softmax of scale * teacher_logits[n] over the listed ids:
+ *   loss[n] = sum_k q_k (ln q_k - ln p_{id_k})
+ *   d_logits_v = d_loss[n] scale (p_v - sum_{k : id_k = v} q_k)
+ * A negative id is an absent entry (as is one whose teacher logit is -inf); an
+ * id may be listed twice.  A row whose loss_mask is 0 or that lists no id is
+ * not read: loss = lse = 0 and a gradient of zeros.  All sums are float32 in a
+ * fixed order.
+ */
+typedef struct {
+  int32_t n_rows;    /* N >= 0                                                  */
+  int32_t vocab;     /* V in [1, 2^24]                                          */
+  int64_t stride;    /* elements between rows of logits (and of d_logits), >= V */
+  int32_t dtype;     /* STP_BF16 or STP_FP32, of logits and d_logits            */
+  float scale;       /* positive, 1 / temperature of both softmaxes             */
+  int32_t n_teacher; /* K in [1, 256]: listed ids of a row                      */
+} stp_distill_desc;
+
+/* Device workspace of stp_distill_fwd and stp_distill_step (their error word). */
+stp_status stp_distill_workspace_size(const stp_distill_desc* desc, size_t* ws_bytes);
+
+/*
+ *   logits          device [N, V], rows stride elements apart, any alignment
+ *   teacher_ids     device int32 [N, K];  teacher_logits device float32 [N, K]
+ *   d_loss_mask     device uint8 [N], or NULL (every row)
+ *   loss, lse       device float32 [N]
+ *   d_loss          device float32 [N]: the weight of each row's loss
+ *   d_logits        device, strided like logits; may be logits itself
+ *   d_ws            device, 256-byte aligned; its first word is the device
+ *                   error word: an id >= V in a row that is read sets it, and
+ *                   counts as absent
+ * stp_distill_bwd takes the forward's lse.  stp_distill_step is the forward
+ * and the backward in one launch, for weights that are known beforehand: each
+ * row's logits are read from memory once.
+ */
+stp_status stp_distill_fwd(const stp_distill_desc* desc, const void* logits, const int32_t* teacher_ids,
+                           const float* teacher_logits, const uint8_t* d_loss_mask, float* loss, float* lse,
+                           void* d_ws, void* stream);
+stp_status stp_distill_bwd(const stp_distill_desc* desc, const void* logits, const int32_t* teacher_ids,
+                           const float* teacher_logits, const uint8_t* d_loss_mask, const float* lse,
+                           const float* d_loss, void* d_logits, void* stream);
+stp_status stp_distill_step(const stp_distill_desc* desc, const void* logits, const int32_t* teacher_ids,
+                            const float* teacher_logits, const uint8_t* d_loss_mask, const float* d_loss,
+                            float* loss, float* lse, void* d_logits, void* d_ws, void* stream);
 
 /*
  * Read the device error word of a workspace (fwd_ws or bwd_ws): synchronizes

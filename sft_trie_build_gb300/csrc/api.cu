@@ -10,6 +10,12 @@
 
 namespace stp {
 
+stp_status check_window(int32_t window, int32_t n_sink) {
+  if (window < 1) return fail(STP_EINVAL, "window must be at least 1 (got %d)", window);
+  if (n_sink < 0) return fail(STP_EINVAL, "n_sink must be >= 0 (got %d)", n_sink);
+  return STP_OK;
+}
+
 stp_status check_desc(const stp_attn_desc* d) {
   if (!d) return fail(STP_EINVAL, "attention descriptor is NULL");
   if (d->n_rows < 0) return fail(STP_EINVAL, "n_rows < 0");
@@ -62,20 +68,38 @@ static stp_status fill_common(const stp_attn_desc* d, const int32_t* se, const v
 
 using namespace stp;
 
-extern "C" stp_status stp_attn_fwd(const stp_attn_desc* desc, const void* q, const void* k,
-                                   const void* v, const int32_t* d_subtree_end,
-                                   const void* d_tile_meta, void* o, float* lse, void* d_ws,
-                                   void* stream) {
+// The positions and the window of windowed attention (nullptr: none).
+struct Window {
+  const int32_t* pos;
+  int32_t window, n_sink;
+};
+
+static stp_status set_window(const char* name, const Window* w, AttnArgs& a) {
+  if (!w) return STP_OK;
+  if (!w->pos) return fail(STP_EINVAL, "%s: NULL device pointer", name);
+  if (misaligned(w->pos, 16)) return fail(STP_EINVAL, "%s: position_ids must be 16-byte aligned", name);
+  a.pos = w->pos;
+  a.window = clip_window(w->window);
+  a.n_sink = w->n_sink;
+  return STP_OK;
+}
+
+static stp_status attn_fwd(const char* name, const Window* win, const stp_attn_desc* desc, const void* q, const void* k,
+                           const void* v, const int32_t* d_subtree_end, const void* d_tile_meta, void* o, float* lse,
+                           void* d_ws, void* stream) {
   clear_error();
   stp_status st = check_desc(desc);
+  if (!st && win) st = check_window(win->window, win->n_sink);
   if (st) return st;
   if (!q || !k || !v || !d_subtree_end || !d_tile_meta || !o || !lse || !d_ws)
-    return fail(STP_EINVAL, "stp_attn_fwd: NULL device pointer");
+    return fail(STP_EINVAL, "%s: NULL device pointer", name);
   if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) ||
       misaligned(lse, 16) || misaligned(d_tile_meta, 256) || misaligned(d_ws, 256))
-    return fail(STP_EINVAL, "stp_attn_fwd: tensors must be 16-byte and workspaces 256-byte aligned");
-  if (desc->n_rows == 0) return STP_OK;
+    return fail(STP_EINVAL, "%s: tensors must be 16-byte and workspaces 256-byte aligned", name);
   AttnArgs a{};
+  st = set_window(name, win, a);
+  if (st) return st;
+  if (desc->n_rows == 0) return STP_OK;
   fill_common(desc, d_subtree_end, d_tile_meta, a);
   a.q = q;
   a.k = k;
@@ -91,27 +115,29 @@ extern "C" stp_status stp_attn_fwd(const stp_attn_desc* desc, const void* q, con
   } else {
     e = simt_fwd(a, false, s);
   }
-  if (e != cudaSuccess) return fail(STP_ECUDA, "stp_attn_fwd: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return fail(STP_ECUDA, "%s: %s", name, cudaGetErrorString(e));
   return STP_OK;
 }
 
-extern "C" stp_status stp_attn_bwd(const stp_attn_desc* desc, const void* q, const void* k,
-                                   const void* v, const void* o, const float* lse,
-                                   const void* d_o, const int32_t* d_subtree_end,
-                                   const void* d_tile_meta, void* dq, void* dk, void* dv,
-                                   void* d_ws, void* stream) {
+static stp_status attn_bwd(const char* name, const Window* win, const stp_attn_desc* desc, const void* q, const void* k,
+                           const void* v, const void* o, const float* lse, const void* d_o,
+                           const int32_t* d_subtree_end, const void* d_tile_meta, void* dq, void* dk, void* dv,
+                           void* d_ws, void* stream) {
   clear_error();
   stp_status st = check_desc(desc);
+  if (!st && win) st = check_window(win->window, win->n_sink);
   if (st) return st;
   if (!q || !k || !v || !o || !lse || !d_o || !d_subtree_end || !d_tile_meta || !dq || !dk ||
       !dv || !d_ws)
-    return fail(STP_EINVAL, "stp_attn_bwd: NULL device pointer");
+    return fail(STP_EINVAL, "%s: NULL device pointer", name);
   if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(o, 16) ||
       misaligned(lse, 16) || misaligned(d_o, 16) || misaligned(dq, 16) || misaligned(dk, 16) ||
       misaligned(dv, 16) || misaligned(d_tile_meta, 256) || misaligned(d_ws, 256))
-    return fail(STP_EINVAL, "stp_attn_bwd: tensors must be 16-byte and workspaces 256-byte aligned");
-  if (desc->n_rows == 0) return STP_OK;
+    return fail(STP_EINVAL, "%s: tensors must be 16-byte and workspaces 256-byte aligned", name);
   AttnArgs a{};
+  st = set_window(name, win, a);
+  if (st) return st;
+  if (desc->n_rows == 0) return STP_OK;
   fill_common(desc, d_subtree_end, d_tile_meta, a);
   a.q = q;
   a.k = k;
@@ -142,6 +168,40 @@ extern "C" stp_status stp_attn_bwd(const stp_attn_desc* desc, const void* q, con
   } else {
     e = simt_bwd(a, false, s);
   }
-  if (e != cudaSuccess) return fail(STP_ECUDA, "stp_attn_bwd: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return fail(STP_ECUDA, "%s: %s", name, cudaGetErrorString(e));
   return STP_OK;
+}
+
+extern "C" stp_status stp_attn_fwd(const stp_attn_desc* desc, const void* q, const void* k,
+                                   const void* v, const int32_t* d_subtree_end,
+                                   const void* d_tile_meta, void* o, float* lse, void* d_ws,
+                                   void* stream) {
+  return attn_fwd("stp_attn_fwd", nullptr, desc, q, k, v, d_subtree_end, d_tile_meta, o, lse, d_ws, stream);
+}
+
+extern "C" stp_status stp_attn_bwd(const stp_attn_desc* desc, const void* q, const void* k,
+                                   const void* v, const void* o, const float* lse,
+                                   const void* d_o, const int32_t* d_subtree_end,
+                                   const void* d_tile_meta, void* dq, void* dk, void* dv,
+                                   void* d_ws, void* stream) {
+  return attn_bwd("stp_attn_bwd", nullptr, desc, q, k, v, o, lse, d_o, d_subtree_end, d_tile_meta, dq, dk, dv, d_ws,
+                  stream);
+}
+
+extern "C" stp_status stp_attn_window_fwd(const stp_attn_desc* desc, int32_t window, int32_t n_sink, const void* q,
+                                          const void* k, const void* v, const int32_t* d_subtree_end,
+                                          const int32_t* d_position_ids, const void* d_tile_meta, void* o, float* lse,
+                                          void* d_ws, void* stream) {
+  const Window w = {d_position_ids, window, n_sink};
+  return attn_fwd("stp_attn_window_fwd", &w, desc, q, k, v, d_subtree_end, d_tile_meta, o, lse, d_ws, stream);
+}
+
+extern "C" stp_status stp_attn_window_bwd(const stp_attn_desc* desc, int32_t window, int32_t n_sink, const void* q,
+                                          const void* k, const void* v, const void* o, const float* lse,
+                                          const void* d_o, const int32_t* d_subtree_end,
+                                          const int32_t* d_position_ids, const void* d_tile_meta, void* dq, void* dk,
+                                          void* dv, void* d_ws, void* stream) {
+  const Window w = {d_position_ids, window, n_sink};
+  return attn_bwd("stp_attn_window_bwd", &w, desc, q, k, v, o, lse, d_o, d_subtree_end, d_tile_meta, dq, dk, dv, d_ws,
+                  stream);
 }

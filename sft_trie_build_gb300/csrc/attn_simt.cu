@@ -34,6 +34,11 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
   return __float2bfloat16_rn(x);
 }
 
+// Whether a key at pos_j of a query's path is near enough, or among the first tokens.
+__device__ __forceinline__ bool in_window(const AttnArgs& a, int pos_i, int pos_j) {
+  return pos_i - pos_j < a.window || pos_j < a.n_sink;
+}
+
 // Loads rows [row0, row0+n) of one head of a [R, T, H, D] tensor into
 // shared memory with row stride `ld` floats.
 template <typename Tin, int D>
@@ -45,13 +50,14 @@ __device__ __forceinline__ void stage_rows(float* dst, int ld, const Tin* src, s
   }
 }
 
-template <typename Tin, int D>
+template <typename Tin, int D, bool WIN>
 __global__ void __launch_bounds__(256) fwd_simt_kernel(AttnArgs a) {
   constexpr int DH = D / 2;
   extern __shared__ float sm[];
   float* Ks = sm;                  // [128][D]
   float* Vs = Ks + kTile * D;      // [128][D]
   int* se_s = reinterpret_cast<int*>(Vs + kTile * D);
+  int* pos_s = se_s + kTile;       // windowed attention only
   const int qt = blockIdx.x, h = blockIdx.y, r = blockIdx.z;
   const int tid = threadIdx.x, t = tid >> 1, half = tid & 1;
   const int T = a.T, NT = T / kTile, G = a.Hq / a.Hkv, g = h / G;
@@ -61,6 +67,7 @@ __global__ void __launch_bounds__(256) fwd_simt_kernel(AttnArgs a) {
   const Tin* K = static_cast<const Tin*>(a.k);
   const Tin* V = static_cast<const Tin*>(a.v);
   const float qs = a.scale * kLog2e;
+  const int pos_i = WIN ? a.pos[rowT + i] : 0;
   float qv[DH], o[DH];
 #pragma unroll
   for (int d = 0; d < DH; ++d) {
@@ -80,6 +87,7 @@ __global__ void __launch_bounds__(256) fwd_simt_kernel(AttnArgs a) {
     stage_rows<Tin, D>(Ks, D, K, rowT + k0, a.Hkv, g, kTile, tid, 256);
     stage_rows<Tin, D>(Vs, D, V, rowT + k0, a.Hkv, g, kTile, tid, 256);
     if (tid < kTile) se_s[tid] = a.se[rowT + k0 + tid];
+    if (WIN && tid < kTile) pos_s[tid] = a.pos[rowT + k0 + tid];
     __syncthreads();
     for (int c0 = 0; c0 < kTile; c0 += 32) {
       float s[32];
@@ -92,7 +100,8 @@ __global__ void __launch_bounds__(256) fwd_simt_kernel(AttnArgs a) {
         for (int d = 0; d < DH; ++d) acc = fmaf(qv[d], kr[d], acc);
         acc += __shfl_xor_sync(0xffffffffu, acc, 1);
         const int j = k0 + c0 + c;
-        const bool vis = !part || (j <= i && se_s[c0 + c] >= i);
+        const bool vis = !part || (j <= i && se_s[c0 + c] >= i &&
+                                   (!WIN || in_window(a, pos_i, pos_s[c0 + c])));
         s[c] = vis ? acc : -INFINITY;
         mx = fmaxf(mx, s[c]);
       }
@@ -143,7 +152,7 @@ __global__ void __launch_bounds__(256) delta_kernel(AttnArgs a) {
 
 constexpr int kChunk = 32;  // query / key rows staged per step in the backward
 
-template <typename Tin, int D>
+template <typename Tin, int D, bool WIN>
 __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
   constexpr int DH = D / 2, LD = D + 1;
   extern __shared__ float sm[];
@@ -153,6 +162,7 @@ __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
   float* dOc = Qc + kChunk * D;     // [32][D]
   float* lse2 = dOc + kChunk * D;   // [32]
   float* dlt = lse2 + kChunk;       // [32]
+  int* pos_c = reinterpret_cast<int*>(dlt + kChunk);  // [32], windowed attention only
   const int kt = blockIdx.x, g = blockIdx.y, r = blockIdx.z;
   const int tid = threadIdx.x, t = tid >> 1, half = tid & 1;
   const int T = a.T, NT = T / kTile, G = a.Hq / a.Hkv;
@@ -165,6 +175,7 @@ __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
   stage_rows<Tin, D>(Kown, LD, K, rowT + kt * kTile, a.Hkv, g, kTile, tid, 256);
   stage_rows<Tin, D>(Vown, LD, V, rowT + kt * kTile, a.Hkv, g, kTile, tid, 256);
   const int sej = a.se[rowT + j];
+  const int pos_j = WIN ? a.pos[rowT + j] : 0;
   const float qs = a.scale * kLog2e;
   float dk[DH], dv[DH];
 #pragma unroll
@@ -189,6 +200,7 @@ __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
         if (tid < kChunk) {
           lse2[tid] = a.lse[((size_t)r * a.Hq + h) * T + i0 + tid] * kLog2e;
           dlt[tid] = a.delta[((size_t)r * a.Hq + h) * T + i0 + tid];
+          if (WIN) pos_c[tid] = a.pos[rowT + i0 + tid];
         }
         __syncthreads();
         for (int c = 0; c < kChunk; ++c) {
@@ -203,7 +215,7 @@ __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
           }
           s += __shfl_xor_sync(0xffffffffu, s, 1);
           dp += __shfl_xor_sync(0xffffffffu, dp, 1);
-          const bool vis = !part || (j <= i && sej >= i);
+          const bool vis = !part || (j <= i && sej >= i && (!WIN || in_window(a, pos_c[c], pos_j)));
           const float p = vis ? exp2f(s * qs - lse2[c]) : 0.f;
           const float ds = p * (dp - dlt[c]);
 #pragma unroll
@@ -224,7 +236,7 @@ __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
   }
 }
 
-template <typename Tin, int D>
+template <typename Tin, int D, bool WIN>
 __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
   constexpr int DH = D / 2, LD = D + 1;
   extern __shared__ float sm[];
@@ -233,6 +245,7 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
   float* Kc = dOown + kTile * LD;     // [32][D]
   float* Vc = Kc + kChunk * D;        // [32][D]
   int* sec = reinterpret_cast<int*>(Vc + kChunk * D);
+  int* pos_c = sec + kChunk;          // [32], windowed attention only
   const int qt = blockIdx.x, h = blockIdx.y, r = blockIdx.z;
   const int tid = threadIdx.x, t = tid >> 1, half = tid & 1;
   const int T = a.T, NT = T / kTile, G = a.Hq / a.Hkv, g = h / G;
@@ -247,6 +260,7 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
   const float qs = a.scale * kLog2e;
   const float lse2 = a.lse[((size_t)r * a.Hq + h) * T + i] * kLog2e;
   const float dlt = a.delta[((size_t)r * a.Hq + h) * T + i];
+  const int pos_i = WIN ? a.pos[rowT + i] : 0;
   float dq[DH];
 #pragma unroll
   for (int d = 0; d < DH; ++d) dq[d] = 0.f;
@@ -266,6 +280,7 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
       stage_rows<Tin, D>(Kc, D, K, rowT + j0, a.Hkv, g, kChunk, tid, 256);
       stage_rows<Tin, D>(Vc, D, V, rowT + j0, a.Hkv, g, kChunk, tid, 256);
       if (tid < kChunk) sec[tid] = a.se[rowT + j0 + tid];
+      if (WIN && tid < kChunk) pos_c[tid] = a.pos[rowT + j0 + tid];
       __syncthreads();
       for (int c = 0; c < kChunk; ++c) {
         const int j = j0 + c;
@@ -279,7 +294,7 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
         }
         s += __shfl_xor_sync(0xffffffffu, s, 1);
         dp += __shfl_xor_sync(0xffffffffu, dp, 1);
-        const bool vis = !part || (j <= i && sec[c] >= i);
+        const bool vis = !part || (j <= i && sec[c] >= i && (!WIN || in_window(a, pos_i, pos_c[c])));
         const float p = vis ? exp2f(s * qs - lse2) : 0.f;
         const float ds = p * (dp - dlt);
 #pragma unroll
@@ -292,36 +307,40 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
   for (int d = 0; d < DH; ++d) dQ[((rowT + i) * a.Hq + h) * D + half * DH + d] = from_f<Tin>(dq[d] * a.scale);
 }
 
-template <typename Tin, int D>
+template <typename Tin, int D, bool WIN>
 cudaError_t launch_fwd(const AttnArgs& a, cudaStream_t s) {
-  const size_t smem = 2 * kTile * D * sizeof(float) + kTile * sizeof(int);
-  cudaFuncSetAttribute(fwd_simt_kernel<Tin, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  fwd_simt_kernel<Tin, D><<<dim3(a.T / kTile, a.Hq, a.R), 256, smem, s>>>(a);
+  const size_t smem = 2 * kTile * D * sizeof(float) + (WIN ? 2 : 1) * kTile * sizeof(int);
+  cudaFuncSetAttribute(fwd_simt_kernel<Tin, D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  fwd_simt_kernel<Tin, D, WIN><<<dim3(a.T / kTile, a.Hq, a.R), 256, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename Tin, int D>
+template <typename Tin, int D, bool WIN>
 cudaError_t launch_bwd(const AttnArgs& a, cudaStream_t s) {
   delta_kernel<Tin, D><<<1024, 256, 0, s>>>(a);
-  const size_t smem_kv = (2 * kTile * (D + 1) + 2 * kChunk * D + 2 * kChunk) * sizeof(float);
-  cudaFuncSetAttribute(dkdv_simt_kernel<Tin, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_kv);
-  dkdv_simt_kernel<Tin, D><<<dim3(a.T / kTile, a.Hkv, a.R), 256, smem_kv, s>>>(a);
-  const size_t smem_q = (2 * kTile * (D + 1) + 2 * kChunk * D) * sizeof(float) + kChunk * sizeof(int);
-  cudaFuncSetAttribute(dq_simt_kernel<Tin, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_q);
-  dq_simt_kernel<Tin, D><<<dim3(a.T / kTile, a.Hq, a.R), 256, smem_q, s>>>(a);
+  const size_t smem_kv =
+      (2 * kTile * (D + 1) + 2 * kChunk * D + 2 * kChunk) * sizeof(float) + (WIN ? kChunk * sizeof(int) : 0);
+  cudaFuncSetAttribute(dkdv_simt_kernel<Tin, D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_kv);
+  dkdv_simt_kernel<Tin, D, WIN><<<dim3(a.T / kTile, a.Hkv, a.R), 256, smem_kv, s>>>(a);
+  const size_t smem_q =
+      (2 * kTile * (D + 1) + 2 * kChunk * D) * sizeof(float) + (WIN ? 2 : 1) * kChunk * sizeof(int);
+  cudaFuncSetAttribute(dq_simt_kernel<Tin, D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_q);
+  dq_simt_kernel<Tin, D, WIN><<<dim3(a.T / kTile, a.Hq, a.R), 256, smem_q, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t simt_fwd(const AttnArgs& a, bool bf16, cudaStream_t s) {
-  if (bf16) return a.D == 64 ? launch_fwd<__nv_bfloat16, 64>(a, s) : launch_fwd<__nv_bfloat16, 128>(a, s);
-  return a.D == 64 ? launch_fwd<float, 64>(a, s) : launch_fwd<float, 128>(a, s);
+  if (bf16) return a.D == 64 ? launch_fwd<__nv_bfloat16, 64, false>(a, s) : launch_fwd<__nv_bfloat16, 128, false>(a, s);
+  if (a.pos) return a.D == 64 ? launch_fwd<float, 64, true>(a, s) : launch_fwd<float, 128, true>(a, s);
+  return a.D == 64 ? launch_fwd<float, 64, false>(a, s) : launch_fwd<float, 128, false>(a, s);
 }
 
 cudaError_t simt_bwd(const AttnArgs& a, bool bf16, cudaStream_t s) {
-  if (bf16) return a.D == 64 ? launch_bwd<__nv_bfloat16, 64>(a, s) : launch_bwd<__nv_bfloat16, 128>(a, s);
-  return a.D == 64 ? launch_bwd<float, 64>(a, s) : launch_bwd<float, 128>(a, s);
+  if (bf16) return a.D == 64 ? launch_bwd<__nv_bfloat16, 64, false>(a, s) : launch_bwd<__nv_bfloat16, 128, false>(a, s);
+  if (a.pos) return a.D == 64 ? launch_bwd<float, 64, true>(a, s) : launch_bwd<float, 128, true>(a, s);
+  return a.D == 64 ? launch_bwd<float, 64, false>(a, s) : launch_bwd<float, 128, false>(a, s);
 }
 
 }  // namespace stp

@@ -12,7 +12,9 @@
 //               owns the TMEM allocation (512 columns: S_0, S_1, O_0, O_1);
 //   warps 0-3   softmax for head slot 0, warps 4-7 for head slot 1: one thread
 //               per query row (= TMEM lane); the predicate
-//               j <= i && subtree_end[j] >= i is applied on PARTIAL tiles only;
+//               j <= i && subtree_end[j] >= i is applied on PARTIAL tiles only
+//               (WIN: and position[i] - position[j] < window or
+//               position[j] < n_sink);
 //               online softmax in base 2; O is rescaled in TMEM only when the
 //               running max grows by more than 2^8 (exact: numerator and
 //               denominator keep the same reference max).
@@ -96,6 +98,8 @@ struct FwdParams {
   const int32_t* se;
   const int32_t* csr_cnt;
   const int32_t* csr;
+  const int32_t* pos;   // position_ids (WIN only)
+  int window, n_sink;
   __nv_bfloat16* o;
   float* lse;
   uint32_t* err;
@@ -114,6 +118,7 @@ constexpr int kThreads = 384;
 constexpr int kRegsAtLaunch = 168, kRegsMath = 216, kRegsCtl = 72;
 static_assert(kThreads * kRegsAtLaunch >= 256 * kRegsMath + 128 * kRegsCtl, "register split");
 
+template <bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const FwdParams p) {
@@ -305,6 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = tmem + lane_base + hs * 128;
     const uint32_t o_addr = tmem + lane_base + 256 + hs * 128;
     const int32_t* se_row = p.se + (size_t)row0;
+    const int32_t* pos_row = WIN ? p.pos + (size_t)row0 : nullptr;
+    const int pos_i = WIN ? pos_row[i] : 0;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = run && hs < nh;
     for (int e = 0; ok && e < cnt; ++e) {
@@ -326,6 +333,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             bits |= (uint32_t)(j + 1 <= i && v.y >= i) << (4 * c + 1);
             bits |= (uint32_t)(j + 2 <= i && v.z >= i) << (4 * c + 2);
             bits |= (uint32_t)(j + 3 <= i && v.w >= i) << (4 * c + 3);
+          }
+          if (WIN) {
+            // near enough on the query's own path, or among the first tokens
+            const int4* pos4 = reinterpret_cast<const int4*>(pos_row + k0);
+            uint32_t near = 0;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const int4 v = __ldg(pos4 + 8 * w + c);
+              near |= (uint32_t)(pos_i - v.x < p.window || v.x < p.n_sink) << (4 * c + 0);
+              near |= (uint32_t)(pos_i - v.y < p.window || v.y < p.n_sink) << (4 * c + 1);
+              near |= (uint32_t)(pos_i - v.z < p.window || v.z < p.n_sink) << (4 * c + 2);
+              near |= (uint32_t)(pos_i - v.w < p.window || v.w < p.n_sink) << (4 * c + 3);
+            }
+            bits &= near;
           }
           vis[w] = bits;
         }
@@ -511,6 +532,8 @@ struct BwdParams {
   const int32_t* csc_cnt;
   const int32_t* csc;
   const int32_t* csc_pair;
+  const int32_t* pos;   // position_ids (WIN only)
+  int window, n_sink;
   const uint8_t* sbias; // [R][Hq][NT] bias tiles of the scores (-LSE / scale)
   const uint8_t* dbias; // [R][Hq][NT] bias tiles of dP (-Delta)
   uint8_t* ds;          // this launch's slot: [pair][slot_heads] dS^T tiles
@@ -549,6 +572,7 @@ constexpr int kBwdPrefetch = 2;  // iterations ahead for the L2 prefetch of Q, d
 constexpr int kBwdRegsMath = 192, kBwdRegsCtl = 56, kBwdRegsStore = 72;
 static_assert(128 * (2 * kBwdRegsMath + kBwdRegsCtl + kBwdRegsStore) <= kBwdThreads * 128, "register split");
 
+template <bool WIN>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     bwd_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -784,6 +808,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int t = threadIdx.x & 127;     // key row = TMEM lane
     const int jk = kt * 128 + t;         // key index in the row
     const int se_j = p.se[(size_t)row0 + jk];
+    // queries at positions below pos_lim are near enough (all, for a first token)
+    int pos_lim = 0;
+    if (WIN) {
+      const int pos_j = p.pos[(size_t)row0 + jk];
+      pos_lim = pos_j < p.n_sink ? 0x7fffffff : pos_j + p.window;
+    }
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = lane_base + half * 64, dp_col = lane_base + 128 + half * 64;
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
@@ -793,6 +823,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int qt = ent >> 1, part = ent & 1;
       if (j + 1 < n_it) ent = list[(j + 1) / p.G];
       const int q0 = qt * 128 + half * 64;
+      uint32_t near[2] = {~0u, ~0u};
+      if (WIN && part) {
+        const int4* pos4 = reinterpret_cast<const int4*>(p.pos + (size_t)row0 + q0);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint32_t bits = 0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const int4 v = __ldg(pos4 + 8 * w + c);
+            bits |= (uint32_t)(v.x < pos_lim) << (4 * c + 0);
+            bits |= (uint32_t)(v.y < pos_lim) << (4 * c + 1);
+            bits |= (uint32_t)(v.z < pos_lim) << (4 * c + 2);
+            bits |= (uint32_t)(v.w < pos_lim) << (4 * c + 3);
+          }
+          near[w] = bits;
+        }
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(&bars[C_SF], j & 1, abort_flag, p.err))) {
         ok = false;
         break;
@@ -817,6 +864,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int i = q0 + cc;
             if (!(jk <= i && se_j >= i)) y.x = -INFINITY;
             if (!(jk <= i + 1 && se_j >= i + 1)) y.y = -INFINITY;
+            if (WIN) {
+              if (!((near[cc >> 5] >> (cc & 31)) & 1u)) y.x = -INFINITY;
+              if (!((near[cc >> 5] >> ((cc + 1) & 31)) & 1u)) y.y = -INFINITY;
+            }
           }
           u[cc] = __float_as_uint(ex2(y.x));
           u[cc + 1] = __float_as_uint(ex2(y.y));
@@ -1151,18 +1202,26 @@ cudaError_t tc_fwd(const AttnArgs& a, cudaStream_t s) {
   p.se = a.se;
   p.csr_cnt = a.csr_cnt;
   p.csr = a.csr;
+  p.pos = a.pos;
+  p.window = a.window;
+  p.n_sink = a.n_sink;
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.lse = a.lse;
   p.err = a.err;
   static bool attr = false;
   if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(fwd_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(fwd_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmemLimit);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(fwd_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e != cudaSuccess) return e;
     attr = true;
   }
   const unsigned grid = (unsigned)(p.NT * p.R * p.Hkv * p.npairs);
-  fwd_tc_kernel<<<grid, kThreads, kSmemLimit, s>>>(mq, mk, mv, p);
+  if (a.pos)
+    fwd_tc_kernel<true><<<grid, kThreads, kSmemLimit, s>>>(mq, mk, mv, p);
+  else
+    fwd_tc_kernel<false><<<grid, kThreads, kSmemLimit, s>>>(mq, mk, mv, p);
   return cudaGetLastError();
 }
 
@@ -1234,6 +1293,9 @@ cudaError_t tc_bwd(const AttnArgs& a, cudaStream_t s) {
   p.csc_cnt = a.csc_cnt;
   p.csc = a.csc;
   p.csc_pair = a.csc_pair;
+  p.pos = a.pos;
+  p.window = a.window;
+  p.n_sink = a.n_sink;
   p.sbias = static_cast<const uint8_t*>(a.sbias);
   p.dbias = static_cast<const uint8_t*>(a.dbias);
   p.dk = static_cast<__nv_bfloat16*>(a.dk);
@@ -1258,7 +1320,9 @@ cudaError_t tc_bwd(const AttnArgs& a, cudaStream_t s) {
   q.err = a.err;
   static bool attr = false;
   if (!attr) {
-    cudaError_t e = cudaFuncSetAttribute(bwd_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+    cudaError_t e = cudaFuncSetAttribute(bwd_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(bwd_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(dq_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqSmem);
     if (e != cudaSuccess) return e;
@@ -1294,7 +1358,10 @@ cudaError_t tc_bwd(const AttnArgs& a, cudaStream_t s) {
     p.ng = q.ng = g1 - g0;
     p.ds = static_cast<uint8_t*>(a.ds) + (size_t)(gi % slots) * a.ds_slot_bytes;
     q.ds = p.ds;
-    bwd_tc_kernel<<<(unsigned)(p.NT * p.R * p.ng), kBwdThreads, kBwdSmem, sg>>>(mq, mk, mv, mdo, p);
+    if (a.pos)
+      bwd_tc_kernel<true><<<(unsigned)(p.NT * p.R * p.ng), kBwdThreads, kBwdSmem, sg>>>(mq, mk, mv, mdo, p);
+    else
+      bwd_tc_kernel<false><<<(unsigned)(p.NT * p.R * p.ng), kBwdThreads, kBwdSmem, sg>>>(mq, mk, mv, mdo, p);
     dq_tc_kernel<<<(unsigned)(p.NT * p.R * q.ng * q.nquad), kDqThreads, kDqSmem, sg>>>(mk, q);
     if (n_groups > 1) {
       cudaError_t e = cudaEventRecord(bs->join[slot], sg);

@@ -15,6 +15,8 @@
 //   row_base   int32 [R]              first pair index of the row
 //   csc_pair   int32 [R][NT][NT]      pair index of each csc entry
 //   pair_count int32                  non-empty pairs over all rows
+//   pmin, pmax int32 [R][NT]          min / max position over each tile (windowed classes)
+//   qmin       int32 [R][T]           min position from a token's tile start up to it (same)
 // A non-empty (query tile, key tile) pair has the index
 // row_base[r] + csr_off[r][qt] + (position of kt in the csr list of qt):
 // pairs are numbered query-tile major, key tiles ascending, rows in any order.
@@ -45,7 +47,7 @@ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct TileMeta {
   size_t err, cls, csr_cnt, csr, csc_cnt, csc, kmin, kmax, crank, csr_off, row_base, csc_pair,
-      pair_count, total;
+      pair_count, pmin, pmax, qmin, total;
 };
 
 inline TileMeta tile_meta_layout(int64_t R, int64_t NT) {
@@ -64,6 +66,9 @@ inline TileMeta tile_meta_layout(int64_t R, int64_t NT) {
   m.row_base = o; o += align256(size_t(R) * 4);
   m.csc_pair = o; o += align256(size_t(R * NT * NT) * 4);
   m.pair_count = o; o += 256;
+  m.pmin = o;    o += align256(size_t(R * NT) * 4);
+  m.pmax = o;    o += align256(size_t(R * NT) * 4);
+  m.qmin = o;    o += align256(size_t(R * NT) * kTile * 4);
   m.total = o;
   return m;
 }
@@ -137,6 +142,7 @@ enum : uint32_t {
   kErrTimeout = 1u << 1,        // a bounded wait ran out
   kErrBadList = 1u << 2,        // a tile list entry out of range
   kErrTmem = 1u << 3,           // tensor-memory allocation returned an unusable address
+  kErrBadPosition = 1u << 5,    // a position outside [0, 2^30)
   kErrCapacity = 1u << 4        // more non-empty tile pairs than the dS workspace holds
 };
 

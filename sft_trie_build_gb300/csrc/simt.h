@@ -21,6 +21,8 @@ struct AttnArgs {
   void* dk;
   void* dv;
   const int32_t* se;     // subtree_end [R, T]
+  const int32_t* pos;    // position_ids [R, T] (windowed attention), else nullptr
+  int window, n_sink;    // windowed attention
   const int32_t* csr_cnt;
   const int32_t* csr;
   const int32_t* csc_cnt;

@@ -31,6 +31,10 @@ EXPORTED = ["stp_pack", "stp_plan_info", "stp_plan_write", "stp_plan_rows_of", "
             "stp_logprob_workspace_size", "stp_logprob_gather",
             "stp_gdn_plan_bound", "stp_gdn_plan", "stp_gdn_workspace_size", "stp_gdn_fwd",
             "stp_gdn_train_workspace_size", "stp_gdn_fwd_train", "stp_gdn_bwd",
+            "stp_qk_norm_rope_workspace_size", "stp_qk_norm_rope_fwd", "stp_qk_norm_rope_bwd",
+            "stp_count_window_tile_pairs", "stp_classify_window", "stp_attn_window_fwd", "stp_attn_window_bwd",
+            "stp_token_stats_workspace_size", "stp_token_stats_fwd", "stp_token_stats_bwd",
+            "stp_distill_workspace_size", "stp_distill_fwd", "stp_distill_bwd", "stp_distill_step",
             "stp_device_status", "stp_last_error", "stp_version"]
 
 
@@ -60,6 +64,23 @@ class LogprobDesc(ctypes.Structure):
 class GdnDesc(ctypes.Structure):
     _fields_ = [("n_rows", ctypes.c_int32), ("row_len", ctypes.c_int32), ("n_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class QkDesc(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64)]
+
+
+class StatsDesc(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("top_k", ctypes.c_int32)]
+
+
+class DistillDesc(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("n_teacher", ctypes.c_int32)]
 
 
 class AttnDesc(ctypes.Structure):
@@ -147,6 +168,36 @@ def lib():
         L.stp_gdn_fwd_train.restype = st
         L.stp_gdn_bwd.argtypes = [ctypes.POINTER(GdnDesc)] + [_P] * 13
         L.stp_gdn_bwd.restype = st
+        qk, f64 = ctypes.POINTER(QkDesc), ctypes.POINTER(ctypes.c_double)
+        L.stp_qk_norm_rope_workspace_size.argtypes = [qk, _SZ]
+        L.stp_qk_norm_rope_workspace_size.restype = st
+        L.stp_qk_norm_rope_fwd.argtypes = [qk] + [_P] * 4 + [f64] + [_P] * 4
+        L.stp_qk_norm_rope_fwd.restype = st
+        L.stp_qk_norm_rope_bwd.argtypes = [qk] + [_P] * 4 + [f64] + [_P] * 9
+        L.stp_qk_norm_rope_bwd.restype = st
+        i32, attn = ctypes.c_int32, ctypes.POINTER(AttnDesc)
+        L.stp_count_window_tile_pairs.argtypes = [_I32P, _I32P, i32, i32, i32, i32, _I64P]
+        L.stp_count_window_tile_pairs.restype = st
+        L.stp_classify_window.argtypes = [attn, i32, i32] + [_P] * 4
+        L.stp_classify_window.restype = st
+        L.stp_attn_window_fwd.argtypes = [attn, i32, i32] + [_P] * 10
+        L.stp_attn_window_fwd.restype = st
+        L.stp_attn_window_bwd.argtypes = [attn, i32, i32] + [_P] * 14
+        L.stp_attn_window_bwd.restype = st
+        L.stp_token_stats_workspace_size.argtypes = [ctypes.POINTER(StatsDesc), _SZ]
+        L.stp_token_stats_workspace_size.restype = st
+        L.stp_token_stats_fwd.argtypes = [ctypes.POINTER(StatsDesc)] + [_P] * 9
+        L.stp_token_stats_fwd.restype = st
+        L.stp_token_stats_bwd.argtypes = [ctypes.POINTER(StatsDesc)] + [_P] * 8
+        L.stp_token_stats_bwd.restype = st
+        L.stp_distill_workspace_size.argtypes = [ctypes.POINTER(DistillDesc), _SZ]
+        L.stp_distill_workspace_size.restype = st
+        L.stp_distill_fwd.argtypes = [ctypes.POINTER(DistillDesc)] + [_P] * 8
+        L.stp_distill_fwd.restype = st
+        L.stp_distill_bwd.argtypes = [ctypes.POINTER(DistillDesc)] + [_P] * 8
+        L.stp_distill_bwd.restype = st
+        L.stp_distill_step.argtypes = [ctypes.POINTER(DistillDesc)] + [_P] * 10
+        L.stp_distill_step.restype = st
         L.stp_device_status.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_int32)]
         L.stp_device_status.restype = st
         L.stp_last_error.argtypes = []
@@ -498,6 +549,135 @@ def stp_gdn_bwd(desc: GdnDesc, plan: np.ndarray, d_plan, x, conv_w, g, beta, d_o
     _check(lib().stp_gdn_bwd(ctypes.byref(desc), plan.ctypes.data_as(_P), _dptr(d_plan), _dptr(x), _dptr(conv_w),
                              _dptr(g), _dptr(beta), _dptr(d_o), _dptr(dx), _dptr(dconv_w), _dptr(dg), _dptr(dbeta),
                              _dptr(ws), _stream(stream)), "stp_gdn_bwd")
+
+
+def qk_desc(n_tokens, n_q_heads, n_kv_heads, head_dim=128, rotary_dim=None, interleaved=False, dtype=STP_BF16,
+            eps=1e-6, q_stride=None, k_stride=None) -> QkDesc:
+    """rotary_dim None rotates every channel; strides None are those of contiguous tensors."""
+    return QkDesc(n_tokens, n_q_heads, n_kv_heads, head_dim, head_dim if rotary_dim is None else rotary_dim,
+                  int(interleaved), dtype, eps, n_q_heads * head_dim if q_stride is None else q_stride,
+                  n_kv_heads * head_dim if k_stride is None else k_stride)
+
+
+def _freq(inv_freq, desc):
+    if inv_freq is None:
+        return None
+    if inv_freq.dtype != np.float64 or not inv_freq.flags.c_contiguous:
+        inv_freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if inv_freq.size < desc.rotary_dim // 2:
+        raise ValueError("inv_freq must hold rotary_dim / 2 values")
+    return _ptr(inv_freq, ctypes.c_double)
+
+
+def stp_qk_norm_rope_workspace_size(desc: QkDesc) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().stp_qk_norm_rope_workspace_size(ctypes.byref(desc), ctypes.byref(out)),
+           "stp_qk_norm_rope_workspace_size")
+    return out.value
+
+
+def stp_qk_norm_rope_fwd(desc: QkDesc, q, k, w_q, w_k, inv_freq, position_ids, q_out, k_out, stream=None):
+    """inv_freq: host float64 array [rotary_dim / 2] (None when rotary_dim is 0)."""
+    _check(lib().stp_qk_norm_rope_fwd(ctypes.byref(desc), _dptr(q), _dptr(k), _dptr(w_q), _dptr(w_k),
+                                      _freq(inv_freq, desc), _dptr(position_ids), _dptr(q_out), _dptr(k_out),
+                                      _stream(stream)), "stp_qk_norm_rope_fwd")
+
+
+def stp_qk_norm_rope_bwd(desc: QkDesc, q, k, w_q, w_k, inv_freq, position_ids, d_q, d_k, dx_q, dx_k, dw_q, dw_k, ws,
+                         stream=None):
+    _check(lib().stp_qk_norm_rope_bwd(ctypes.byref(desc), _dptr(q), _dptr(k), _dptr(w_q), _dptr(w_k),
+                                      _freq(inv_freq, desc), _dptr(position_ids), _dptr(d_q), _dptr(d_k),
+                                      _dptr(dx_q), _dptr(dx_k), _dptr(dw_q), _dptr(dw_k), _dptr(ws),
+                                      _stream(stream)), "stp_qk_norm_rope_bwd")
+
+
+def stp_count_window_tile_pairs(subtree_end: np.ndarray, position_ids: np.ndarray, window: int, n_sink: int = 0) -> int:
+    """Exact non-empty tile pairs that stp_classify_window lists for host int32 [R, T] arrays."""
+    se = np.ascontiguousarray(subtree_end, dtype=np.int32)
+    pos = np.ascontiguousarray(position_ids, dtype=np.int32)
+    if se.ndim != 2 or se.shape != pos.shape:
+        raise ValueError("subtree_end and position_ids must both be [n_rows, row_len]")
+    out = ctypes.c_int64()
+    _check(lib().stp_count_window_tile_pairs(_ptr(se, ctypes.c_int32), _ptr(pos, ctypes.c_int32), se.shape[0],
+                                             se.shape[1], int(window), int(n_sink), ctypes.byref(out)),
+           "stp_count_window_tile_pairs")
+    return out.value
+
+
+def stp_classify_window(desc: Desc, window: int, n_sink: int, subtree_end, position_ids, tile_meta, stream=None):
+    d = desc.c()
+    _check(lib().stp_classify_window(ctypes.byref(d), window, n_sink, _dptr(subtree_end), _dptr(position_ids),
+                                     _dptr(tile_meta), _stream(stream)), "stp_classify_window")
+
+
+def stp_attn_window_fwd(desc: Desc, window: int, n_sink: int, q, k, v, subtree_end, position_ids, tile_meta, o, lse, ws,
+                        stream=None):
+    d = desc.c()
+    _check(lib().stp_attn_window_fwd(ctypes.byref(d), window, n_sink, _dptr(q), _dptr(k), _dptr(v),
+                                     _dptr(subtree_end), _dptr(position_ids), _dptr(tile_meta), _dptr(o), _dptr(lse),
+                                     _dptr(ws), _stream(stream)), "stp_attn_window_fwd")
+
+
+def stp_attn_window_bwd(desc: Desc, window: int, n_sink: int, q, k, v, o, lse, d_o, subtree_end, position_ids,
+                        tile_meta, dq, dk, dv, ws, stream=None):
+    d = desc.c()
+    _check(lib().stp_attn_window_bwd(ctypes.byref(d), window, n_sink, _dptr(q), _dptr(k), _dptr(v), _dptr(o),
+                                     _dptr(lse), _dptr(d_o), _dptr(subtree_end), _dptr(position_ids),
+                                     _dptr(tile_meta), _dptr(dq), _dptr(dk), _dptr(dv), _dptr(ws), _stream(stream)),
+           "stp_attn_window_bwd")
+
+
+def stats_desc(n_rows, vocab, top_k=0, dtype=STP_BF16, scale=1.0, stride=None) -> StatsDesc:
+    return StatsDesc(n_rows, vocab, vocab if stride is None else stride, dtype, scale, top_k)
+
+
+def stp_token_stats_workspace_size(desc: StatsDesc) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().stp_token_stats_workspace_size(ctypes.byref(desc), ctypes.byref(out)),
+           "stp_token_stats_workspace_size")
+    return out.value
+
+
+def stp_token_stats_fwd(desc: StatsDesc, logits, targets, logprob, entropy, lse, top_id, top_logprob, ws, stream=None):
+    _check(lib().stp_token_stats_fwd(ctypes.byref(desc), _dptr(logits), _dptr(targets), _dptr(logprob),
+                                     _dptr(entropy), _dptr(lse), _dptr(top_id), _dptr(top_logprob), _dptr(ws),
+                                     _stream(stream)), "stp_token_stats_fwd")
+
+
+def stp_token_stats_bwd(desc: StatsDesc, logits, targets, lse, entropy, d_logprob, d_entropy, d_logits, stream=None):
+    _check(lib().stp_token_stats_bwd(ctypes.byref(desc), _dptr(logits), _dptr(targets), _dptr(lse), _dptr(entropy),
+                                     _dptr(d_logprob), _dptr(d_entropy), _dptr(d_logits), _stream(stream)),
+           "stp_token_stats_bwd")
+
+
+def distill_desc(n_rows, vocab, n_teacher, dtype=STP_BF16, scale=1.0, stride=None) -> DistillDesc:
+    return DistillDesc(n_rows, vocab, vocab if stride is None else stride, dtype, scale, n_teacher)
+
+
+def stp_distill_workspace_size(desc: DistillDesc) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().stp_distill_workspace_size(ctypes.byref(desc), ctypes.byref(out)), "stp_distill_workspace_size")
+    return out.value
+
+
+def stp_distill_fwd(desc: DistillDesc, logits, teacher_ids, teacher_logits, loss_mask, loss, lse, ws, stream=None):
+    _check(lib().stp_distill_fwd(ctypes.byref(desc), _dptr(logits), _dptr(teacher_ids), _dptr(teacher_logits),
+                                 _dptr(loss_mask), _dptr(loss), _dptr(lse), _dptr(ws), _stream(stream)),
+           "stp_distill_fwd")
+
+
+def stp_distill_bwd(desc: DistillDesc, logits, teacher_ids, teacher_logits, loss_mask, lse, d_loss, d_logits,
+                    stream=None):
+    _check(lib().stp_distill_bwd(ctypes.byref(desc), _dptr(logits), _dptr(teacher_ids), _dptr(teacher_logits),
+                                 _dptr(loss_mask), _dptr(lse), _dptr(d_loss), _dptr(d_logits), _stream(stream)),
+           "stp_distill_bwd")
+
+
+def stp_distill_step(desc: DistillDesc, logits, teacher_ids, teacher_logits, loss_mask, d_loss, loss, lse, d_logits, ws,
+                     stream=None):
+    _check(lib().stp_distill_step(ctypes.byref(desc), _dptr(logits), _dptr(teacher_ids), _dptr(teacher_logits),
+                                  _dptr(loss_mask), _dptr(d_loss), _dptr(loss), _dptr(lse), _dptr(d_logits),
+                                  _dptr(ws), _stream(stream)), "stp_distill_step")
 
 
 def stp_device_status(ws, stream=None) -> int:
