@@ -116,17 +116,17 @@ __device__ __forceinline__ Part part_of(const T* row, int V, int rank, int C) {
 
 // ------------------------------------------------------------------ sums
 
-// m: largest raw logit; s, t: sums of 2^d and 2^d d, d = logit * sl2 - ref(m).
+// m: largest raw logit; s, t: sums of 2^d and 2^d d, d = (logit - m) sl2.  The
+// difference comes first: it is near exact where 2^d counts, and a row of the
+// type's lowest value, as masks have it, overflows nowhere.
 struct Acc {
   float m, s, t;
 };
 
-__device__ __forceinline__ float ref_of(float m, float sl2) { return m == -INFINITY ? 0.f : m * sl2; }
-
 // Brings the sums of `a` to the reference of a larger maximum.
 __device__ __forceinline__ void rebase(Acc& a, float m, float sl2) {
   if (a.m != -INFINITY) {
-    const float dl = a.m * sl2 - m * sl2, f = ex2(dl);
+    const float dl = (a.m - m) * sl2, f = ex2(dl);
     a.t = f * fmaf(dl, a.s, a.t);
     a.s *= f;
   }
@@ -136,10 +136,10 @@ __device__ __forceinline__ void rebase(Acc& a, float m, float sl2) {
 template <int N, bool ENT>
 __device__ __forceinline__ void add(Acc& a, const float* z, float most, float sl2) {
   if (most > a.m) rebase(a, most, sl2);
-  const float ref = ref_of(a.m, sl2);
+  const float m = a.m == -INFINITY ? 0.f : a.m;
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    const float d = fmaf(z[e], sl2, -ref), p = ex2(d);
+    const float d = (z[e] - m) * sl2, p = ex2(d);
     a.s += p;
     if (ENT) a.t = fmaf(p, fmaxf(d, kLowest), a.t);
   }
@@ -183,10 +183,8 @@ __device__ __forceinline__ Acc row_sum(Acc a, Acc* red, Acc* mine, int C, float 
   return a;
 }
 
-// ln sum exp(z) - scale m, in the sums' own reference (its rounding cancels).
-__device__ __forceinline__ float log_sum(const Acc& a, float sl2) {
-  return kLn2T * (log2f(a.s) - fmaf(a.m, sl2, -ref_of(a.m, sl2)));
-}
+// ln sum exp(z) - scale m.
+__device__ __forceinline__ float log_sum(const Acc& a) { return kLn2T * log2f(a.s); }
 
 // One pass over the block's part of a row.  With TOP, the thread's largest
 // value and the round in which it came are kept in (best, round).
@@ -399,7 +397,7 @@ __global__ void __launch_bounds__(kRowThreads) stats_fwd_kernel(const StatsParam
       if (rank == 0) rank_top(sh, C * p.K, p.K);
     }
   }
-  const float ls = log_sum(a, p.sl2);
+  const float ls = log_sum(a);
   const bool none = a.m == -INFINITY && a.s == 0.f;   // nothing but -inf
   if (rank == 0) {
     if (t == 0) {
@@ -574,7 +572,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillParam
     int round;
     Acc s = pass<T, false, false>(row, part, p.sl2, best, round);
     s = row_sum(s, red, &mine, C, p.sl2);
-    const float ls = log_sum(s, p.sl2);
+    const float ls = log_sum(s);
     lse = fmaf(s.m, p.scale, ls);
     if (rank == 0) {
       const float lnq = kLn2T * (a - top - log2f(sum));
