@@ -74,13 +74,16 @@ struct Window {
   int32_t window, n_sink;
 };
 
-static stp_status set_window(const char* name, const Window* w, AttnArgs& a) {
+static stp_status set_window(const char* name, const Window* w, const stp_attn_desc* d, const void* tile_meta,
+                             AttnArgs& a) {
   if (!w) return STP_OK;
   if (!w->pos) return fail(STP_EINVAL, "%s: NULL device pointer", name);
   if (misaligned(w->pos, 16)) return fail(STP_EINVAL, "%s: position_ids must be 16-byte aligned", name);
   a.pos = w->pos;
-  a.window = clip_window(w->window);
-  a.n_sink = w->n_sink;
+  const TileMeta m = tile_meta_layout(d->n_rows, d->row_len / kTile);
+  const char* base = static_cast<const char*>(tile_meta);
+  a.lim = reinterpret_cast<const int32_t*>(base + m.lim);
+  a.word = reinterpret_cast<const uint32_t*>(base + m.word);
   return STP_OK;
 }
 
@@ -97,7 +100,7 @@ static stp_status attn_fwd(const char* name, const Window* win, const stp_attn_d
       misaligned(lse, 16) || misaligned(d_tile_meta, 256) || misaligned(d_ws, 256))
     return fail(STP_EINVAL, "%s: tensors must be 16-byte and workspaces 256-byte aligned", name);
   AttnArgs a{};
-  st = set_window(name, win, a);
+  st = set_window(name, win, desc, d_tile_meta, a);
   if (st) return st;
   if (desc->n_rows == 0) return STP_OK;
   fill_common(desc, d_subtree_end, d_tile_meta, a);
@@ -135,7 +138,7 @@ static stp_status attn_bwd(const char* name, const Window* win, const stp_attn_d
       misaligned(dv, 16) || misaligned(d_tile_meta, 256) || misaligned(d_ws, 256))
     return fail(STP_EINVAL, "%s: tensors must be 16-byte and workspaces 256-byte aligned", name);
   AttnArgs a{};
-  st = set_window(name, win, a);
+  st = set_window(name, win, desc, d_tile_meta, a);
   if (st) return st;
   if (desc->n_rows == 0) return STP_OK;
   fill_common(desc, d_subtree_end, d_tile_meta, a);

@@ -34,11 +34,6 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
   return __float2bfloat16_rn(x);
 }
 
-// Whether a key at pos_j of a query's path is near enough, or among the first tokens.
-__device__ __forceinline__ bool in_window(const AttnArgs& a, int pos_i, int pos_j) {
-  return pos_i - pos_j < a.window || pos_j < a.n_sink;
-}
-
 // Loads rows [row0, row0+n) of one head of a [R, T, H, D] tensor into
 // shared memory with row stride `ld` floats.
 template <typename Tin, int D>
@@ -57,7 +52,7 @@ __global__ void __launch_bounds__(256) fwd_simt_kernel(AttnArgs a) {
   float* Ks = sm;                  // [128][D]
   float* Vs = Ks + kTile * D;      // [128][D]
   int* se_s = reinterpret_cast<int*>(Vs + kTile * D);
-  int* pos_s = se_s + kTile;       // windowed attention only
+  int* lim_s = se_s + kTile;       // windowed attention only
   const int qt = blockIdx.x, h = blockIdx.y, r = blockIdx.z;
   const int tid = threadIdx.x, t = tid >> 1, half = tid & 1;
   const int T = a.T, NT = T / kTile, G = a.Hq / a.Hkv, g = h / G;
@@ -87,7 +82,7 @@ __global__ void __launch_bounds__(256) fwd_simt_kernel(AttnArgs a) {
     stage_rows<Tin, D>(Ks, D, K, rowT + k0, a.Hkv, g, kTile, tid, 256);
     stage_rows<Tin, D>(Vs, D, V, rowT + k0, a.Hkv, g, kTile, tid, 256);
     if (tid < kTile) se_s[tid] = a.se[rowT + k0 + tid];
-    if (WIN && tid < kTile) pos_s[tid] = a.pos[rowT + k0 + tid];
+    if (WIN && tid < kTile) lim_s[tid] = a.lim[rowT + k0 + tid];
     __syncthreads();
     for (int c0 = 0; c0 < kTile; c0 += 32) {
       float s[32];
@@ -101,7 +96,7 @@ __global__ void __launch_bounds__(256) fwd_simt_kernel(AttnArgs a) {
         acc += __shfl_xor_sync(0xffffffffu, acc, 1);
         const int j = k0 + c0 + c;
         const bool vis = !part || (j <= i && se_s[c0 + c] >= i &&
-                                   (!WIN || in_window(a, pos_i, pos_s[c0 + c])));
+                                   (!WIN || pos_i < lim_s[c0 + c]));
         s[c] = vis ? acc : -INFINITY;
         mx = fmaxf(mx, s[c]);
       }
@@ -175,7 +170,7 @@ __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
   stage_rows<Tin, D>(Kown, LD, K, rowT + kt * kTile, a.Hkv, g, kTile, tid, 256);
   stage_rows<Tin, D>(Vown, LD, V, rowT + kt * kTile, a.Hkv, g, kTile, tid, 256);
   const int sej = a.se[rowT + j];
-  const int pos_j = WIN ? a.pos[rowT + j] : 0;
+  const int lim_j = WIN ? a.lim[rowT + j] : 0;
   const float qs = a.scale * kLog2e;
   float dk[DH], dv[DH];
 #pragma unroll
@@ -215,7 +210,7 @@ __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
           }
           s += __shfl_xor_sync(0xffffffffu, s, 1);
           dp += __shfl_xor_sync(0xffffffffu, dp, 1);
-          const bool vis = !part || (j <= i && sej >= i && (!WIN || in_window(a, pos_c[c], pos_j)));
+          const bool vis = !part || (j <= i && sej >= i && (!WIN || pos_c[c] < lim_j));
           const float p = vis ? exp2f(s * qs - lse2[c]) : 0.f;
           const float ds = p * (dp - dlt[c]);
 #pragma unroll
@@ -245,7 +240,7 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
   float* Kc = dOown + kTile * LD;     // [32][D]
   float* Vc = Kc + kChunk * D;        // [32][D]
   int* sec = reinterpret_cast<int*>(Vc + kChunk * D);
-  int* pos_c = sec + kChunk;          // [32], windowed attention only
+  int* lim_c = sec + kChunk;          // [32], windowed attention only
   const int qt = blockIdx.x, h = blockIdx.y, r = blockIdx.z;
   const int tid = threadIdx.x, t = tid >> 1, half = tid & 1;
   const int T = a.T, NT = T / kTile, G = a.Hq / a.Hkv, g = h / G;
@@ -280,7 +275,7 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
       stage_rows<Tin, D>(Kc, D, K, rowT + j0, a.Hkv, g, kChunk, tid, 256);
       stage_rows<Tin, D>(Vc, D, V, rowT + j0, a.Hkv, g, kChunk, tid, 256);
       if (tid < kChunk) sec[tid] = a.se[rowT + j0 + tid];
-      if (WIN && tid < kChunk) pos_c[tid] = a.pos[rowT + j0 + tid];
+      if (WIN && tid < kChunk) lim_c[tid] = a.lim[rowT + j0 + tid];
       __syncthreads();
       for (int c = 0; c < kChunk; ++c) {
         const int j = j0 + c;
@@ -294,7 +289,7 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
         }
         s += __shfl_xor_sync(0xffffffffu, s, 1);
         dp += __shfl_xor_sync(0xffffffffu, dp, 1);
-        const bool vis = !part || (j <= i && sec[c] >= i && (!WIN || in_window(a, pos_i, pos_c[c])));
+        const bool vis = !part || (j <= i && sec[c] >= i && (!WIN || pos_i < lim_c[c]));
         const float p = vis ? exp2f(s * qs - lse2) : 0.f;
         const float ds = p * (dp - dlt);
 #pragma unroll

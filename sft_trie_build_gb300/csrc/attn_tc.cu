@@ -13,8 +13,8 @@
 //   warps 0-3   softmax for head slot 0, warps 4-7 for head slot 1: one thread
 //               per query row (= TMEM lane); the predicate
 //               j <= i && subtree_end[j] >= i is applied on PARTIAL tiles only
-//               (WIN: and position[i] - position[j] < window or
-//               position[j] < n_sink);
+//               (WIN: and position[i] < lim[j], on the 32 x 32 blocks of the
+//               tile that are PARTIAL; EMPTY blocks are skipped, P = 0);
 //               online softmax in base 2; O is rescaled in TMEM only when the
 //               running max grows by more than 2^8 (exact: numerator and
 //               denominator keep the same reference max).
@@ -98,12 +98,29 @@ struct FwdParams {
   const int32_t* se;
   const int32_t* csr_cnt;
   const int32_t* csr;
-  const int32_t* pos;   // position_ids (WIN only)
-  int window, n_sink;
+  const int32_t* pos;     // WIN only: position_ids, lim and the block classes
+  const int32_t* lim;     // of stp_classify_window
+  const uint32_t* word;
   __nv_bfloat16* o;
   float* lse;
   uint32_t* err;
 };
+
+// Visibility of 32 keys to query i of a windowed row, but for j <= i: bit c is
+// set iff subtree_end >= i and pos_i < lim of key c (both signs negative).
+__device__ __forceinline__ uint32_t window_bits(const int4* se4, const int4* lim4, int i, int pos_i) {
+  uint32_t bits = 0;
+  auto put = [&](int se, int lim) { bits = __funnelshift_l((uint32_t)((i - 1 - se) & (pos_i - lim)), bits, 1); };
+#pragma unroll
+  for (int c = 7; c >= 0; --c) {
+    const int4 s = __ldg(se4 + c), l = __ldg(lim4 + c);
+    put(s.w, l.w);
+    put(s.z, l.z);
+    put(s.y, l.y);
+    put(s.x, l.x);
+  }
+  return bits;
+}
 
 enum {
   B_Q = 0, B_KF = 1, B_VF = 3, B_KE = 5, B_VE = 7, B_SF = 9, B_PF = 11, B_OD = 13, B_DRAIN = 15,
@@ -310,8 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = tmem + lane_base + hs * 128;
     const uint32_t o_addr = tmem + lane_base + 256 + hs * 128;
     const int32_t* se_row = p.se + (size_t)row0;
-    const int32_t* pos_row = WIN ? p.pos + (size_t)row0 : nullptr;
-    const int pos_i = WIN ? pos_row[i] : 0;
+    const int pos_i = WIN ? p.pos[(size_t)row0 + i] : 0;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = run && hs < nh;
     for (int e = 0; ok && e < cnt; ++e) {
@@ -320,7 +336,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // computed before the scores are ready so the loads stay off the
       // critical path
       uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-      if (part) {
+      uint32_t cls = 0xaa;   // WIN: two bits per 32 keys, the classes of the warp's blocks
+      if (WIN) {
+        if (part) {
+          cls = (p.word[((size_t)r * p.NT + qt) * p.NT + kt] >> (8 * (warp & 3))) & 0xff;
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            if (((cls >> (2 * w)) & 3) == kPartial) {
+              vis[w] = window_bits(reinterpret_cast<const int4*>(se_row + k0) + 8 * w,
+                                   reinterpret_cast<const int4*>(p.lim + (size_t)row0 + k0) + 8 * w, i, pos_i);
+              if (kt == qt && w == (warp & 3)) vis[w] &= (2u << lane) - 1;   // j <= i
+            }
+        }
+      } else if (part) {
         const int4* se4 = reinterpret_cast<const int4*>(se_row + k0);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -334,20 +362,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             bits |= (uint32_t)(j + 2 <= i && v.z >= i) << (4 * c + 2);
             bits |= (uint32_t)(j + 3 <= i && v.w >= i) << (4 * c + 3);
           }
-          if (WIN) {
-            // near enough on the query's own path, or among the first tokens
-            const int4* pos4 = reinterpret_cast<const int4*>(pos_row + k0);
-            uint32_t near = 0;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const int4 v = __ldg(pos4 + 8 * w + c);
-              near |= (uint32_t)(pos_i - v.x < p.window || v.x < p.n_sink) << (4 * c + 0);
-              near |= (uint32_t)(pos_i - v.y < p.window || v.y < p.n_sink) << (4 * c + 1);
-              near |= (uint32_t)(pos_i - v.z < p.window || v.z < p.n_sink) << (4 * c + 2);
-              near |= (uint32_t)(pos_i - v.w < p.window || v.w < p.n_sink) << (4 * c + 3);
-            }
-            bits &= near;
-          }
           vis[w] = bits;
         }
       }
@@ -358,12 +372,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_after_sync();
       // the whole score row: 128 TMEM columns of this thread's lane
       uint32_t u[128];
-      tmem_ld32(s_addr + 0, u);
-      tmem_ld32(s_addr + 32, u + 32);
-      tmem_ld32(s_addr + 64, u + 64);
-      tmem_ld32(s_addr + 96, u + 96);
+      auto there = [&](int w) { return !WIN || ((cls >> (2 * w)) & 3) != kEmpty; };   // the same for the whole warp
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        if (there(w)) tmem_ld32(s_addr + 32 * w, u + 32 * w);
       tmem_ld_wait();
-      if (part) {
+      if (WIN) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (((cls >> (2 * w)) & 3) == kPartial) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((vis[w] >> c) & 1u)) u[32 * w + c] = 0xff800000u;
+          }
+      } else if (part) {
 #pragma unroll
         for (int c = 0; c < 128; ++c)
           if (!((vis[c >> 5] >> (c & 31)) & 1u)) u[c] = 0xff800000u;
@@ -372,10 +394,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // chains keep the dependent-latency path short
       float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < 128; c += 8)
+      for (int w = 0; w < 4; ++w)
+        if (there(w)) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          mx4[t] = max3(mx4[t], __uint_as_float(u[c + 2 * t]), __uint_as_float(u[c + 2 * t + 1]));
+          for (int c = 32 * w; c < 32 * w + 32; c += 8)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              mx4[t] = max3(mx4[t], __uint_as_float(u[c + 2 * t]), __uint_as_float(u[c + 2 * t + 1]));
+        }
       const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
       const float m_new = fmaxf(m_run, mx * p.scale_log2);
       const float m_use = (m_new > m_run + kRescaleThreshold) ? m_new : m_run;
@@ -394,16 +420,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int hf = 0; hf < 2; ++hf) {
         uint32_t pk[32];
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const int c0 = 64 * hf + 2 * c;
-          const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(u[c0]), __uint_as_float(u[c0 + 1])), sl2, nm2);
-          const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(u[c0 + 2]), __uint_as_float(u[c0 + 3])), sl2, nm2);
-          const float2 p0 = make_float2(ex2(y0.x), ex2(y0.y));
-          const float2 p1 = make_float2(ex2(y1.x), ex2(y1.y));
-          acc2 = __fadd2_rn(acc2, p0);
-          acc2b = __fadd2_rn(acc2b, p1);
-          pk[c] = pack_bf16x2(p0.x, p0.y);
-          pk[c + 1] = pack_bf16x2(p1.x, p1.y);
+        for (int w = 0; w < 2; ++w) {
+          if (!there(2 * hf + w)) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) pk[16 * w + c] = 0;
+            continue;
+          }
+#pragma unroll
+          for (int c = 16 * w; c < 16 * w + 16; c += 2) {
+            const int c0 = 64 * hf + 2 * c;
+            const float2 y0 = __ffma2_rn(make_float2(__uint_as_float(u[c0]), __uint_as_float(u[c0 + 1])), sl2, nm2);
+            const float2 y1 = __ffma2_rn(make_float2(__uint_as_float(u[c0 + 2]), __uint_as_float(u[c0 + 3])), sl2, nm2);
+            const float2 p0 = make_float2(ex2(y0.x), ex2(y0.y));
+            const float2 p1 = make_float2(ex2(y1.x), ex2(y1.y));
+            acc2 = __fadd2_rn(acc2, p0);
+            acc2b = __fadd2_rn(acc2b, p1);
+            pk[c] = pack_bf16x2(p0.x, p0.y);
+            pk[c + 1] = pack_bf16x2(p1.x, p1.y);
+          }
         }
         tmem_st32(s_addr + 32 * hf, pk);
       }
@@ -532,8 +566,9 @@ struct BwdParams {
   const int32_t* csc_cnt;
   const int32_t* csc;
   const int32_t* csc_pair;
-  const int32_t* pos;   // position_ids (WIN only)
-  int window, n_sink;
+  const int32_t* pos;   // WIN only, as in FwdParams
+  const int32_t* lim;
+  const uint32_t* word;
   const uint8_t* sbias; // [R][Hq][NT] bias tiles of the scores (-LSE / scale)
   const uint8_t* dbias; // [R][Hq][NT] bias tiles of dP (-Delta)
   uint8_t* ds;          // this launch's slot: [pair][slot_heads] dS^T tiles
@@ -808,12 +843,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int t = threadIdx.x & 127;     // key row = TMEM lane
     const int jk = kt * 128 + t;         // key index in the row
     const int se_j = p.se[(size_t)row0 + jk];
-    // queries at positions below pos_lim are near enough (all, for a first token)
-    int pos_lim = 0;
-    if (WIN) {
-      const int pos_j = p.pos[(size_t)row0 + jk];
-      pos_lim = pos_j < p.n_sink ? 0x7fffffff : pos_j + p.window;
-    }
+    const int lim_j = WIN ? p.lim[(size_t)row0 + jk] : 0;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = lane_base + half * 64, dp_col = lane_base + 128 + half * 64;
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
@@ -823,21 +853,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const int qt = ent >> 1, part = ent & 1;
       if (j + 1 < n_it) ent = list[(j + 1) / p.G];
       const int q0 = qt * 128 + half * 64;
-      uint32_t near[2] = {~0u, ~0u};
+      // WIN: which of the 64 queries see the key, by the classes of the warp's
+      // two blocks: jk <= i <= subtree_end, pos_i < lim_j in a partial one
+      uint32_t vis[2] = {~0u, ~0u};
       if (WIN && part) {
-        const int4* pos4 = reinterpret_cast<const int4*>(p.pos + (size_t)row0 + q0);
+        const uint32_t word = p.word[((size_t)r * p.NT + qt) * p.NT + kt] >> (2 * (warp & 3));
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          uint32_t bits = 0;
+          const int cls = (word >> (8 * (2 * half + w))) & 3;
+          if (cls == kEmpty) vis[w] = 0;
+          if (cls == kPartial) {
+            const int4* pos4 = reinterpret_cast<const int4*>(p.pos + (size_t)row0 + q0 + 32 * w);
+            uint32_t bits = 0;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int4 v = __ldg(pos4 + 8 * w + c);
-            bits |= (uint32_t)(v.x < pos_lim) << (4 * c + 0);
-            bits |= (uint32_t)(v.y < pos_lim) << (4 * c + 1);
-            bits |= (uint32_t)(v.z < pos_lim) << (4 * c + 2);
-            bits |= (uint32_t)(v.w < pos_lim) << (4 * c + 3);
+            for (int c = 7; c >= 0; --c) {
+              const int4 v = __ldg(pos4 + c);
+              bits = __funnelshift_l((uint32_t)(v.w - lim_j), bits, 1);
+              bits = __funnelshift_l((uint32_t)(v.z - lim_j), bits, 1);
+              bits = __funnelshift_l((uint32_t)(v.y - lim_j), bits, 1);
+              bits = __funnelshift_l((uint32_t)(v.x - lim_j), bits, 1);
+            }
+            const int lo = jk - (q0 + 32 * w), hi = se_j - (q0 + 32 * w);
+            bits &= hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1;
+            vis[w] = lo <= 0 ? bits : lo > 31 ? 0u : bits & (~0u << lo);
           }
-          near[w] = bits;
         }
       }
       if (!__all_sync(0xffffffffu, mbar_wait(&bars[C_SF], j & 1, abort_flag, p.err))) {
@@ -860,14 +899,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int u2 = 0; u2 < 2; ++u2) {
           const int cc = col + 2 * u2;
           float2 y = __fmul2_rn(make_float2(__uint_as_float(u[cc]), __uint_as_float(u[cc + 1])), sl2);
-          if (part) {
+          if (WIN && part) {
+            if (!((vis[cc >> 5] >> (cc & 31)) & 1u)) y.x = -INFINITY;
+            if (!((vis[cc >> 5] >> ((cc + 1) & 31)) & 1u)) y.y = -INFINITY;
+          } else if (part) {
             const int i = q0 + cc;
             if (!(jk <= i && se_j >= i)) y.x = -INFINITY;
             if (!(jk <= i + 1 && se_j >= i + 1)) y.y = -INFINITY;
-            if (WIN) {
-              if (!((near[cc >> 5] >> (cc & 31)) & 1u)) y.x = -INFINITY;
-              if (!((near[cc >> 5] >> ((cc + 1) & 31)) & 1u)) y.y = -INFINITY;
-            }
           }
           u[cc] = __float_as_uint(ex2(y.x));
           u[cc + 1] = __float_as_uint(ex2(y.y));
@@ -1203,8 +1241,8 @@ cudaError_t tc_fwd(const AttnArgs& a, cudaStream_t s) {
   p.csr_cnt = a.csr_cnt;
   p.csr = a.csr;
   p.pos = a.pos;
-  p.window = a.window;
-  p.n_sink = a.n_sink;
+  p.lim = a.lim;
+  p.word = a.word;
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.lse = a.lse;
   p.err = a.err;
@@ -1294,8 +1332,8 @@ cudaError_t tc_bwd(const AttnArgs& a, cudaStream_t s) {
   p.csc = a.csc;
   p.csc_pair = a.csc_pair;
   p.pos = a.pos;
-  p.window = a.window;
-  p.n_sink = a.n_sink;
+  p.lim = a.lim;
+  p.word = a.word;
   p.sbias = static_cast<const uint8_t*>(a.sbias);
   p.dbias = static_cast<const uint8_t*>(a.dbias);
   p.dk = static_cast<__nv_bfloat16*>(a.dk);

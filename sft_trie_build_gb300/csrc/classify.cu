@@ -22,8 +22,6 @@
 #include <cuda_runtime.h>
 
 #include <mutex>
-#include <new>
-#include <vector>
 
 #include "internal.h"
 #include "layout.h"
@@ -65,59 +63,6 @@ __device__ __forceinline__ int8_t tile_class(int qt, int kt, int kmn, int kmx) {
   return kPartial;
 }
 
-// Windowed classes (window W, first S positions visible): a tile of the tree
-// stays FULL when no query of the tile is W or more past the key tile's
-// smallest position, or all its keys are among the first S; it becomes EMPTY
-// when every query that the key tile reaches is W or more past its largest
-// position and none of its keys is among the first S.  The queries reached are
-// those up to kmax, so a query tile in which another branch or tree begins
-// still drops the key tiles that are far from its first branch.
-struct TileWindow {
-  int W, S;
-  const int32_t* pmin;   // [R][NT]
-  const int32_t* pmax;   // [R][NT]
-  const int32_t* qmin;   // [R][T]
-};
-
-__host__ __device__ inline int8_t window_class(int8_t c, int qt, int kt, int kmx, const int32_t* pmin,
-                                               const int32_t* pmax, const int32_t* qmin, int W, int S) {
-  if (c == kEmpty || kt == qt) return c;
-  const int q0 = qt * kTile, last = kmx < q0 + kTile - 1 ? kmx : q0 + kTile - 1;
-  if (qmin[last] - pmax[kt] >= W && pmin[kt] >= S) return kEmpty;
-  if (c == kFull && !(pmax[qt] - pmin[kt] < W || pmax[kt] < S)) return kPartial;
-  return c;
-}
-
-constexpr int kMaxPosition = 1 << 30;   // positions and windows: sums of two fit an int
-
-__global__ void __launch_bounds__(128) tile_positions_kernel(const int32_t* __restrict__ pos, int T, int NT,
-                                                             int32_t* __restrict__ pmin, int32_t* __restrict__ pmax,
-                                                             int32_t* __restrict__ qmin, uint32_t* __restrict__ err) {
-  const int tile = blockIdx.x, r = blockIdx.y, t = threadIdx.x, lane = t & 31, w = t >> 5;
-  const size_t at = (size_t)r * T + tile * kTile + t;
-  const int v = pos[at];
-  if (v < 0 || v >= kMaxPosition) atomicOr(err, kErrBadPosition);
-  int mn = v, mx = v;   // prefix minimum, maximum
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, mn, o);
-    if (lane >= o) mn = min(mn, y);
-    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  }
-  __shared__ int smn[4], smx[4];
-  if (lane == 31) {
-    smn[w] = mn;
-    smx[w] = mx;
-  }
-  __syncthreads();
-  for (int k = 0; k < w; ++k) mn = min(mn, smn[k]);
-  qmin[at] = mn;
-  if (t == 127) {
-    pmin[(size_t)r * NT + tile] = mn;
-    pmax[(size_t)r * NT + tile] = max(max(smx[0], smx[1]), max(smx[2], smx[3]));
-  }
-}
-
 // Exclusive prefix count of `flag` over the 128 threads of the block;
 // returns the thread's position and writes the block total to *total.
 __device__ __forceinline__ int block_scan128(bool flag, int* s_warp, int* total) {
@@ -133,8 +78,7 @@ __device__ __forceinline__ int block_scan128(bool flag, int* s_warp, int* total)
   return pos;
 }
 
-template <bool WIN>
-__global__ void __launch_bounds__(128) tile_lists_kernel(TileWindow win, int NT, const int32_t* __restrict__ kmin,
+__global__ void __launch_bounds__(128) tile_lists_kernel(int NT, const int32_t* __restrict__ kmin,
                                                          const int32_t* __restrict__ kmax,
                                                          int8_t* __restrict__ cls,
                                                          int32_t* __restrict__ csr_cnt,
@@ -157,9 +101,6 @@ __global__ void __launch_bounds__(128) tile_lists_kernel(TileWindow win, int NT,
       int8_t c = kEmpty;
       if (kt < NT) {
         c = tile_class(b, kt, mn[kt], mx[kt]);
-        if (WIN)
-          c = window_class(c, b, kt, mx[kt], win.pmin + (size_t)r * NT, win.pmax + (size_t)r * NT,
-                           win.qmin + (size_t)r * NT * kTile, win.W, win.S);
         crow[kt] = c;
       }
       int tot;
@@ -180,9 +121,6 @@ __global__ void __launch_bounds__(128) tile_lists_kernel(TileWindow win, int NT,
     for (int q0 = 0; q0 < NT; q0 += 128) {
       const int qt = q0 + t;
       int8_t c = qt < NT ? tile_class(qt, b, kmn, kmx) : kEmpty;
-      if (WIN && qt < NT)
-        c = window_class(c, qt, b, kmx, win.pmin + (size_t)r * NT, win.pmax + (size_t)r * NT,
-                         win.qmin + (size_t)r * NT * kTile, win.W, win.S);
       int tot;
       const int pos = block_scan128(c != kEmpty, s_warp, &tot);
       if (c != kEmpty) list[base + pos] = (qt << 1) | (c == kPartial ? 1 : 0);
@@ -253,16 +191,14 @@ __global__ void __launch_bounds__(128) tile_pair_index_kernel(int NT, const int3
 
 // The launches after min / max: lists, ranks, pair numbering.
 cudaError_t launch_lists(const stp_attn_desc* d, const int32_t* kmin, const int32_t* kmax,
-                         char* base, const TileMeta& m, uint32_t* err, cudaStream_t s,
-                         const TileWindow* win = nullptr) {
+                         char* base, const TileMeta& m, uint32_t* err, cudaStream_t s) {
   const int NT = d->row_len / kTile;
   dim3 grid(NT, d->n_rows);
   int32_t* pair_count = reinterpret_cast<int32_t*>(base + m.pair_count);
   cudaError_t e = cudaMemsetAsync(pair_count, 0, 4, s);
   if (e != cudaSuccess) return e;
-  auto lists = win ? tile_lists_kernel<true> : tile_lists_kernel<false>;
-  lists<<<grid, 128, 0, s>>>(
-      win ? *win : TileWindow{}, NT, kmin, kmax, reinterpret_cast<int8_t*>(base + m.cls),
+  tile_lists_kernel<<<grid, 128, 0, s>>>(
+      NT, kmin, kmax, reinterpret_cast<int8_t*>(base + m.cls),
       reinterpret_cast<int32_t*>(base + m.csr_cnt), reinterpret_cast<int32_t*>(base + m.csr),
       reinterpret_cast<int32_t*>(base + m.csc_cnt), reinterpret_cast<int32_t*>(base + m.csc),
       reinterpret_cast<int32_t*>(base + m.crank));
@@ -343,85 +279,6 @@ extern "C" stp_status stp_classify(const stp_attn_desc* desc, const int32_t* d_s
   cudaError_t e = launch_lists(desc, reinterpret_cast<const int32_t*>(base + m.kmin),
                                reinterpret_cast<const int32_t*>(base + m.kmax), base, m, err, s);
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_classify: %s", cudaGetErrorString(e));
-  return STP_OK;
-}
-
-extern "C" stp_status stp_count_window_tile_pairs(const int32_t* subtree_end, const int32_t* position_ids,
-                                                  int32_t n_rows, int32_t row_len, int32_t window, int32_t n_sink,
-                                                  int64_t* n_pairs) {
-  clear_error();
-  if (!n_pairs || ((!subtree_end || !position_ids) && n_rows > 0))
-    return fail(STP_EINVAL, "stp_count_window_tile_pairs: NULL pointer");
-  if (n_rows < 0 || row_len <= 0 || row_len % kTile)
-    return fail(STP_EINVAL, "stp_count_window_tile_pairs: need n_rows >= 0 and row_len a positive multiple of 128");
-  stp_status st = check_window(window, n_sink);
-  if (st) return st;
-  const int W = clip_window(window), NT = row_len / kTile;
-  int64_t total = 0;
-  try {
-    std::vector<int32_t> kmx(NT), pmin(NT), pmax(NT), qmin(row_len);
-    for (int64_t r = 0; r < n_rows; ++r) {
-      const int32_t *se = subtree_end + r * row_len, *pos = position_ids + r * row_len;
-      for (int kt = 0; kt < NT; ++kt) {
-        int32_t mx = -1, lo = kMaxPosition, hi = -1;
-        for (int32_t j = kt * kTile; j < (kt + 1) * kTile; ++j) {
-          if (se[j] < j || se[j] >= row_len)
-            return fail(STP_EINVAL, "stp_count_window_tile_pairs: subtree_end[%lld][%d] = %d outside [j, row_len)",
-                        (long long)r, j, se[j]);
-          if (pos[j] < 0 || pos[j] >= kMaxPosition)
-            return fail(STP_EINVAL, "stp_count_window_tile_pairs: position_ids[%lld][%d] = %d outside [0, 2^30)",
-                        (long long)r, j, pos[j]);
-          mx = se[j] > mx ? se[j] : mx;
-          lo = pos[j] < lo ? pos[j] : lo;
-          hi = pos[j] > hi ? pos[j] : hi;
-          qmin[j] = lo;
-        }
-        kmx[kt] = mx;
-        pmin[kt] = lo;
-        pmax[kt] = hi;
-      }
-      // whether a tile is listed does not depend on the key tile's smallest subtree_end
-      for (int kt = 0; kt < NT; ++kt)
-        for (int qt = kt; qt <= kmx[kt] / kTile; ++qt)
-          total += window_class(kPartial, qt, kt, kmx[kt], pmin.data(), pmax.data(), qmin.data(), W, n_sink) != kEmpty;
-    }
-  } catch (const std::bad_alloc&) {
-    return fail(STP_ENOMEM, "stp_count_window_tile_pairs: out of memory");
-  }
-  *n_pairs = total;
-  return STP_OK;
-}
-
-extern "C" stp_status stp_classify_window(const stp_attn_desc* desc, int32_t window, int32_t n_sink,
-                                          const int32_t* d_subtree_end, const int32_t* d_position_ids,
-                                          void* d_tile_meta, void* stream) {
-  clear_error();
-  stp_status st = check_desc(desc);
-  if (!st) st = check_window(window, n_sink);
-  if (st) return st;
-  if (!d_subtree_end || !d_position_ids || !d_tile_meta)
-    return fail(STP_EINVAL, "stp_classify_window: NULL device pointer");
-  if ((reinterpret_cast<uintptr_t>(d_tile_meta) & 255) ||
-      (reinterpret_cast<uintptr_t>(d_subtree_end) | reinterpret_cast<uintptr_t>(d_position_ids)) & 15)
-    return fail(STP_EINVAL, "stp_classify_window: tile_meta must be 256-byte, the row arrays 16-byte aligned");
-  if (desc->n_rows == 0) return STP_OK;
-  const int NT = desc->row_len / kTile;
-  const TileMeta m = tile_meta_layout(desc->n_rows, NT);
-  char* base = static_cast<char*>(d_tile_meta);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint32_t* err = reinterpret_cast<uint32_t*>(base + m.err);
-  int32_t *kmin = reinterpret_cast<int32_t*>(base + m.kmin), *kmax = reinterpret_cast<int32_t*>(base + m.kmax);
-  int32_t *pmin = reinterpret_cast<int32_t*>(base + m.pmin), *pmax = reinterpret_cast<int32_t*>(base + m.pmax);
-  int32_t* qmin = reinterpret_cast<int32_t*>(base + m.qmin);
-  cudaError_t e = cudaMemsetAsync(err, 0, 4, s);
-  const dim3 grid(NT, desc->n_rows);
-  if (e == cudaSuccess) {
-    tile_minmax_kernel<<<grid, 128, 0, s>>>(d_subtree_end, desc->row_len, NT, kmin, kmax, err);
-    tile_positions_kernel<<<grid, 128, 0, s>>>(d_position_ids, desc->row_len, NT, pmin, pmax, qmin, err);
-    const TileWindow win = {clip_window(window), n_sink, pmin, pmax, qmin};
-    e = launch_lists(desc, kmin, kmax, base, m, err, s, &win);
-  }
-  if (e != cudaSuccess) return fail(STP_ECUDA, "stp_classify_window: %s", cudaGetErrorString(e));
   return STP_OK;
 }
 

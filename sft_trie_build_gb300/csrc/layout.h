@@ -15,8 +15,14 @@
 //   row_base   int32 [R]              first pair index of the row
 //   csc_pair   int32 [R][NT][NT]      pair index of each csc entry
 //   pair_count int32                  non-empty pairs over all rows
-//   pmin, pmax int32 [R][NT]          min / max position over each tile (windowed classes)
-//   qmin       int32 [R][T]           min position from a token's tile start up to it (same)
+// and, written by stp_classify_window alone, with blocks of 32 tokens:
+//   smin, smax int32 [R][T/32]        min / max subtree_end over each block
+//   pmin, pmax int32 [R][T/32]        min / max position over each block
+//   qmin       int32 [R][T]           min position from the token's block start up to it
+//   lim        int32 [R][T]           a key's window: queries at positions below lim are near
+//   word       uint32 [R][NT][NT]     classes of the 4 x 4 blocks of a tile (q-tile major):
+//                                     bits 2 (4 qb + kb) and up
+//   ticket     int32 [R]              blocks of the row that have written their lists
 // A non-empty (query tile, key tile) pair has the index
 // row_base[r] + csr_off[r][qt] + (position of kt in the csr list of qt):
 // pairs are numbered query-tile major, key tiles ascending, rows in any order.
@@ -47,7 +53,7 @@ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct TileMeta {
   size_t err, cls, csr_cnt, csr, csc_cnt, csc, kmin, kmax, crank, csr_off, row_base, csc_pair,
-      pair_count, pmin, pmax, qmin, total;
+      pair_count, smin, smax, pmin, pmax, qmin, lim, word, ticket, total;
 };
 
 inline TileMeta tile_meta_layout(int64_t R, int64_t NT) {
@@ -66,9 +72,14 @@ inline TileMeta tile_meta_layout(int64_t R, int64_t NT) {
   m.row_base = o; o += align256(size_t(R) * 4);
   m.csc_pair = o; o += align256(size_t(R * NT * NT) * 4);
   m.pair_count = o; o += 256;
-  m.pmin = o;    o += align256(size_t(R * NT) * 4);
-  m.pmax = o;    o += align256(size_t(R * NT) * 4);
+  m.smin = o;    o += align256(size_t(R * NT) * 16);
+  m.smax = o;    o += align256(size_t(R * NT) * 16);
+  m.pmin = o;    o += align256(size_t(R * NT) * 16);
+  m.pmax = o;    o += align256(size_t(R * NT) * 16);
   m.qmin = o;    o += align256(size_t(R * NT) * kTile * 4);
+  m.lim = o;     o += align256(size_t(R * NT) * kTile * 4);
+  m.word = o;    o += align256(size_t(R * NT * NT) * 4);
+  m.ticket = o;  o += align256(size_t(R) * 4);
   m.total = o;
   return m;
 }

@@ -22,7 +22,8 @@ struct AttnArgs {
   void* dv;
   const int32_t* se;     // subtree_end [R, T]
   const int32_t* pos;    // position_ids [R, T] (windowed attention), else nullptr
-  int window, n_sink;    // windowed attention
+  const int32_t* lim;    // [R, T]: key j is near the queries at positions below lim[j]
+  const uint32_t* word;  // [R, NT, NT]: classes of a tile's 32 x 32 blocks
   const int32_t* csr_cnt;
   const int32_t* csr;
   const int32_t* csc_cnt;
