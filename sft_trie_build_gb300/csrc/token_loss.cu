@@ -9,12 +9,15 @@
 // The gradients are a second pass, p = exp(z - lse), written as it goes.
 //
 // Bound by memory: forward one read of the logits, backward one read and one
-// write.  C blocks share a row (C = 1 when there are rows enough for every
-// SM): they are a thread-block cluster, and their sums meet in the shared
-// memory of its first block, so one launch does a row whatever C is.  A block
-// streams 16-byte pieces, four per thread in flight; a row may start at any
-// address of its type: up to one piece's elements at either end of the row
-// are taken one by one.
+// write, the step of both one read and one write too, its second pass out of
+// L2.  C blocks share a row (C = 1 when there are rows enough for every SM):
+// they are a thread-block cluster, and their sums meet in the shared memory of
+// its first block, so one launch does a row whatever C is.  A thread streams
+// 16-byte pieces through its own ring of slots in shared memory (asynchronous
+// copies, no barrier), which keeps 192 KB on the way per SM while other blocks
+// of the SM are at their row's end.  A row may start at any address of its
+// type: up to one piece's elements at either end of the row are taken one by
+// one.
 //
 // Top tokens without a second pass over the row: a thread remembers the
 // maximum of its own strip of pieces.  The K-th largest over groups of four
@@ -25,6 +28,9 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <mutex>
+#include <type_traits>
 
 #include "internal.h"
 #include "layout.h"
@@ -40,22 +46,30 @@ using tc::ex2;
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxTop = 32;
-constexpr int kMaxTeacher = kRowThreads;
+constexpr int kMaxTeacher = 256;
 constexpr int kMaxSplit = 8;        // blocks of a row: the portable cluster size
+constexpr int kFlight = 4;          // pieces of a round per thread
+// Rounds on their way per thread, and blocks per SM: forward and backward 3
+// and 4 (48 KB in flight per block), the step of both passes 4 and 3, where
+// fewer rows in work keep more of them in L2.  Of 2..12 rounds and 1..8 blocks,
+// these measured best on rows of 151936 bf16 logits: 8192 rows' statistics 405 us
+// (462 without the ring), 4096 rows' step 445 us (516).
+constexpr int kPassRounds = 3, kPassBlocks = 4;
+constexpr int kStepRounds = 4, kStepBlocks = 3;
+constexpr int ring_bytes(int rounds) { return rounds * kFlight * kRowThreads * 16; }
 constexpr int kGroups = 64;         // groups of threads whose maxima bound the top tokens
-constexpr int kFlight = 4;          // pieces in flight per thread
 constexpr float kLog2eT = 1.4426950408889634f;
 constexpr float kLn2T = 0.6931471805599453f;
 // 2^d is 0 below this, so that d = -inf adds 0 to sum 2^d d, not NaN
 constexpr float kLowest = -256.f;
 
+// 16 bytes of a row: E elements.
 template <typename T>
-struct Piece;  // 16 bytes of a row
+struct Piece;
 template <>
 struct Piece<__nv_bfloat16> {
   static constexpr int E = 8;
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* f) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+  static __device__ __forceinline__ void get(uint4 v, float* f) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -63,23 +77,26 @@ struct Piece<__nv_bfloat16> {
       f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = tc::pack_bf16x2(f[2 * i], f[2 * i + 1]);
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  // the one rounding to bf16, of a finished gradient
+  static __device__ __forceinline__ uint4 put(const float* f) {
+    return make_uint4(tc::pack_bf16x2(f[0], f[1]), tc::pack_bf16x2(f[2], f[3]), tc::pack_bf16x2(f[4], f[5]),
+                      tc::pack_bf16x2(f[6], f[7]));
   }
+  static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
 };
 template <>
 struct Piece<float> {
   static constexpr int E = 4;
-  static __device__ __forceinline__ void load(const float* p, float* f) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+  static __device__ __forceinline__ void get(uint4 v, float* f) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
   }
-  static __device__ __forceinline__ void store(float* p, const float* f) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  static __device__ __forceinline__ uint4 put(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
+  static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
 };
 
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -133,15 +150,58 @@ __device__ __forceinline__ void rebase(Acc& a, float m, float sl2) {
   a.m = m;
 }
 
+// Adds N logits, `most` and `least` their extremes; pairs go through the packed
+// two-lane operations, which halve the instructions of a pass that issues
+// more than it may.
 template <int N, bool ENT>
-__device__ __forceinline__ void add(Acc& a, const float* z, float most, float sl2) {
+__device__ __forceinline__ void add(Acc& a, const float* z, float most, float least, float sl2) {
   if (most > a.m) rebase(a, most, sl2);
   const float m = a.m == -INFINITY ? 0.f : a.m;
+  if (N % 2 || (ENT && !((least - m) * sl2 > -1e30f))) {
+    // one by one: d = -inf has to add 0 to t
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const float d = (z[e] - m) * sl2, p = ex2(d);
-    a.s += p;
-    if (ENT) a.t = fmaf(p, fmaxf(d, kLowest), a.t);
+    for (int e = 0; e < N; ++e) {
+      const float d = (z[e] - m) * sl2, p = ex2(d);
+      a.s += p;
+      if (ENT) a.t = fmaf(p, fmaxf(d, kLowest), a.t);
+    }
+  } else {
+    const float2 m2 = make_float2(-m, -m), l2 = make_float2(sl2, sl2);
+    float2 s = make_float2(0.f, 0.f), t = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e + 1 < N; e += 2) {
+      const float2 d = __fmul2_rn(__fadd2_rn(make_float2(z[e], z[e + 1]), m2), l2);
+      const float2 p = make_float2(ex2(d.x), ex2(d.y));
+      s = __fadd2_rn(s, p);
+      if (ENT) t = __ffma2_rn(p, d, t);
+    }
+    a.s += s.x + s.y;
+    if (ENT) a.t += t.x + t.y;
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void extremes(const float* z, float& most, float& least) {
+  most = least = z[0];
+  if (N % 2) {
+#pragma unroll
+    for (int e = 1; e + 1 < N; e += 2) {
+      most = tc::max3(most, z[e], z[e + 1]);
+      asm("min.f32 %0, %0, %1, %2;" : "+f"(least) : "f"(z[e]), "f"(z[e + 1]));
+    }
+  } else {
+    // two chains, then their ends
+    float m1 = z[1], l1 = z[1];
+#pragma unroll
+    for (int e = 2; e + 3 < N; e += 4) {
+      most = tc::max3(most, z[e], z[e + 1]);
+      m1 = tc::max3(m1, z[e + 2], z[e + 3]);
+      asm("min.f32 %0, %0, %1, %2;" : "+f"(least) : "f"(z[e]), "f"(z[e + 1]));
+      asm("min.f32 %0, %0, %1, %2;" : "+f"(l1) : "f"(z[e + 2]), "f"(z[e + 3]));
+    }
+    most = tc::max3(most, m1, z[N - 2]);
+    most = fmaxf(most, z[N - 1]);
+    least = fminf(fminf(least, l1), fminf(z[N - 2], z[N - 1]));
   }
 }
 
@@ -170,55 +230,75 @@ __device__ __forceinline__ Acc block_sum(Acc a, Acc* red, float sl2) {
   return a;
 }
 
-// The row's sums in all threads of its blocks.
-__device__ __forceinline__ Acc row_sum(Acc a, Acc* red, Acc* mine, int C, float sl2) {
-  a = block_sum(a, red, sl2);
-  if (C > 1) {
-    cg::cluster_group cl = cg::this_cluster();
-    if (threadIdx.x == 0) *mine = a;
-    cl.sync();
-    a = *cl.map_shared_rank(mine, 0);
-    for (int r = 1; r < C; ++r) a = merge(a, *cl.map_shared_rank(mine, r), sl2);
-  }
+// The row's sums, from those that each of its blocks has left in its `mine`.
+__device__ __forceinline__ Acc cluster_sum(Acc* mine, int C, float sl2) {
+  cg::cluster_group cl = cg::this_cluster();
+  Acc a = *cl.map_shared_rank(mine, 0);
+  for (int r = 1; r < C; ++r) a = merge(a, *cl.map_shared_rank(mine, r), sl2);
   return a;
 }
 
 // ln sum exp(z) - scale m.
 __device__ __forceinline__ float log_sum(const Acc& a) { return kLn2T * log2f(a.s); }
 
-// One pass over the block's part of a row.  With TOP, the thread's largest
-// value and the round in which it came are kept in (best, round).
-template <typename T, bool ENT, bool TOP>
-__device__ __forceinline__ Acc pass(const T* row, const Part& p, float sl2, float& best, int& round) {
+// A thread's pieces on their way: R rounds of kFlight pieces each, in
+// shared memory that no other thread touches, so the copies need no barrier.
+template <int R>
+struct Ring {
+  uint4* slot;        // of this thread; pieces kRowThreads apart
+  const uint4* body;
+  int b1;
+
+  __device__ __forceinline__ void fetch(int round, int b) const {
+    const uint4* s = slot + round * kFlight * kRowThreads;
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f)
+      if (b + f * kRowThreads < b1)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(s + f * kRowThreads)),
+                     "l"(body + b + f * kRowThreads)
+                     : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void start(int b) const {
+#pragma unroll
+    for (int r = 0; r < R; ++r) fetch(r, b + r * kFlight * kRowThreads);
+  }
+  // the oldest round has landed
+  static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(R - 1) : "memory"); }
+  __device__ __forceinline__ uint4 piece(int round, int f) const { return slot[(round * kFlight + f) * kRowThreads]; }
+};
+
+template <int R, typename T>
+__device__ __forceinline__ Ring<R> ring_of(uint4* buffer, const T* row, const Part& p) {
+  return {buffer + threadIdx.x, reinterpret_cast<const uint4*>(row + p.head), p.b1};
+}
+
+// One pass over the block's part of a row, whose first rounds are on their
+// way.  With TOP, the thread's largest value and the round in which it came
+// are kept in (best, round).
+template <typename T, bool ENT, bool TOP, int R>
+__device__ __forceinline__ Acc pass(const T* row, const Part& p, const Ring<R>& ring, float sl2, float& best, int& round) {
   constexpr int E = Piece<T>::E;
   Acc a = {-INFINITY, 0.f, 0.f};
-  const T* body = row + p.head;
-  int k = 0;
-  for (int b = p.b0 + (int)threadIdx.x; b < p.b1; b += kFlight * kRowThreads, ++k) {
+  const float extra = p.extra >= 0 ? to_f(row[p.extra]) : 0.f;
+  int s = 0;
+  for (int b = p.b0 + (int)threadIdx.x, k = 0; b < p.b1; b += kFlight * kRowThreads, ++k) {
+    ring.wait();
     float z[kFlight * E];
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      const int at = b + f * kRowThreads;
-      if (at < p.b1) {
-        Piece<T>::load(body + (int64_t)at * E, z + f * E);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) z[f * E + e] = -INFINITY;
-      }
-    }
-    float most = z[0];
-#pragma unroll
-    for (int e = 1; e < kFlight * E; ++e) most = fmaxf(most, z[e]);
+    for (int f = 0; f < kFlight; ++f)
+      Piece<T>::get(b + f * kRowThreads < p.b1 ? ring.piece(s, f) : Piece<T>::lowest(), z + f * E);
+    float most, least;
+    extremes<kFlight * E>(z, most, least);
     if (TOP && most > best) {
       best = most;
       round = k;
     }
-    add<kFlight * E, ENT>(a, z, most, sl2);
+    add<kFlight * E, ENT>(a, z, most, least, sl2);
+    ring.fetch(s, b + R * kFlight * kRowThreads);
+    s = s + 1 == R ? 0 : s + 1;
   }
-  if (p.extra >= 0) {
-    const float z = to_f(row[p.extra]);
-    add<1, ENT>(a, &z, z, sl2);
-  }
+  if (p.extra >= 0) add<1, ENT>(a, &extra, extra, extra, sl2);
   return a;
 }
 
@@ -234,13 +314,15 @@ __device__ __forceinline__ float value_of(uint64_t key) {
   return __uint_as_float(u ^ ((int32_t)u < 0 ? 0x80000000u : 0xffffffffu));
 }
 
+constexpr int kCand = 512;
+
 struct TopShared {
-  uint64_t group[kGroups];
-  uint64_t bound;
-  int n_strips;
-  uint16_t strip[kRowThreads];
-  uint64_t cand[kRowThreads];
+  __align__(16) uint64_t group[kGroups];
+  __align__(16) uint64_t cand[kCand];   // first the threads' maxima, then the candidates
   uint64_t top[kMaxTop];
+  uint64_t bound;
+  int n_strips, n_cand;
+  uint16_t strip[kRowThreads];
 };
 
 // Entry of `key` into the warp's list (one key per lane < K, `least` its
@@ -260,45 +342,65 @@ __device__ __forceinline__ void enter(uint64_t& held, uint64_t& least, bool want
   }
 }
 
-// sh.top[0..K) = the K largest of sh.cand[0..n), descending; n <= kRowThreads.
-__device__ __forceinline__ void rank_top(TopShared& sh, int n, int K) {
-  __syncthreads();
-  if ((int)threadIdx.x < n) {
-    const uint64_t mine = sh.cand[threadIdx.x];
-    int rank = 0;
-    for (int j = 0; j < n; ++j) {
-      const uint64_t o = sh.cand[j];
-      rank += o > mine || (o == mine && j < (int)threadIdx.x);
-    }
-    if (rank < K) sh.top[rank] = mine;
+// How many of keys[0..n) come before `mine`, which is keys[at] (equal keys,
+// which stand for no token, in order).
+__device__ __forceinline__ int rank_of(const uint64_t* keys, int n, uint64_t mine, int at) {
+  int rank = 0;
+#pragma unroll 8
+  for (int j = 0; j < n / 2; ++j) {
+    const ulonglong2 o = reinterpret_cast<const ulonglong2*>(keys)[j];
+    rank += o.x > mine || (o.x == mine && 2 * j < at);
+    rank += o.y > mine || (o.y == mine && 2 * j + 1 < at);
   }
-  __syncthreads();
+  if (n & 1) rank += keys[n - 1] > mine;
+  return rank;
 }
 
-// The block's K largest tokens into sh.top.
+// f(key of the token, or 0) on every piece of the chosen strips, one thread a
+// piece; all lanes of a warp call f together.
+template <typename T, typename F>
+__device__ __forceinline__ void each_candidate(const T* row, const Part& p, const TopShared& sh, float floor_v, F f) {
+  constexpr int E = Piece<T>::E;
+  const uint4* body = reinterpret_cast<const uint4*>(row + p.head);
+  const int len = (p.b1 - p.b0 + kRowThreads - 1) / kRowThreads;   // pieces of a strip, the last one perhaps outside
+  const int total = sh.n_strips * len;
+  for (int i0 = (int)threadIdx.x & ~31; i0 < total; i0 += kRowThreads) {
+    const int i = i0 + ((int)threadIdx.x & 31);
+    const int at = i < total ? p.b0 + sh.strip[i / len] + (i % len) * kRowThreads : p.b1;
+    float z[E];
+    Piece<T>::get(at < p.b1 ? body[at] : Piece<T>::lowest(), z);
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < E; ++e) any = any || (z[e] >= floor_v && z[e] > -INFINITY);
+    if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      f(z[e] >= floor_v && z[e] > -INFINITY ? key_of(z[e], (uint32_t)(p.head + at * E + e)) : 0);
+  }
+  if (__any_sync(0xffffffffu, p.extra >= 0)) {
+    const float z = p.extra >= 0 ? to_f(row[p.extra]) : -INFINITY;
+    f(z >= floor_v && z > -INFINITY ? key_of(z, (uint32_t)p.extra) : 0);
+  }
+}
+
+// The block's K largest tokens into sh.top, descending, 0 where none is left.
 template <typename T>
 __device__ void block_top(const T* row, const Part& p, float best, int round, int K, TopShared& sh) {
-  constexpr int E = Piece<T>::E;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const uint64_t mine = best > -INFINITY ? key_of(best, (uint32_t)round) : 0;
-  uint64_t g = mine;
-#pragma unroll
-  for (int o = 1; o < kRowThreads / kGroups; o <<= 1) {
-    const uint64_t x = __shfl_xor_sync(0xffffffffu, g, o);
-    g = x > g ? x : g;
-  }
-  if (t % (kRowThreads / kGroups) == 0) sh.group[t / (kRowThreads / kGroups)] = g;
-  if (t == 0) sh.n_strips = 0;
+  // groups of threads kGroups apart, so that a short row still fills them
+  sh.cand[t] = mine;
+  if (t == 0) sh.n_strips = sh.n_cand = 0;
+  if (t < K) sh.top[t] = 0;
   __syncthreads();
   if (t < kGroups) {
-    const uint64_t x = sh.group[t];
-    int rank = 0;
-    for (int j = 0; j < kGroups; ++j) {
-      const uint64_t o = sh.group[j];
-      rank += o > x || (o == x && j < t);
-    }
-    if (rank == K - 1) sh.bound = x;
+    uint64_t g = mine;
+#pragma unroll
+    for (int o = kGroups; o < kRowThreads; o += kGroups) g = sh.cand[t + o] > g ? sh.cand[t + o] : g;
+    sh.group[t] = g;
   }
+  __syncthreads();
+  if (t < kGroups && rank_of(sh.group, kGroups, sh.group[t], t) == K - 1) sh.bound = sh.group[t];
   __syncthreads();
   const uint64_t bound = sh.bound;
   const bool in = mine != 0 && mine >= bound;
@@ -308,30 +410,57 @@ __device__ void block_top(const T* row, const Part& p, float best, int round, in
   at = __shfl_sync(0xffffffffu, at, 0);
   if (in) sh.strip[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)t;
   __syncthreads();
-  uint64_t held = lane < K ? 0 : ~0ull, least = 0;
   const float floor_v = bound ? value_of(bound) : -INFINITY;
-  const int n = sh.n_strips;
-  for (int i = warp; i < n; i += kRowWarps) {
-    const int first = p.b0 + sh.strip[i];
-    for (int b = first; b < p.b1; b += 32 * kRowThreads) {
-      const int at_b = b + lane * kRowThreads;
-      const bool live = at_b < p.b1;
-      float z[E];
-      if (live) Piece<T>::load(row + p.head + (int64_t)at_b * E, z);
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint64_t key = live ? key_of(z[e], (uint32_t)(p.head + at_b * E + e)) : 0;
-        enter(held, least, live && z[e] > -INFINITY && z[e] >= floor_v && key > least, key);
-      }
+  each_candidate(row, p, sh, floor_v, [&](uint64_t key) {
+    if (key) {
+      const int i = atomicAdd(&sh.n_cand, 1);
+      if (i < kCand) sh.cand[i] = key;
     }
+  });
+  __syncthreads();
+  int n = sh.n_cand;
+  if (n > kCand) {
+    // many values that tie or lie in few strips: a list of K per warp instead
+    __syncthreads();
+    uint64_t held = lane < K ? 0 : ~0ull, least = 0;
+    each_candidate(row, p, sh, floor_v, [&](uint64_t key) { enter(held, least, key > least, key); });
+    if (lane < K) sh.cand[warp * K + lane] = held;
+    n = kRowWarps * K;
+    __syncthreads();
   }
-  if (__any_sync(0xffffffffu, p.extra >= 0)) {
-    const float z = p.extra >= 0 ? to_f(row[p.extra]) : -INFINITY;
-    const uint64_t key = key_of(z, (uint32_t)p.extra);
-    enter(held, least, z > -INFINITY && key > least, key);
+  for (int i = t; i < n; i += kRowThreads) {
+    const uint64_t x = sh.cand[i];
+    const int rank = rank_of(sh.cand, n, x, i);
+    if (rank < K) sh.top[rank] = x;
   }
-  if (lane < K) sh.cand[warp * K + lane] = held;
-  rank_top(sh, kRowWarps * K, K);
+  __syncthreads();
+}
+
+// The K largest of the C blocks' lists, each descending, into sh.top of the
+// first block: a key's place is its place in its own list and, by halving,
+// those in the others.
+__device__ __forceinline__ void merge_top(TopShared& sh, int C, int K) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int t = threadIdx.x, mine = t / K, at = t % K;
+  uint64_t key = 0;
+  if (t < C * K) {
+    key = cl.map_shared_rank(&sh, mine)->top[at];
+    sh.cand[t] = key;
+  }
+  __syncthreads();
+  if (key) {
+    // how many keys of each list are larger, by halving: the lists in step, so
+    // that the reads of a step are on their way together
+    int lo[kMaxSplit] = {}, rank = 0;
+    for (int step = kMaxTop; step > 0; step >>= 1)
+#pragma unroll
+      for (int l = 0; l < kMaxSplit; ++l)
+        if (l < C && lo[l] + step <= K && sh.cand[l * K + lo[l] + step - 1] > key) lo[l] += step;
+#pragma unroll
+    for (int l = 0; l < kMaxSplit; ++l) rank += l == mine ? at : lo[l];
+    if (rank < K) sh.top[rank] = key;
+  }
+  __syncthreads();
 }
 
 // ------------------------------------------------------------------ stats
@@ -348,6 +477,7 @@ struct StatsParams {
   int32_t* top_id;
   float* top_lp;
   uint32_t* err;
+  bool check;   // a block past the rows checks all targets
   // backward
   const float* lse_in;
   const float* ent_in;
@@ -356,12 +486,28 @@ struct StatsParams {
   void* dz;
 };
 
+// The device error word, by a block of its own past the rows' (so that no row
+// waits for it, and no launch clears the word): whether any of `n` whole
+// numbers that are read lies at or above V.
+template <typename F>
+__device__ __forceinline__ void check_below(int64_t n, int V, uint32_t* err, F value) {
+  bool bad = false;
+  for (int64_t i = threadIdx.x; i < n; i += kRowThreads) bad = bad || value(i) >= V;
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *err = bad ? kErrBadList : 0;
+}
+
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kRowThreads) stats_fwd_kernel(const StatsParams p) {
+__global__ void __launch_bounds__(kRowThreads, kPassBlocks) stats_fwd_kernel(const StatsParams p) {
   __shared__ Acc red[kRowWarps];
   __shared__ Acc mine;
   __shared__ TopShared sh;
+  extern __shared__ uint4 buffer[];
   const int C = p.C, n = (int)(blockIdx.x / C), rank = (int)(blockIdx.x % C), t = threadIdx.x;
+  if (n == p.N) {
+    if (rank == 0) check_below(p.N, p.V, p.err, [&](int64_t i) { return p.target[i]; });
+    return;
+  }
   const int target = p.target[n];
   if (target < 0) {   // the same for every block of the row
     if (rank == 0) {
@@ -375,31 +521,30 @@ __global__ void __launch_bounds__(kRowThreads) stats_fwd_kernel(const StatsParam
   }
   const T* row = static_cast<const T*>(p.z) + (int64_t)n * p.stride;
   const Part part = part_of(row, p.V, rank, C);
+  const auto ring = ring_of<kPassRounds>(buffer, row, part);
+  ring.start(part.b0 + t);
   float zt = 0.f;
   if (rank == 0 && t == 0) {
-    if (target < p.V) {
-      zt = to_f(row[target]);
-    } else {
-      zt = NAN;
-      atomicOr(p.err, kErrBadList);
-    }
+    zt = target < p.V ? to_f(row[target]) : NAN;
+    if (!p.check && target >= p.V) atomicOr(p.err, kErrBadList);
   }
   float best = -INFINITY;
   int round = 0;
-  Acc a = pass<T, true, TOP>(row, part, p.sl2, best, round);
-  a = row_sum(a, red, &mine, C, p.sl2);
-  if (TOP) {
-    block_top(row, part, best, round, p.K, sh);
-    if (C > 1) {
-      cg::cluster_group cl = cg::this_cluster();
-      cl.sync();
-      if (rank == 0 && t < C * p.K) sh.cand[t] = cl.map_shared_rank(&sh, t / p.K)->top[t % p.K];
-      if (rank == 0) rank_top(sh, C * p.K, p.K);
+  Acc a = block_sum(pass<T, true, TOP>(row, part, ring, p.sl2, best, round), red, p.sl2);
+  if (TOP) block_top(row, part, best, round, p.K, sh);
+  if (C > 1) {
+    cg::cluster_group cl = cg::this_cluster();
+    if (t == 0) mine = a;
+    cl.sync();
+    if (rank == 0) {
+      a = cluster_sum(&mine, C, p.sl2);
+      if (TOP) merge_top(sh, C, p.K);
     }
+    cl.barrier_arrive();   // the first block has read the others' shared memory
   }
-  const float ls = log_sum(a);
-  const bool none = a.m == -INFINITY && a.s == 0.f;   // nothing but -inf
   if (rank == 0) {
+    const float ls = log_sum(a);
+    const bool none = a.m == -INFINITY && a.s == 0.f;   // nothing but -inf
     if (t == 0) {
       p.lse[n] = none ? -INFINITY : fmaf(a.m, p.scale, ls);
       p.logprob[n] = none && !isnan(zt) ? -INFINITY : fmaf(zt - a.m, p.scale, -ls);
@@ -411,29 +556,32 @@ __global__ void __launch_bounds__(kRowThreads) stats_fwd_kernel(const StatsParam
       p.top_lp[(int64_t)n * p.K + t] = key ? fmaf(value_of(key) - a.m, p.scale, -ls) : -INFINITY;
     }
   }
-  if (C > 1) cg::this_cluster().sync();   // the first block reads the others' shared memory
+  if (C > 1) cg::this_cluster().barrier_wait();
 }
 
-// Writes f(z, id) over the block's part of a row; `same`: the output row has
-// the input row's alignment (else element by element).
-template <typename T, typename F>
-__device__ __forceinline__ void map_row(const T* row, T* out, const Part& p, F f) {
+// Writes f(z, id) over the block's part of a row, whose first rounds are on
+// their way: 16-byte pieces where the output row has the input row's
+// alignment, else element by element.
+template <typename T, int R, typename F>
+__device__ __forceinline__ void map_row(const T* row, T* out, const Part& p, const Ring<R>& ring, F f) {
   constexpr int E = Piece<T>::E;
-  const bool same = ((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
-  if (same) {
+  if (((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
+    uint4* to = reinterpret_cast<uint4*>(out + p.head);
+    int s = 0;
     for (int b = p.b0 + (int)threadIdx.x; b < p.b1; b += kFlight * kRowThreads) {
-      float z[kFlight][E];
-#pragma unroll
-      for (int k = 0; k < kFlight; ++k)
-        if (b + k * kRowThreads < p.b1) Piece<T>::load(row + p.head + (int64_t)(b + k * kRowThreads) * E, z[k]);
+      ring.wait();
 #pragma unroll
       for (int k = 0; k < kFlight; ++k) {
         const int at = b + k * kRowThreads;
         if (at < p.b1) {
-          f(z[k], p.head + at * E, std::integral_constant<int, E>());
-          Piece<T>::store(out + p.head + (int64_t)at * E, z[k]);
+          float z[E];
+          Piece<T>::get(ring.piece(s, k), z);
+          f(z, p.head + at * E, std::integral_constant<int, E>());
+          __stcs(to + at, Piece<T>::put(z));
         }
       }
+      ring.fetch(s, b + R * kFlight * kRowThreads);
+      s = s + 1 == R ? 0 : s + 1;
     }
     if (p.extra >= 0) {
       float z = to_f(row[p.extra]);
@@ -441,6 +589,7 @@ __device__ __forceinline__ void map_row(const T* row, T* out, const Part& p, F f
       put(out + p.extra, z);
     }
   } else {
+    asm volatile("cp.async.wait_all;" ::: "memory");   // the ring is not used
     for (int i = p.lo + (int)threadIdx.x; i < p.hi; i += kRowThreads) {
       float z = to_f(row[i]);
       f(&z, i, std::integral_constant<int, 1>());
@@ -452,15 +601,14 @@ __device__ __forceinline__ void map_row(const T* row, T* out, const Part& p, F f
 // Zeros over the block's part of a row.
 template <typename T>
 __device__ __forceinline__ void zero_row(T* out, int V, int rank, int C) {
-  constexpr int E = Piece<T>::E;
   const Part p = part_of(out, V, rank, C);
-  const float z[E] = {};
-  for (int b = p.b0 + (int)threadIdx.x; b < p.b1; b += kRowThreads) Piece<T>::store(out + p.head + (int64_t)b * E, z);
+  uint4* to = reinterpret_cast<uint4*>(out + p.head);
+  for (int b = p.b0 + (int)threadIdx.x; b < p.b1; b += kRowThreads) __stcs(to + b, make_uint4(0, 0, 0, 0));
   if (p.extra >= 0) put(out + p.extra, 0.f);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads) stats_bwd_kernel(const StatsParams p) {
+__global__ void __launch_bounds__(kRowThreads, kPassBlocks) stats_bwd_kernel(const StatsParams p) {
   const int C = p.C, n = (int)(blockIdx.x / C), rank = (int)(blockIdx.x % C);
   const int target = p.target[n];
   const T* row = static_cast<const T*>(p.z) + (int64_t)n * p.stride;
@@ -472,7 +620,10 @@ __global__ void __launch_bounds__(kRowThreads) stats_bwd_kernel(const StatsParam
   const Part part = part_of(row, p.V, rank, C);
   const float scale = p.scale, lse = p.lse_in[n], g = p.g_lp[n] * scale, h = p.g_ent ? p.g_ent[n] * scale : 0.f;
   const float c = p.g_ent ? fmaf(h, p.ent_in[n], g) : g;
-  map_row(row, out, part, [=](float* z, int id, auto N) {
+  extern __shared__ uint4 buffer[];
+  const auto ring = ring_of<kPassRounds>(buffer, row, part);
+  ring.start(part.b0 + threadIdx.x);
+  map_row(row, out, part, ring, [=](float* z, int id, auto N) {
     float zt = 0.f;
 #pragma unroll
     for (int e = 0; e < N(); ++e) {
@@ -499,6 +650,7 @@ struct DistillParams {
   const float* g;
   void* dz;
   uint32_t* err;
+  bool check;   // a block past the rows checks all ids
 };
 
 struct TeacherShared {
@@ -529,23 +681,29 @@ __device__ __forceinline__ float block_add(float v, float* red) {
 }
 
 // Forward (LSE), backward (GRAD) or both.  Thread k < K holds the teacher's
-// k-th entry.  With both, C is chosen so that the rows in work stay in L2
-// between the two passes.
+// k-th entry.  With both, the second pass finds the row in L2.
 template <typename T, bool LSE, bool GRAD>
-__global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillParams p) {
+__global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPassBlocks) distill_kernel(const DistillParams p) {
   __shared__ Acc red[kRowWarps];
   __shared__ Acc mine;
   __shared__ TeacherShared ts;
   const int C = p.C, n = (int)(blockIdx.x / C), rank = (int)(blockIdx.x % C), t = threadIdx.x;
   const T* row = static_cast<const T*>(p.z) + (int64_t)n * p.stride;
   T* out = GRAD ? static_cast<T*>(p.dz) + (int64_t)n * p.stride : nullptr;
+  extern __shared__ uint4 buffer[];
+  if (LSE && n == p.N) {
+    if (rank == 0)
+      check_below((int64_t)p.N * p.K, p.V, p.err,
+                  [&](int64_t i) { return p.mask && !p.mask[i / p.K] ? -1 : p.ids[i]; });
+    return;
+  }
   const bool wanted = !p.mask || p.mask[n];
   int id = -1;
   float a = -INFINITY;
   if (wanted && t < p.K) {
     id = p.ids[(int64_t)n * p.K + t];
     if (id >= p.V) {
-      if (LSE && rank == 0) atomicOr(p.err, kErrBadList);
+      if (LSE && rank == 0 && !p.check) atomicOr(p.err, kErrBadList);
       id = -1;
     }
     if (id >= 0) a = p.tl[(int64_t)n * p.K + t] * p.sl2;
@@ -557,12 +715,14 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillParam
     return;
   }
   const Part part = part_of(row, p.V, rank, C);
+  const auto ring = ring_of<LSE && GRAD ? kStepRounds : kPassRounds>(buffer, row, part);
+  ring.start(part.b0 + t);
   const float zk = id >= 0 ? to_f(row[id]) : 0.f;
   const float top = block_max(a, ts.red);
   const float ek = id >= 0 ? ex2(a - top) : 0.f;
   const float sum = block_add(ek, ts.red);
   const float q = ek / sum;
-  if (GRAD) {
+  if (GRAD && t < kMaxTeacher) {
     ts.id[t] = id;
     ts.q[t] = q;
   }
@@ -570,8 +730,16 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillParam
   if (LSE) {
     float best;
     int round;
-    Acc s = pass<T, false, false>(row, part, p.sl2, best, round);
-    s = row_sum(s, red, &mine, C, p.sl2);
+    Acc s = pass<T, false, false>(row, part, ring, p.sl2, best, round);
+    if (GRAD) ring.start(part.b0 + t);   // again, now out of L2
+    s = block_sum(s, red, p.sl2);
+    if (C > 1) {
+      cg::cluster_group cl = cg::this_cluster();
+      if (t == 0) mine = s;
+      cl.sync();
+      s = cluster_sum(&mine, C, p.sl2);
+      cl.barrier_arrive();   // the others' sums have been read
+    }
     const float ls = log_sum(s);
     lse = fmaf(s.m, p.scale, ls);
     if (rank == 0) {
@@ -589,7 +757,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillParam
   if (GRAD) {
     const float scale = p.scale, g = p.g[n] * scale;
     __syncthreads();   // every zk is read before a logit may be overwritten
-    map_row(row, out, part, [=](float* z, int, auto N) {
+    map_row(row, out, part, ring, [=](float* z, int, auto N) {
 #pragma unroll
       for (int e = 0; e < N(); ++e) z[e] = g * ex2(fmaf(z[e], scale, -lse) * kLog2eT);
     });
@@ -606,7 +774,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(const DistillParam
       if (own && first) put(out + id, g * (ex2(fmaf(zk, scale, -lse) * kLog2eT) - qs));
     }
   }
-  if (LSE && C > 1) cg::this_cluster().sync();   // blocks read each other's shared memory
+  if (LSE && C > 1) cg::this_cluster().barrier_wait();
 }
 
 // ------------------------------------------------------------------- host
@@ -637,17 +805,60 @@ bool off_type(const void* x, int dtype) {
   return reinterpret_cast<uintptr_t>(x) & (dtype == STP_BF16 ? 1 : 3);
 }
 
-// Blocks of a row: enough that the GPU is full, while a block keeps 16 KB.
+// Blocks of a row: more than one where the rows alone do not fill the GPU, while
+// a block keeps 16 KB; a cluster's meeting costs more than that of a block
+// (2048 rows: 100 us with one block each, 138 with two).
 int split_of(int64_t rows, int64_t row_bytes) {
   int c = 1;
   while (c < kMaxSplit && rows * c < 608 && row_bytes / (2 * c) >= 16384) c *= 2;
   return c;
 }
 
-cudaError_t launch(const void* kernel, int64_t rows, int C, void* params, bool cluster, cudaStream_t s) {
+// For the step of both passes: the rows in work, kStepBlocks of 152 SMs over C,
+// have to stay in L2 from one pass to the next; beyond about 72 MB of its
+// 129 they do not (rows of 304 KB: 531 us with one block, 445 with two, 629 with
+// four, which meet too often).
+int step_split_of(int64_t rows, int64_t row_bytes) {
+  int c = split_of(rows, row_bytes);
+  while (c < kMaxSplit && 152 * kStepBlocks * row_bytes / c > (72 << 20)) c *= 2;
+  return c;
+}
+
+// The most whole numbers that one block checks: above, the
+// error word is cleared first and every row checks its own.
+constexpr int64_t kCheckMost = 65536;
+
+template <typename T>
+cudaError_t allow_rings_of() {
+  const void* pass[] = {(const void*)stats_fwd_kernel<T, false>, (const void*)stats_fwd_kernel<T, true>,
+                        (const void*)stats_bwd_kernel<T>, (const void*)distill_kernel<T, true, false>,
+                        (const void*)distill_kernel<T, false, true>};
+  cudaError_t e = cudaFuncSetAttribute((const void*)distill_kernel<T, true, true>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(kStepRounds));
+  for (const void* k : pass)
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(kPassRounds));
+  return e;
+}
+
+// The kernels' dynamic shared memory, above the default limit: set once.
+cudaError_t allow_rings() {
+  static std::once_flag once;
+  static cudaError_t err = cudaSuccess;
+  std::call_once(once, [] {
+    err = allow_rings_of<__nv_bfloat16>();
+    if (err == cudaSuccess) err = allow_rings_of<float>();
+  });
+  return err;
+}
+
+cudaError_t launch(const void* kernel, int rounds, int64_t rows, int C, void* params, bool cluster, cudaStream_t s) {
+  const cudaError_t e = allow_rings();
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * C));
   cfg.blockDim = dim3(kRowThreads);
+  cfg.dynamicSmemBytes = ring_bytes(rounds);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -704,9 +915,11 @@ extern "C" stp_status stp_token_stats_fwd(const stp_stats_desc* desc, const void
                            (desc->top_k > 0 && (!top_id || !top_logprob))))
     return fail(STP_EINVAL, "stp_token_stats_fwd: NULL device pointer");
   if (off_type(logits, desc->dtype)) return fail(STP_EINVAL, "stp_token_stats_fwd: logits misaligned for their type");
-  cudaError_t e = cudaMemsetAsync(d_ws, 0, 4, s);
+  const bool check = desc->n_rows > 0 && desc->n_rows <= kCheckMost;
+  cudaError_t e = check ? cudaSuccess : cudaMemsetAsync(d_ws, 0, 4, s);
   if (e == cudaSuccess && desc->n_rows > 0) {
     StatsParams p{};
+    p.check = check;
     p.N = desc->n_rows;
     p.V = desc->vocab;
     p.K = desc->top_k;
@@ -726,7 +939,7 @@ extern "C" stp_status stp_token_stats_fwd(const stp_stats_desc* desc, const void
                         ? (p.K ? (const void*)stats_fwd_kernel<__nv_bfloat16, true>
                                : (const void*)stats_fwd_kernel<__nv_bfloat16, false>)
                         : (p.K ? (const void*)stats_fwd_kernel<float, true> : (const void*)stats_fwd_kernel<float, false>);
-    e = launch(k, p.N, p.C, &p, true, s);
+    e = launch(k, kPassRounds, p.N + p.check, p.C, &p, true, s);
   }
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_token_stats_fwd: %s", cudaGetErrorString(e));
   return STP_OK;
@@ -758,7 +971,7 @@ extern "C" stp_status stp_token_stats_bwd(const stp_stats_desc* desc, const void
   p.C = split_of(p.N, row_bytes(p.V, desc->dtype));
   const cudaError_t e = launch(desc->dtype == STP_BF16 ? (const void*)stats_bwd_kernel<__nv_bfloat16>
                                                        : (const void*)stats_bwd_kernel<float>,
-                               p.N, p.C, &p, false, static_cast<cudaStream_t>(stream));
+                               kPassRounds, p.N, p.C, &p, false, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_token_stats_bwd: %s", cudaGetErrorString(e));
   return STP_OK;
 }
@@ -786,7 +999,8 @@ static stp_status distill(const char* name, const stp_distill_desc* desc, const 
   if (off_type(logits, desc->dtype) || off_type(dz, desc->dtype))
     return fail(STP_EINVAL, "%s: logits misaligned for their type", name);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = fwd ? cudaMemsetAsync(ws, 0, 4, s) : cudaSuccess;
+  const bool check = desc->n_rows > 0 && (int64_t)desc->n_rows * desc->n_teacher <= kCheckMost;
+  cudaError_t e = fwd && !check ? cudaMemsetAsync(ws, 0, 4, s) : cudaSuccess;
   if (e == cudaSuccess && desc->n_rows > 0) {
     DistillParams p = distill_params(desc, logits, ids, tl, mask);
     p.loss = loss;
@@ -795,19 +1009,17 @@ static stp_status distill(const char* name, const stp_distill_desc* desc, const 
     p.g = g;
     p.dz = dz;
     p.err = static_cast<uint32_t*>(ws);
+    p.check = check;
     const int64_t bytes = row_bytes(p.V, desc->dtype);
-    p.C = split_of(p.N, bytes);
-    // both passes: the rows in work at one time have to stay in L2
-    if (fwd && grad)
-      while (p.C < kMaxSplit && bytes / p.C > 40960) p.C *= 2;
-    const bool b = desc->dtype == STP_BF16;
-    const void* k = fwd && grad ? (b ? (const void*)distill_kernel<__nv_bfloat16, true, true>
-                                     : (const void*)distill_kernel<float, true, true>)
-                    : fwd       ? (b ? (const void*)distill_kernel<__nv_bfloat16, true, false>
-                                     : (const void*)distill_kernel<float, true, false>)
-                                : (b ? (const void*)distill_kernel<__nv_bfloat16, false, true>
-                                     : (const void*)distill_kernel<float, false, true>);
-    e = launch(k, p.N, p.C, &p, fwd, s);
+    const bool both = fwd && grad, b = desc->dtype == STP_BF16;
+    p.C = both ? step_split_of(p.N, bytes) : split_of(p.N, bytes);
+    const void* k = both  ? (b ? (const void*)distill_kernel<__nv_bfloat16, true, true>
+                               : (const void*)distill_kernel<float, true, true>)
+                    : fwd ? (b ? (const void*)distill_kernel<__nv_bfloat16, true, false>
+                               : (const void*)distill_kernel<float, true, false>)
+                          : (b ? (const void*)distill_kernel<__nv_bfloat16, false, true>
+                               : (const void*)distill_kernel<float, false, true>);
+    e = launch(k, both ? kStepRounds : kPassRounds, p.N + p.check, p.C, &p, fwd, s);
   }
   if (e != cudaSuccess) return fail(STP_ECUDA, "%s: %s", name, cudaGetErrorString(e));
   return STP_OK;

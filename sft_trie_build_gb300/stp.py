@@ -168,12 +168,12 @@ def lib():
         L.stp_gdn_fwd_train.restype = st
         L.stp_gdn_bwd.argtypes = [ctypes.POINTER(GdnDesc)] + [_P] * 13
         L.stp_gdn_bwd.restype = st
-        qk, f64 = ctypes.POINTER(QkDesc), ctypes.POINTER(ctypes.c_double)
+        qk = ctypes.POINTER(QkDesc)
         L.stp_qk_norm_rope_workspace_size.argtypes = [qk, _SZ]
         L.stp_qk_norm_rope_workspace_size.restype = st
-        L.stp_qk_norm_rope_fwd.argtypes = [qk] + [_P] * 4 + [f64] + [_P] * 4
+        L.stp_qk_norm_rope_fwd.argtypes = [qk] + [_P] * 9
         L.stp_qk_norm_rope_fwd.restype = st
-        L.stp_qk_norm_rope_bwd.argtypes = [qk] + [_P] * 4 + [f64] + [_P] * 9
+        L.stp_qk_norm_rope_bwd.argtypes = [qk] + [_P] * 14
         L.stp_qk_norm_rope_bwd.restype = st
         i32, attn = ctypes.c_int32, ctypes.POINTER(AttnDesc)
         L.stp_count_window_tile_pairs.argtypes = [_I32P, _I32P, i32, i32, i32, i32, _I64P]
@@ -218,21 +218,21 @@ def _ptr(a, ctype):
 
 
 def _dptr(t):
-    """Device pointer of a torch tensor (or an int address)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return ctypes.c_void_p(t)
-    return ctypes.c_void_p(t.data_ptr())
+    """Device address of a torch tensor (or an int address); None is NULL."""
+    return t if t is None or isinstance(t, int) else t.data_ptr()
+
+
+_current_stream = None
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            _current_stream = torch.cuda.current_stream
+        return _current_stream().cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 # ---------------------------------------------------------------------------
@@ -560,13 +560,13 @@ def qk_desc(n_tokens, n_q_heads, n_kv_heads, head_dim=128, rotary_dim=None, inte
 
 
 def _freq(inv_freq, desc):
+    """Host address of rotary_dim / 2 float64 values (and the array that holds them)."""
     if inv_freq is None:
-        return None
-    if inv_freq.dtype != np.float64 or not inv_freq.flags.c_contiguous:
-        inv_freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+        return None, None
+    inv_freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
     if inv_freq.size < desc.rotary_dim // 2:
         raise ValueError("inv_freq must hold rotary_dim / 2 values")
-    return _ptr(inv_freq, ctypes.c_double)
+    return inv_freq.ctypes.data, inv_freq
 
 
 def stp_qk_norm_rope_workspace_size(desc: QkDesc) -> int:
@@ -578,15 +578,17 @@ def stp_qk_norm_rope_workspace_size(desc: QkDesc) -> int:
 
 def stp_qk_norm_rope_fwd(desc: QkDesc, q, k, w_q, w_k, inv_freq, position_ids, q_out, k_out, stream=None):
     """inv_freq: host float64 array [rotary_dim / 2] (None when rotary_dim is 0)."""
+    freq, _held = _freq(inv_freq, desc)
     _check(lib().stp_qk_norm_rope_fwd(ctypes.byref(desc), _dptr(q), _dptr(k), _dptr(w_q), _dptr(w_k),
-                                      _freq(inv_freq, desc), _dptr(position_ids), _dptr(q_out), _dptr(k_out),
+                                      freq, _dptr(position_ids), _dptr(q_out), _dptr(k_out),
                                       _stream(stream)), "stp_qk_norm_rope_fwd")
 
 
 def stp_qk_norm_rope_bwd(desc: QkDesc, q, k, w_q, w_k, inv_freq, position_ids, d_q, d_k, dx_q, dx_k, dw_q, dw_k, ws,
                          stream=None):
+    freq, _held = _freq(inv_freq, desc)
     _check(lib().stp_qk_norm_rope_bwd(ctypes.byref(desc), _dptr(q), _dptr(k), _dptr(w_q), _dptr(w_k),
-                                      _freq(inv_freq, desc), _dptr(position_ids), _dptr(d_q), _dptr(d_k),
+                                      freq, _dptr(position_ids), _dptr(d_q), _dptr(d_k),
                                       _dptr(dx_q), _dptr(dx_k), _dptr(dw_q), _dptr(dw_k), _dptr(ws),
                                       _stream(stream)), "stp_qk_norm_rope_bwd")
 
