@@ -999,7 +999,7 @@ static stp_status distill(const char* name, const stp_distill_desc* desc, const 
   if (off_type(logits, desc->dtype) || off_type(dz, desc->dtype))
     return fail(STP_EINVAL, "%s: logits misaligned for their type", name);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool check = desc->n_rows > 0 && (int64_t)desc->n_rows * desc->n_teacher <= kCheckMost;
+  const bool check = fwd && desc->n_rows > 0 && (int64_t)desc->n_rows * desc->n_teacher <= kCheckMost;
   cudaError_t e = fwd && !check ? cudaMemsetAsync(ws, 0, 4, s) : cudaSuccess;
   if (e == cudaSuccess && desc->n_rows > 0) {
     DistillParams p = distill_params(desc, logits, ids, tl, mask);
