@@ -543,7 +543,7 @@ typedef struct {
   int64_t k_stride;    /* of k and dx_k: at least Hkv * D; multiples of 16 bytes */
 } stp_qk_desc;
 
-/* Device workspace of stp_qk_norm_rope_bwd: 2432 bytes per channel of a head. */
+/* Device workspace of stp_qk_norm_rope_bwd: 1216 bytes per channel of a head. */
 stp_status stp_qk_norm_rope_workspace_size(const stp_qk_desc* desc, size_t* ws_bytes);
 
 /*

@@ -14,8 +14,11 @@
 // channels (16 bytes each in bf16) that are the two sides of eight rotated
 // pairs, so the rotation needs no exchange between lanes: runs u and
 // u + rotary_dim / 16 for halves, 2u and 2u + 1 for interleaved pairs.  D / 16
-// lanes make a vector (G, the next power of two, with the rest idle), a warp
-// takes 32 / G heads of one token at a time.
+// lanes make a vector (G, the next power of two, with the rest idle), a pass
+// of a warp takes 32 / G heads of one token.  The next passes' vectors come by
+// asynchronous copies into slots of shared memory of the lane's own, so they
+// take no registers and need no barrier.  16384 tokens of 32 + 8 heads of 128
+// bf16 channels: forward 57 us, 5.9 TB/s, backward 84 us, 6.0 TB/s.
 //
 // The angle in turns is position * (inv_freq / 2 pi) mod 1, kept as 64-bit
 // fixed point: the product wraps by itself, so a position of a million is as
@@ -28,18 +31,28 @@
 
 #include "internal.h"
 #include "layout.h"
+#include "tc_ptx.cuh"
 
 namespace stp {
 namespace {
 
 constexpr int kQkThreads = 256;
 constexpr int kQkMaxDim = 512;
-constexpr int kQkBwdBlocks = 608;   // partial sums of dw a call writes, at most
+constexpr int kQkFwdBlocks = 4, kQkBwdBlocks = 2;    // per SM
+constexpr int kQkBwdGrid = 152 * kQkBwdBlocks;       // partial sums of dw a call writes, at most
+// Passes on their way per warp.  More than these cost: the forward of 16384 tokens of
+// 40 heads of 128 bf16 channels measured 57 us with 2, 3 and 4, 65 with 6, the
+// backward 84 with 2, 94 with 3 and 4.
+template <typename T>
+constexpr int fwd_depth() { return sizeof(T) == 2 ? 3 : 2; }
+constexpr int kQkBwdDepth = 2;
+// Shared memory of `runs` runs of eight channels per lane and pass.
+template <typename T>
+constexpr int ring_bytes(int runs, int depth) { return runs * ((int)sizeof(T) / 2) * depth * kQkThreads * 16; }
 
 struct QkParams {
   int N, Hq, Hkv, D, rot;
-  int hp, parts;        // forward: heads of a work item, items of a token
-  int blocks_q, blocks;  // backward: blocks of the queries, of both
+  int blocks_q, blocks;  // blocks of the queries (backward), of both
   int64_t qs, ks;       // elements between tokens of q / k (and of dx_q / dx_k)
   float eps;
   const void* q;
@@ -57,46 +70,61 @@ struct QkParams {
   uint64_t freq[kQkMaxDim / 2];   // turns per position, 2^-64 units
 };
 
-// Eight channels: 16 bytes of bf16 or 32 of float.
+// Eight channels as four pairs: kPieces 16-byte pieces of memory.
 template <typename T>
 struct Run;
 template <>
 struct Run<__nv_bfloat16> {
-  uint4 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float* f) const {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  static constexpr int kPieces = 1;
+  static __device__ __forceinline__ void get(const uint4* v, float2* f) {
+    const uint32_t w[4] = {v->x, v->y, v->z, v->w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
   // the one rounding to bf16, of the finished value
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  static __device__ __forceinline__ void put(__nv_bfloat16* p, const float2* f) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(tc::pack_bf16x2(f[0].x, f[0].y), tc::pack_bf16x2(f[1].x, f[1].y),
+                                              tc::pack_bf16x2(f[2].x, f[2].y), tc::pack_bf16x2(f[3].x, f[3].y));
   }
 };
 template <>
 struct Run<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+  static constexpr int kPieces = 2;
+  static __device__ __forceinline__ void get(const uint4* v, float2* f) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[2 * i] = make_float2(__uint_as_float(v[i].x), __uint_as_float(v[i].y));
+      f[2 * i + 1] = make_float2(__uint_as_float(v[i].z), __uint_as_float(v[i].w));
+    }
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float* f) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  static __device__ __forceinline__ void put(float* p, const float2* f) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
   }
-  static __device__ __forceinline__ void store(float* p, const float* f) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+};
+
+// A lane's vectors on their way, `depth` of them, in shared memory that no
+// other thread touches: P pieces each, kQkThreads apart.
+template <int P>
+struct Lane {
+  uint4* slot;
+  __device__ __forceinline__ void fetch(int at, int piece, const void* src) const {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     tc::smem_u32(slot + (at * P + piece) * kQkThreads)),
+                 "l"(src)
+                 : "memory");
+  }
+  template <typename T>
+  __device__ __forceinline__ void fetch_run(int at, int piece, const T* src) const {
+#pragma unroll
+    for (int i = 0; i < Run<T>::kPieces; ++i) fetch(at, piece + i, reinterpret_cast<const uint4*>(src) + i);
+  }
+  template <typename T>
+  __device__ __forceinline__ void get_run(int at, int piece, float2* f) const {
+    uint4 v[Run<T>::kPieces];
+#pragma unroll
+    for (int i = 0; i < Run<T>::kPieces; ++i) v[i] = slot[(at * P + piece + i) * kQkThreads];
+    Run<T>::get(v, f);
   }
 };
 
@@ -113,33 +141,53 @@ __device__ __forceinline__ void run_at(int u, int rot, int& a, int& b) {
   }
 }
 
-// cos and sin of the eight pairs of lane u at position t; (1, 0) past them.
-__device__ __forceinline__ void angles(const uint64_t* freq, int u, int rot, int t, float* c, float* s) {
+// cos and sin of the eight pairs of lane u at position t, (1, 0) past the
+// rotated ones.  The 32 / G lanes of the same u make a share each and exchange
+// them.
+template <int G>
+__device__ __forceinline__ void angles(const uint64_t* freq, int u, int rot, int t, float2* c, float2* s) {
+  constexpr int NG = 32 / G < 8 ? 32 / G : 8, EACH = 8 / NG;
+  const int grp = ((int)threadIdx.x & 31) / G % NG;
+  float ce[EACH], se[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    ce[i] = 1.f;
+    se[i] = 0.f;
+    if (u < rot / 16) {
+      // the top 32 bits as a signed part of a turn, in half turns
+      const uint64_t turns = (uint64_t)(int64_t)t * freq[8 * u + i * NG + grp];
+      sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &se[i], &ce[i]);
+    }
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    c[e] = 1.f;
-    s[e] = 0.f;
-  }
-  if (u < rot / 16) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint64_t turns = (uint64_t)(int64_t)t * freq[8 * u + e];
-      // the top 32 bits as a signed part of a turn, in half turns
-      sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s[e], &c[e]);
+    float cv = ce[e / NG], sv = se[e / NG];
+    if (NG > 1) {
+      cv = __shfl_sync(0xffffffffu, cv, (e % NG) * G + u);
+      sv = __shfl_sync(0xffffffffu, sv, (e % NG) * G + u);
     }
+    (e & 1 ? c[e / 2].y : c[e / 2].x) = cv;
+    (e & 1 ? s[e / 2].y : s[e / 2].x) = sv;
   }
 }
 
-// (a, b) -> (a cos - b sin, a sin + b cos) over the lane's eight pairs.
+// (a, b) -> (a cos - b sin, a sin + b cos) over a lane's eight pairs; x holds
+// its two runs, c and s the pairs' cosines and sines.
 template <bool INTER>
-__device__ __forceinline__ void rotate(float* x, const float* c, const float* s) {
+__device__ __forceinline__ void rotate(float2* x, const float2* c, const float2* s) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float& a = x[INTER ? 2 * e : e];
-    float& b = x[INTER ? 2 * e + 1 : e + 8];
-    const float a0 = a, b0 = b;
-    a = fmaf(a0, c[e], -b0 * s[e]);
-    b = fmaf(a0, s[e], b0 * c[e]);
+  for (int e = 0; e < 4; ++e) {
+    if (INTER) {
+      const float2 a = x[2 * e], b = x[2 * e + 1];   // pairs 2e and 2e + 1
+      x[2 * e] = __ffma2_rn(a, make_float2(c[e].x, c[e].x),
+                            __fmul2_rn(make_float2(a.y, a.x), make_float2(-s[e].x, s[e].x)));
+      x[2 * e + 1] = __ffma2_rn(b, make_float2(c[e].y, c[e].y),
+                                __fmul2_rn(make_float2(b.y, b.x), make_float2(-s[e].y, s[e].y)));
+    } else {
+      const float2 a = x[e], b = x[e + 4];
+      x[e] = __ffma2_rn(a, c[e], __fmul2_rn(b, make_float2(-s[e].x, -s[e].y)));
+      x[e + 4] = __ffma2_rn(a, s[e], __fmul2_rn(b, c[e]));
+    }
   }
 }
 
@@ -150,183 +198,269 @@ __device__ __forceinline__ float sum_group(float v) {
   return v;
 }
 
-// One work item: `hp` heads (queries first, then keys) of one token, by one
-// warp; two vectors per lane are in flight.
+// A lane's place in its warp's run of passes (32 / G heads of one token each:
+// the queries' passes of a token, then the keys', then the next token): a
+// pointer that goes on by `step` elements but where the tensor or the token
+// changes.
+template <typename T>
+struct Walk {
+  T* base[2];          // of queries and keys, at the lane's first head and channel
+  int64_t stride[2];   // between tokens
+  int64_t tok;
+  T* p;
+  int pass, pq, passes, step;
+  __device__ __forceinline__ void init(T* q, T* k, int64_t qs, int64_t ks, int offset, int64_t unit, int pq_, int pk,
+                                       int step_) {
+    base[0] = q + offset;
+    base[1] = k + offset;
+    stride[0] = qs;
+    stride[1] = ks;
+    pq = pq_;
+    passes = pq_ + pk;
+    step = step_;
+    tok = unit / passes;
+    pass = (int)(unit % passes);
+    p = pass < pq ? base[0] + tok * qs + pass * step : base[1] + tok * ks + (pass - pq) * step;
+  }
+  __device__ __forceinline__ void next() {
+    p += step;
+    if (++pass == pq) p = base[1] + tok * stride[1];
+    if (pass == passes) {
+      pass = 0;
+      p = base[0] + ++tok * stride[0];
+    }
+  }
+};
+
+// An equal run of `units` passes for this warp of the blocks [b0, b0 + blocks).
+struct Share {
+  int64_t u0;
+  int n;
+  __device__ __forceinline__ Share(int64_t units, int b0, int blocks) {
+    const int64_t warps = (int64_t)blocks * (kQkThreads / 32);
+    const int64_t me = (int64_t)((int)blockIdx.x - b0) * (kQkThreads / 32) + (threadIdx.x >> 5);
+    u0 = units * me / warps;
+    n = (int)(units * (me + 1) / warps - u0);
+  }
+};
+
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Loads the frequencies and a weight into shared memory.
+__device__ __forceinline__ void load_constants(const QkParams& p, const float* src, uint64_t* freq, float* w) {
+  for (int i = threadIdx.x; i < p.rot / 2; i += kQkThreads) freq[i] = p.freq[i];
+  for (int i = threadIdx.x; i < p.D; i += kQkThreads) w[i] = src ? src[i] : 1.f;
+}
+
+__device__ __forceinline__ void load_weight(const float* w, int ra, int rb, float2* wl) {
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const float4 v = *reinterpret_cast<const float4*>(w + (e < 4 ? ra + 2 * e : rb + 2 * e - 8));
+    wl[e] = make_float2(v.x, v.y);
+    wl[e + 1] = make_float2(v.z, v.w);
+  }
+}
+
+// Every warp takes an equal run of passes, several of them on their way; a
+// token's angles are made when its first pass comes up.
 template <typename T, int G, bool INTER>
-__global__ void __launch_bounds__(kQkThreads) qk_fwd_kernel(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kQkThreads, kQkFwdBlocks) qk_fwd_kernel(const __grid_constant__ QkParams p) {
   __shared__ uint64_t freq[kQkMaxDim / 2];
   __shared__ __align__(16) float w[2][kQkMaxDim];
-  for (int i = threadIdx.x; i < p.rot / 2; i += kQkThreads) freq[i] = p.freq[i];
-  for (int i = threadIdx.x; i < p.D; i += kQkThreads) {
-    w[0][i] = p.wq ? p.wq[i] : 1.f;
-    w[1][i] = p.wk ? p.wk[i] : 1.f;
-  }
-  __syncthreads();
-  constexpr int NG = 32 / G, R = 2;
+  extern __shared__ uint4 ring[];
+  constexpr int NG = 32 / G, RP = Run<T>::kPieces, DEPTH = fwd_depth<T>();
   const int lane = threadIdx.x & 31, u = lane % G, grp = lane / G;
   const bool on = u < p.D / 16;
   int ra, rb;
   run_at<INTER>(on ? u : 0, p.rot, ra, rb);
-  const float inv_d = 1.f / (float)p.D;
-  const int H = p.Hq + p.Hkv;
-  const int64_t items = (int64_t)p.N * p.parts;
-  const int64_t step = (int64_t)gridDim.x * (kQkThreads / 32);
-  for (int64_t it = (int64_t)blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
-    const int64_t tok = it / p.parts;
-    const int h0 = (int)(it - tok * p.parts) * p.hp, h1 = min(H, h0 + p.hp);
-    float c[8], s[8];
-    angles(freq, u, p.rot, p.pos[tok], c, s);
-    for (int hb = h0; hb < h1; hb += NG * R) {
-      Run<T> xa[R], xb[R];
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        const int h = hb + k * NG + grp;
-        xa[k].zero();
-        xb[k].zero();
-        if (on && h < h1) {
-          const T* src = h < p.Hq ? static_cast<const T*>(p.q) + tok * p.qs + (int64_t)h * p.D
-                                  : static_cast<const T*>(p.k) + tok * p.ks + (int64_t)(h - p.Hq) * p.D;
-          xa[k].load(src + ra);
-          xb[k].load(src + rb);
-        }
+  const int pq = (p.Hq + NG - 1) / NG, pk = (p.Hkv + NG - 1) / NG, passes = pq + pk;
+  const Share sh((int64_t)p.N * passes, 0, gridDim.x);
+  // whether the lane holds a head of pass k
+  auto live = [&](int k) { return on && (k < pq ? k * NG + grp < p.Hq : (k - pq) * NG + grp < p.Hkv); };
+  const Lane<2 * RP> in = {ring + threadIdx.x};
+  Walk<const T> src;
+  src.init(static_cast<const T*>(p.q), static_cast<const T*>(p.k), p.qs, p.ks, grp * p.D + ra, sh.u0, pq, pk, NG * p.D);
+  int left = sh.n;   // passes not fetched yet
+  auto fetch = [&](int at) {
+    if (left > 0) {
+      if (live(src.pass)) {
+        in.fetch_run(at, 0, src.p);
+        in.fetch_run(at, RP, src.p + (rb - ra));
       }
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        const int h = hb + k * NG + grp;
-        float x[16];
-        xa[k].get(x);
-        xb[k].get(x + 8);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-        ss = sum_group<G>(ss);
-        const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
-        const bool is_q = h < p.Hq;
-        const float* wv = w[is_q ? 0 : 1];
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const float4 wa = *reinterpret_cast<const float4*>(wv + ra + e);
-          const float4 wb = *reinterpret_cast<const float4*>(wv + rb + e);
-          x[e] *= r * wa.x; x[e + 1] *= r * wa.y; x[e + 2] *= r * wa.z; x[e + 3] *= r * wa.w;
-          x[8 + e] *= r * wb.x; x[9 + e] *= r * wb.y; x[10 + e] *= r * wb.z; x[11 + e] *= r * wb.w;
-        }
-        rotate<INTER>(x, c, s);
-        if (on && h < h1) {
-          T* dst = is_q ? static_cast<T*>(p.q_out) + (tok * p.Hq + h) * p.D
-                        : static_cast<T*>(p.k_out) + (tok * p.Hkv + (h - p.Hq)) * p.D;
-          Run<T>::store(dst + ra, x);
-          Run<T>::store(dst + rb, x + 8);
-        }
-      }
+      src.next();
+      --left;
     }
+    commit_copies();
+  };
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) fetch(d);
+  load_constants(p, p.wq, freq, w[0]);
+  load_constants(p, p.wk, freq, w[1]);
+  __syncthreads();
+  const float inv_d = 1.f / (float)p.D;
+  float2 c[4], s[4];
+  Walk<T> dst;
+  dst.init(static_cast<T*>(p.q_out), static_cast<T*>(p.k_out), (int64_t)p.Hq * p.D, (int64_t)p.Hkv * p.D,
+           grp * p.D + ra, sh.u0, pq, pk, NG * p.D);
+  const int32_t* pos = p.pos + dst.tok;
+  int t = sh.n > 0 ? *pos : 0;
+  int slot = 0;
+  for (int i = 0; i < sh.n; ++i) {
+    if (i == 0 || dst.pass == 0) {
+      angles<G>(freq, u, p.rot, t, c, s);
+      if (sh.n - i > passes - dst.pass) t = *++pos;   // on its way for the next token
+    }
+    wait_copies<DEPTH - 1>();
+    float2 x[8];   // of lanes that hold no head: anything, and not stored
+    in.template get_run<T>(slot, 0, x);
+    in.template get_run<T>(slot, RP, x + 4);
+    float2 ss2 = __fmul2_rn(x[0], x[0]);
+#pragma unroll
+    for (int e = 1; e < 8; ++e) ss2 = __ffma2_rn(x[e], x[e], ss2);
+    const float ss = sum_group<G>(on ? ss2.x + ss2.y : 0.f);
+    fetch(slot);
+    slot = slot + 1 == DEPTH ? 0 : slot + 1;
+    const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+    const float2 r2 = make_float2(r, r);
+    float2 wl[8];
+    load_weight(w[dst.pass >= pq], ra, rb, wl);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __fmul2_rn(x[e], __fmul2_rn(r2, wl[e]));
+    rotate<INTER>(x, c, s);
+    if (live(dst.pass)) {
+      Run<T>::put(dst.p, x);
+      Run<T>::put(dst.p + (rb - ra), x + 4);
+    }
+    dst.next();
   }
 }
 
-// A block works on the queries or on the keys alone, so that a lane carries
-// the sums of one weight; each block adds up its lanes' sums in a fixed order
-// and writes them for qk_dw_kernel.
+// The same walk over x and dy.  A block works on the queries or on the keys
+// alone, so that a lane carries the sums of one weight; each block adds up its lanes' sums in a fixed order and writes them for
+// qk_dw_kernel.
 template <typename T, int G, bool INTER>
-__global__ void __launch_bounds__(kQkThreads) qk_bwd_kernel(const __grid_constant__ QkParams p) {
+__global__ void __launch_bounds__(kQkThreads, kQkBwdBlocks) qk_bwd_kernel(const __grid_constant__ QkParams p) {
   __shared__ uint64_t freq[kQkMaxDim / 2];
   __shared__ __align__(16) float w[kQkMaxDim];
-  __shared__ __align__(16) float red[kQkThreads / 32][kQkMaxDim];
-  const bool is_q = (int)blockIdx.x < p.blocks_q;
-  const float* wsrc = is_q ? p.wq : p.wk;
-  for (int i = threadIdx.x; i < p.rot / 2; i += kQkThreads) freq[i] = p.freq[i];
-  for (int i = threadIdx.x; i < p.D; i += kQkThreads) w[i] = wsrc ? wsrc[i] : 1.f;
-  __syncthreads();
-  constexpr int NG = 32 / G;
+  extern __shared__ uint4 ring[];
+  constexpr int NG = 32 / G, RP = Run<T>::kPieces, DEPTH = kQkBwdDepth;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u = lane % G, grp = lane / G;
   const bool on = u < p.D / 16;
   int ra, rb;
   run_at<INTER>(on ? u : 0, p.rot, ra, rb);
-  const float inv_d = 1.f / (float)p.D;
-  const int H = is_q ? p.Hq : p.Hkv;
-  const int64_t xs = is_q ? p.qs : p.ks;
-  const T* xin = static_cast<const T*>(is_q ? p.q : p.k);
-  const T* dy = static_cast<const T*>(is_q ? p.dq : p.dk);
-  T* dx = static_cast<T*>(is_q ? p.q_out : p.k_out);
-  const int block = is_q ? blockIdx.x : blockIdx.x - p.blocks_q;
-  const int64_t step = (int64_t)(is_q ? p.blocks_q : p.blocks - p.blocks_q) * (kQkThreads / 32);
-  float dw[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) dw[e] = 0.f;
-  const int parts = (H + p.hp - 1) / p.hp;
-  const int64_t items = (int64_t)p.N * parts;
-  for (int64_t it = (int64_t)block * (kQkThreads / 32) + warp; it < items; it += step) {
-    const int64_t tok = it / parts;
-    const int h0 = (int)(it - tok * parts) * p.hp, h1 = min(H, h0 + p.hp);
-    float c[8], s[8];
-    angles(freq, u, p.rot, p.pos[tok], c, s);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] = -s[e];
-    for (int hb = h0; hb < h1; hb += NG) {
-      const int h = hb + grp;
-      const bool live = on && h < h1;
-      Run<T> xa, xb, ga, gb;
-      xa.zero();
-      xb.zero();
-      ga.zero();
-      gb.zero();
-      if (live) {
-        const T* src = xin + tok * xs + (int64_t)h * p.D;
-        const T* gsrc = dy + (tok * H + h) * p.D;
-        xa.load(src + ra);
-        xb.load(src + rb);
-        ga.load(gsrc + ra);
-        gb.load(gsrc + rb);
+  const bool is_q = (int)blockIdx.x < p.blocks_q;
+  const int H = is_q ? p.Hq : p.Hkv, passes = (H + NG - 1) / NG, step = NG * p.D, first = grp * p.D + ra;
+  const Share sh((int64_t)p.N * passes, is_q ? 0 : p.blocks_q, is_q ? p.blocks_q : p.blocks - p.blocks_q);
+  const int64_t xs = is_q ? p.qs : p.ks, gs = (int64_t)H * p.D;
+  const Lane<4 * RP> in = {ring + threadIdx.x};
+  // one tensor: no pass is the first of another
+  const T* x0 = static_cast<const T*>(is_q ? p.q : p.k);
+  const T* g0 = static_cast<const T*>(is_q ? p.dq : p.dk);
+  Walk<const T> src, gsrc;
+  src.init(x0, x0, xs, xs, first, sh.u0, passes, 0, step);
+  gsrc.init(g0, g0, gs, gs, first, sh.u0, passes, 0, step);
+  int left = sh.n;
+  auto fetch = [&](int at) {
+    if (left > 0) {
+      if (on && src.pass * NG + grp < H) {
+        in.fetch_run(at, 0, src.p);
+        in.fetch_run(at, RP, src.p + (rb - ra));
+        in.fetch_run(at, 2 * RP, gsrc.p);
+        in.fetch_run(at, 3 * RP, gsrc.p + (rb - ra));
       }
-      float x[16], g[16];
-      xa.get(x);
-      xb.get(x + 8);
-      ga.get(g);
-      gb.get(g + 8);
-      rotate<INTER>(g, c, s);
-      float ss = 0.f, dot = 0.f;
-      float wl[16];
-#pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        *reinterpret_cast<float4*>(wl + e) = *reinterpret_cast<const float4*>(w + ra + e);
-        *reinterpret_cast<float4*>(wl + 8 + e) = *reinterpret_cast<const float4*>(w + rb + e);
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        ss = fmaf(x[e], x[e], ss);
-        dot = fmaf(g[e] * wl[e], x[e], dot);
-      }
-      ss = sum_group<G>(ss);
-      dot = sum_group<G>(dot);
-      const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
-      const float m = dot * inv_d * r * r;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        dw[e] = fmaf(g[e], x[e] * r, dw[e]);
-        g[e] = r * fmaf(g[e], wl[e], -x[e] * m);
-      }
-      if (live) {
-        T* dst = dx + tok * xs + (int64_t)h * p.D;
-        Run<T>::store(dst + ra, g);
-        Run<T>::store(dst + rb, g + 8);
-      }
+      src.next();
+      gsrc.next();
+      --left;
     }
-  }
-  // the warp's groups, then the block's warps
+    commit_copies();
+  };
 #pragma unroll
-  for (int e = 0; e < 16; ++e)
+  for (int d = 0; d < DEPTH; ++d) fetch(d);
+  load_constants(p, is_q ? p.wq : p.wk, freq, w);
+  __syncthreads();
+  const float inv_d = 1.f / (float)p.D;
+  float2 c[4], s[4], dw[8];
 #pragma unroll
-    for (int o = G; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
-  if (on && grp == 0) {
+  for (int e = 0; e < 8; ++e) dw[e] = make_float2(0.f, 0.f);
+  T* d0 = static_cast<T*>(is_q ? p.q_out : p.k_out);
+  Walk<T> dst;
+  dst.init(d0, d0, xs, xs, first, sh.u0, passes, 0, step);
+  const int32_t* pos = p.pos + dst.tok;
+  int t = sh.n > 0 ? *pos : 0;
+  int slot = 0;
+  for (int i = 0; i < sh.n; ++i) {
+    if (i == 0 || dst.pass == 0) {
+      angles<G>(freq, u, p.rot, t, c, s);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = make_float2(-s[e].x, -s[e].y);
+      if (sh.n - i > passes - dst.pass) t = *++pos;
+    }
+    wait_copies<DEPTH - 1>();
+    const bool live = on && dst.pass * NG + grp < H;
+    float2 x[8], g[8];
+    if (live) {
+      in.template get_run<T>(slot, 0, x);
+      in.template get_run<T>(slot, RP, x + 4);
+      in.template get_run<T>(slot, 2 * RP, g);
+      in.template get_run<T>(slot, 3 * RP, g + 4);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = g[e] = make_float2(0.f, 0.f);
+    }
+    rotate<INTER>(g, c, s);
+    float2 ss2 = make_float2(0.f, 0.f), dot2 = make_float2(0.f, 0.f), wl[8];
+    load_weight(w, ra, rb, wl);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      red[warp][ra + e] = dw[e];
-      red[warp][rb + e] = dw[8 + e];
+      ss2 = __ffma2_rn(x[e], x[e], ss2);
+      dot2 = __ffma2_rn(__fmul2_rn(g[e], wl[e]), x[e], dot2);
+    }
+    fetch(slot);
+    slot = slot + 1 == DEPTH ? 0 : slot + 1;
+    const float ss = sum_group<G>(ss2.x + ss2.y);
+    const float dot = sum_group<G>(dot2.x + dot2.y);
+    const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+    const float m = -dot * inv_d * r * r * r;   // dx = g w r + x m
+    const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 gr = __fmul2_rn(g[e], r2);
+      dw[e] = __ffma2_rn(gr, x[e], dw[e]);
+      g[e] = __ffma2_rn(gr, wl[e], __fmul2_rn(x[e], m2));
+    }
+    if (live) {
+      Run<T>::put(dst.p, g);
+      Run<T>::put(dst.p + (rb - ra), g + 4);
+    }
+    dst.next();
+  }
+  // the warp's groups, then the block's warps
+  // (over the ring, which is done with: eight rows of D <= 512 sums fit)
+  float* red = reinterpret_cast<float*>(ring);
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+#pragma unroll
+    for (int o = G; o < 32; o <<= 1) {
+      dw[e].x += __shfl_xor_sync(0xffffffffu, dw[e].x, o);
+      dw[e].y += __shfl_xor_sync(0xffffffffu, dw[e].y, o);
+    }
+  __syncthreads();
+  if (on && grp == 0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      *reinterpret_cast<float2*>(red + warp * p.D + ra + 2 * e) = dw[e];
+      *reinterpret_cast<float2*>(red + warp * p.D + rb + 2 * e) = dw[4 + e];
     }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < p.D; i += kQkThreads) {
     float t = 0.f;
 #pragma unroll
-    for (int k = 0; k < kQkThreads / 32; ++k) t += red[k][i];
+    for (int k = 0; k < kQkThreads / 32; ++k) t += red[k * p.D + i];
     p.part[(int64_t)blockIdx.x * p.D + i] = t;
   }
 }
@@ -393,38 +527,50 @@ stp_status fill_qk(const stp_qk_desc* d, const double* inv_freq, QkParams& p) {
 
 bool off16(const void* x) { return reinterpret_cast<uintptr_t>(x) & 15; }
 
-// Launches `K<T, G, INTER>` for the descriptor's type, vector width and pairs.
-#define STP_QK_LAUNCH(KERNEL, GRID)                                                                    \
-  do {                                                                                                 \
-    const int units = desc->head_dim / 16;                                                             \
-    const int g = units <= 1 ? 1 : units <= 2 ? 2 : units <= 4 ? 4 : units <= 8 ? 8 : units <= 16 ? 16 : 32; \
-    if (desc->dtype == STP_BF16) {                                                                     \
-      STP_QK_G(KERNEL, __nv_bfloat16, GRID);                                                           \
-    } else {                                                                                           \
-      STP_QK_G(KERNEL, float, GRID);                                                                   \
-    }                                                                                                  \
+// Launches KERNEL<T, G, INTER> for the descriptor's type, vector width and
+// pairs; the dynamic shared memory RING(T) may pass the default limit, which is
+// raised once per kernel.
+#define STP_QK_LAUNCH(KERNEL, GRID, RING)                                                          \
+  do {                                                                                             \
+    const int units = desc->head_dim / 16;                                                         \
+    if (units <= 1) STP_QK_T(KERNEL, 1, GRID, RING);                                               \
+    else if (units <= 2) STP_QK_T(KERNEL, 2, GRID, RING);                                          \
+    else if (units <= 4) STP_QK_T(KERNEL, 4, GRID, RING);                                          \
+    else if (units <= 8) STP_QK_T(KERNEL, 8, GRID, RING);                                          \
+    else if (units <= 16) STP_QK_T(KERNEL, 16, GRID, RING);                                        \
+    else STP_QK_T(KERNEL, 32, GRID, RING);                                                         \
   } while (0)
-#define STP_QK_G(KERNEL, T, GRID)                      \
-  switch (g) {                                         \
-    case 1: STP_QK_I(KERNEL, T, 1, GRID); break;       \
-    case 2: STP_QK_I(KERNEL, T, 2, GRID); break;       \
-    case 4: STP_QK_I(KERNEL, T, 4, GRID); break;       \
-    case 8: STP_QK_I(KERNEL, T, 8, GRID); break;       \
-    case 16: STP_QK_I(KERNEL, T, 16, GRID); break;     \
-    default: STP_QK_I(KERNEL, T, 32, GRID); break;     \
-  }
-#define STP_QK_I(KERNEL, T, G, GRID)                           \
-  do {                                                         \
-    if (desc->interleaved)                                     \
-      KERNEL<T, G, true><<<GRID, kQkThreads, 0, s>>>(p);       \
-    else                                                       \
-      KERNEL<T, G, false><<<GRID, kQkThreads, 0, s>>>(p);      \
+#define STP_QK_T(KERNEL, G, GRID, RING)                                                            \
+  do {                                                                                             \
+    if (desc->dtype == STP_BF16 && desc->interleaved)                                              \
+      STP_QK_RUN((KERNEL<__nv_bfloat16, G, true>), GRID, RING(__nv_bfloat16));                     \
+    else if (desc->dtype == STP_BF16)                                                              \
+      STP_QK_RUN((KERNEL<__nv_bfloat16, G, false>), GRID, RING(__nv_bfloat16));                    \
+    else if (desc->interleaved)                                                                    \
+      STP_QK_RUN((KERNEL<float, G, true>), GRID, RING(float));                                     \
+    else                                                                                           \
+      STP_QK_RUN((KERNEL<float, G, false>), GRID, RING(float));                                    \
   } while (0)
+#define STP_QK_RUN(K, GRID, SMEM)                                                                  \
+  do {                                                                                             \
+    static const cudaError_t allowed =                                                             \
+        cudaFuncSetAttribute((const void*)K, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);   \
+    if (allowed != cudaSuccess) return fail(STP_ECUDA, "q/k norm: %s", cudaGetErrorString(allowed)); \
+    K<<<GRID, kQkThreads, SMEM, s>>>(p);                                                           \
+  } while (0)
+#define STP_QK_FWD_RING(T) (ring_bytes<T>(2, fwd_depth<T>()))
+#define STP_QK_BWD_RING(T) (ring_bytes<T>(4, kQkBwdDepth))
 
 int heads_per_pass(int head_dim) {
   int g = 1;
   while (g < head_dim / 16) g <<= 1;
   return 32 / g;
+}
+
+// Blocks for `units` passes: a pass per warp, up to `most`.
+int64_t blocks_of(int64_t units, int64_t most) {
+  const int64_t n = (units + kQkThreads / 32 - 1) / (kQkThreads / 32);
+  return n < most ? n : most;
 }
 
 }  // namespace
@@ -437,7 +583,7 @@ extern "C" stp_status stp_qk_norm_rope_workspace_size(const stp_qk_desc* desc, s
   stp_status st = check_qk(desc);
   if (st) return st;
   if (!ws_bytes) return fail(STP_EINVAL, "stp_qk_norm_rope_workspace_size: NULL output");
-  *ws_bytes = align256((size_t)kQkBwdBlocks * desc->head_dim * 4);
+  *ws_bytes = align256((size_t)kQkBwdGrid * desc->head_dim * 4);
   return STP_OK;
 }
 
@@ -463,18 +609,15 @@ extern "C" stp_status stp_qk_norm_rope_fwd(const stp_qk_desc* desc, const void* 
   p.pos = d_position_ids;
   p.q_out = q_out;
   p.k_out = k_out;
-  const int H = p.Hq + p.Hkv, pass = heads_per_pass(p.D) * 2;
-  const int64_t passes = (H + pass - 1) / pass;
-  // A token's angles are computed once per work item: one item for all heads
-  // of a token, unless that leaves most of the GPU's warps without work.
-  int64_t parts = p.N >= 4096 ? 1 : (4096 + p.N - 1) / p.N;
-  parts = parts < passes ? parts : passes;
-  p.hp = (int)((passes + parts - 1) / parts) * pass;
-  p.parts = (H + p.hp - 1) / p.hp;
-  const int64_t blocks = ((int64_t)p.N * p.parts + kQkThreads / 32 - 1) / (kQkThreads / 32);
-  const unsigned grid = (unsigned)(blocks < 152 * 8 ? blocks : 152 * 8);
+  const int per = heads_per_pass(p.D);
+  const int64_t units = (int64_t)p.N * ((p.Hq + per - 1) / per + (p.Hkv + per - 1) / per);
+  // With tokens enough, one per warp, so that the blocks in work read and write
+  // one moving stretch of memory (57 us of 16384 tokens; equal shares of the whole for
+  // as many warps as are resident 65); with fewer, equal shares.
+  const int64_t token_per_warp = ((int64_t)p.N + kQkThreads / 32 - 1) / (kQkThreads / 32);
+  p.blocks = (int)blocks_of(units, token_per_warp > 152 * kQkFwdBlocks ? token_per_warp : 152 * kQkFwdBlocks);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  STP_QK_LAUNCH(qk_fwd_kernel, grid);
+  STP_QK_LAUNCH(qk_fwd_kernel, (unsigned)p.blocks, STP_QK_FWD_RING);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_qk_norm_rope_fwd: %s", cudaGetErrorString(e));
   return STP_OK;
@@ -514,19 +657,15 @@ extern "C" stp_status stp_qk_norm_rope_bwd(const stp_qk_desc* desc, const void* 
   p.dq = d_q;
   p.dk = d_k;
   p.part = static_cast<float*>(d_ws);
-  const int H = p.Hq + p.Hkv, pass = heads_per_pass(p.D);
-  int64_t parts = p.N >= 4096 ? 1 : (4096 + p.N - 1) / p.N;
-  p.hp = (int)((((H + pass - 1) / pass) + parts - 1) / parts) * pass;
-  const int64_t pq = (p.Hq + p.hp - 1) / p.hp, pk = (p.Hkv + p.hp - 1) / p.hp;
-  const int64_t need_q = (p.N * pq + kQkThreads / 32 - 1) / (kQkThreads / 32);
-  const int64_t need_k = (p.N * pk + kQkThreads / 32 - 1) / (kQkThreads / 32);
-  // blocks in proportion to the heads, at most kQkBwdBlocks and one at least
-  int64_t bq = (int64_t)kQkBwdBlocks * p.Hq / H;
-  bq = bq < 1 ? 1 : bq > kQkBwdBlocks - 1 ? kQkBwdBlocks - 1 : bq;
-  int64_t bk = kQkBwdBlocks - bq;
-  p.blocks_q = (int)(bq < need_q ? bq : need_q);
-  p.blocks = p.blocks_q + (int)(bk < need_k ? bk : need_k);
-  STP_QK_LAUNCH(qk_bwd_kernel, (unsigned)p.blocks);
+  const int per = heads_per_pass(p.D);
+  const int64_t nq = (p.Hq + per - 1) / per, nk = (p.Hkv + per - 1) / per;
+  // queries and keys get blocks by their passes, half a pass more for the
+  // angles of a token, and one at least
+  int64_t bq = (kQkBwdGrid * (2 * nq + 1) + nq + nk + 1) / (2 * (nq + nk + 1));
+  bq = bq < 1 ? 1 : bq > kQkBwdGrid - 1 ? kQkBwdGrid - 1 : bq;
+  p.blocks_q = (int)blocks_of(p.N * nq, bq);
+  p.blocks = p.blocks_q + (int)blocks_of(p.N * nk, kQkBwdGrid - bq);
+  STP_QK_LAUNCH(qk_bwd_kernel, (unsigned)p.blocks, STP_QK_BWD_RING);
   qk_dw_kernel<<<dim3((unsigned)((p.D + 31) / 32), 2), 256, 0, s>>>(p.part, p.D, p.blocks_q, p.blocks, dw_q, dw_k);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_qk_norm_rope_bwd: %s", cudaGetErrorString(e));
