@@ -14,7 +14,8 @@
 //               per query row (= TMEM lane); the predicate
 //               j <= i && subtree_end[j] >= i is applied on PARTIAL tiles only
 //               (WIN: and position[i] < lim[j], on the 32 x 32 blocks of the
-//               tile that are PARTIAL; EMPTY blocks are skipped, P = 0);
+//               tile that are PARTIAL; EMPTY blocks are skipped, P = 0; warps
+//               10 and 11 make the bits ahead, for both heads);
 //               online softmax in base 2; O is rescaled in TMEM only when the
 //               running max grows by more than 2^8 (exact: numerator and
 //               denominator keep the same reference max).
@@ -106,25 +107,14 @@ struct FwdParams {
   uint32_t* err;
 };
 
-// Visibility of 32 keys to query i of a windowed row, but for j <= i: bit c is
-// set iff subtree_end >= i and pos_i < lim of key c (both signs negative).
-__device__ __forceinline__ uint32_t window_bits(const int4* se4, const int4* lim4, int i, int pos_i) {
-  uint32_t bits = 0;
-  auto put = [&](int se, int lim) { bits = __funnelshift_l((uint32_t)((i - 1 - se) & (pos_i - lim)), bits, 1); };
-#pragma unroll
-  for (int c = 7; c >= 0; --c) {
-    const int4 s = __ldg(se4 + c), l = __ldg(lim4 + c);
-    put(s.w, l.w);
-    put(s.z, l.z);
-    put(s.y, l.y);
-    put(s.x, l.x);
-  }
-  return bits;
-}
+// WIN: the visibility words of kVisSlots list entries, [entry % kVisSlots][32 keys][query].
+constexpr int kVisSlots = 4;
+constexpr int kVisBytes = kVisSlots * 4 * 128 * 4;
 
 enum {
   B_Q = 0, B_KF = 1, B_VF = 3, B_KE = 5, B_VE = 7, B_SF = 9, B_PF = 11, B_OD = 13, B_DRAIN = 15,
-  B_COUNT = 16
+  B_COUNT = 16,
+  B_MF = 16, B_ME = B_MF + kVisSlots, B_COUNT_WIN = B_ME + kVisSlots   // WIN: masks full, empty
 };
 
 // Forward: 12 warps = three full warpgroups; registers move from the control
@@ -141,11 +131,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap tv, const FwdParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_COUNT);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + (WIN ? (int)B_COUNT_WIN : (int)B_COUNT));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const uint32_t raw = smem_u32(smem_raw) + kSmallBytes;
+  constexpr int kSmall = kSmallBytes + (WIN ? kVisBytes : 0);
+  uint32_t* vis_s = reinterpret_cast<uint32_t*>(smem_raw + kSmallBytes);   // WIN
+  const uint32_t raw = smem_u32(smem_raw) + kSmall;
   const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
-  uint8_t* big = smem_raw + kSmallBytes + pad;
+  uint8_t* big = smem_raw + kSmall + pad;
   const uint32_t big_s = raw + pad;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -173,8 +165,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars[B_OD + s], 1);
     }
     mbar_init(&bars[B_DRAIN], 1);
+    if (WIN)
+      for (int m = 0; m < kVisSlots; ++m) {
+        mbar_init(&bars[B_MF + m], 2);        // the two mask warps
+        mbar_init(&bars[B_ME + m], 4 * nh);   // the softmax warps that work
+      }
     *abort_flag = 0;
-    if (pad + kSmallBytes + kFwdBigBytes > kSmemLimit || cnt <= 0 || cnt > p.NT) {
+    if (pad + kSmall + kFwdBigBytes > kSmemLimit || cnt <= 0 || cnt > p.NT) {
       *abort_flag = 1;
       atomicOr(p.err, cnt <= 0 || cnt > p.NT ? kErrBadList : kErrTmem);
     }
@@ -317,6 +314,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_drain(&bars[B_DRAIN], 0);
     }
     __syncwarp();
+  } else if (WIN && warp >= 10) {
+    // ------------------------------------------------------------ masks
+    // Two blocks of queries per warp, a query of each per lane; bit c of a word
+    // of a PARTIAL block is set iff subtree_end >= i and pos_i < lim of key c
+    // (both differences negative) and, on the diagonal, j <= i.  Both heads'
+    // softmax read them, so that none is made between a tile's scores and P.
+    const int qb = (warp - 10) * 2, i0 = qt * 128 + 32 * qb + lane;
+    const int pos0 = p.pos[(size_t)row0 + i0], pos1 = p.pos[(size_t)row0 + i0 + 32];
+    const uint32_t* words = p.word + ((size_t)r * p.NT + qt) * p.NT;
+    const uint32_t tri = (2u << lane) - 1;
+    for (int e = 0; run && e < cnt; ++e) {
+      const int kt = list[e] >> 1, slot = e % kVisSlots;
+      if (kt < 0 || kt > qt) break;   // the producer reports it
+      const uint32_t word = (list[e] & 1) ? words[kt] >> (8 * qb) : 0xaaaau;
+      if (e >= kVisSlots &&
+          !__all_sync(0xffffffffu, mbar_wait(&bars[B_ME + slot], (e / kVisSlots - 1) & 1, abort_flag, p.err)))
+        break;
+#pragma unroll 1
+      for (int kb = 0; kb < 4; ++kb) {
+        const bool part0 = ((word >> (2 * kb)) & 3) == kPartial, part1 = ((word >> (8 + 2 * kb)) & 3) == kPartial;
+        if (!part0 && !part1) continue;
+        const size_t k0 = (size_t)row0 + kt * 128 + 32 * kb;
+        const int4* se4 = reinterpret_cast<const int4*>(p.se + k0);
+        const int4* lim4 = reinterpret_cast<const int4*>(p.lim + k0);
+        uint32_t b0 = 0, b1 = 0;
+        auto put = [&](int se, int lim) {
+          b0 = __funnelshift_l((uint32_t)((i0 - 1 - se) & (pos0 - lim)), b0, 1);
+          b1 = __funnelshift_l((uint32_t)((i0 + 31 - se) & (pos1 - lim)), b1, 1);
+        };
+#pragma unroll
+        for (int h = 3; h >= 0; --h) {
+          const int4 sa = __ldg(se4 + 2 * h), sb = __ldg(se4 + 2 * h + 1);
+          const int4 la = __ldg(lim4 + 2 * h), lb = __ldg(lim4 + 2 * h + 1);
+          put(sb.w, lb.w);
+          put(sb.z, lb.z);
+          put(sb.y, lb.y);
+          put(sb.x, lb.x);
+          put(sa.w, la.w);
+          put(sa.z, la.z);
+          put(sa.y, la.y);
+          put(sa.x, la.x);
+        }
+        if (kt == qt && kb == qb) b0 &= tri;
+        if (kt == qt && kb == qb + 1) b1 &= tri;
+        uint32_t* out = vis_s + (slot * 4 + kb) * 128 + 32 * qb + lane;
+        out[0] = b0;
+        out[32] = b1;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[B_MF + slot]);
+    }
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax
     regs_inc<kRegsMath>();
@@ -327,7 +375,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_addr = tmem + lane_base + hs * 128;
     const uint32_t o_addr = tmem + lane_base + 256 + hs * 128;
     const int32_t* se_row = p.se + (size_t)row0;
-    const int pos_i = WIN ? p.pos[(size_t)row0 + i] : 0;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = run && hs < nh;
     for (int e = 0; ok && e < cnt; ++e) {
@@ -338,16 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
       uint32_t cls = 0xaa;   // WIN: two bits per 32 keys, the classes of the warp's blocks
       if (WIN) {
-        if (part) {
-          cls = (p.word[((size_t)r * p.NT + qt) * p.NT + kt] >> (8 * (warp & 3))) & 0xff;
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            if (((cls >> (2 * w)) & 3) == kPartial) {
-              vis[w] = window_bits(reinterpret_cast<const int4*>(se_row + k0) + 8 * w,
-                                   reinterpret_cast<const int4*>(p.lim + (size_t)row0 + k0) + 8 * w, i, pos_i);
-              if (kt == qt && w == (warp & 3)) vis[w] &= (2u << lane) - 1;   // j <= i
-            }
-        }
+        if (part) cls = (p.word[((size_t)r * p.NT + qt) * p.NT + kt] >> (8 * (warp & 3))) & 0xff;
       } else if (part) {
         const int4* se4 = reinterpret_cast<const int4*>(se_row + k0);
 #pragma unroll
@@ -376,7 +414,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int w = 0; w < 4; ++w)
         if (there(w)) tmem_ld32(s_addr + 32 * w, u + 32 * w);
+      if (WIN) {
+        const int slot = e % kVisSlots;
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars[B_MF + slot], (e / kVisSlots) & 1, abort_flag, p.err))) ok = false;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          if (((cls >> (2 * w)) & 3) == kPartial) vis[w] = vis_s[(slot * 4 + w) * 128 + row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_ME + slot]);
+      }
       tmem_ld_wait();
+      if (WIN && !ok) break;
       if (WIN) {
 #pragma unroll
         for (int w = 0; w < 4; ++w)
