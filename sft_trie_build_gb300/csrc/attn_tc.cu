@@ -896,20 +896,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t s_col = lane_base + half * 64, dp_col = lane_base + 128 + half * 64;
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
     bool ok = run;
+    uint32_t vis[2] = {~0u, ~0u};
     int ent = run ? list[0] : 0;
     for (int j = 0; ok && j < n_it; ++j) {
       const int qt = ent >> 1, part = ent & 1;
       if (j + 1 < n_it) ent = list[(j + 1) / p.G];
       const int q0 = qt * 128 + half * 64;
       // WIN: which of the 64 queries see the key, by the classes of the warp's
-      // two blocks: jk <= i <= subtree_end, pos_i < lim_j in a partial one
-      uint32_t vis[2] = {~0u, ~0u};
-      if (WIN && part) {
+      // two blocks: jk <= i <= subtree_end, pos_i < lim_j in a partial one; the
+      // same for all heads of the group
+      if (WIN && part && j % p.G == 0) {
         const uint32_t word = p.word[((size_t)r * p.NT + qt) * p.NT + kt] >> (2 * (warp & 3));
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int cls = (word >> (8 * (2 * half + w))) & 3;
-          if (cls == kEmpty) vis[w] = 0;
+          vis[w] = cls == kEmpty ? 0u : ~0u;
           if (cls == kPartial) {
             const int4* pos4 = reinterpret_cast<const int4*>(p.pos + (size_t)row0 + q0 + 32 * w);
             uint32_t bits = 0;

@@ -44,25 +44,44 @@ struct RowBlocks {
   int window, n_sink;
 };
 
-__host__ __device__ inline int block_class(const RowBlocks& b, int qb, int kb) {
-  const int q0 = qb * kBlock, q1 = q0 + kBlock - 1;
-  if (kb > qb) return kEmpty;
-  if (kb == qb) return kPartial;
-  const int reach = b.smax[kb];
-  if (reach < q0) return kEmpty;
-  const bool near = b.pmin[kb] < b.n_sink;   // some key is a first token
-  if (!near && b.qmin[reach < q1 ? reach : q1] - b.pmax[kb] >= b.window) return kEmpty;
-  if (b.smin[kb] >= q1 && (b.pmax[kb] < b.n_sink || b.pmax[qb] - b.pmin[kb] < b.window)) return kFull;
-  return kPartial;
-}
+// Four neighbouring blocks' values, read at once (16-byte aligned).
+struct alignas(16) Four {
+  int32_t v[4];
+};
+__host__ __device__ inline Four four(const int32_t* p) { return *reinterpret_cast<const Four*>(p); }
 
 // The classes of the sixteen blocks of tile (qt, kt).
 __host__ __device__ inline uint32_t tile_word(const RowBlocks& b, int qt, int kt) {
-  uint32_t w = 0;
-  if (kt > qt) return w;
-  for (int q = 0; q < kPer; ++q)
-    for (int k = 0; k < kPer; ++k) w |= (uint32_t)block_class(b, qt * kPer + q, kt * kPer + k) << (2 * (kPer * q + k));
-  return w;
+  if (kt > qt) return 0;
+  const Four smax = four(b.smax + kPer * kt);
+  const int q_first = qt * kTile;
+  if (kt < qt && smax.v[0] < q_first && smax.v[1] < q_first && smax.v[2] < q_first && smax.v[3] < q_first) return 0;
+  const Four smin = four(b.smin + kPer * kt), kmin = four(b.pmin + kPer * kt), kmax = four(b.pmax + kPer * kt);
+  const Four qmin = four(b.pmin + kPer * qt), qmax = four(b.pmax + kPer * qt);
+  uint32_t word = 0;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int q0 = q_first + q * kBlock, q1 = q0 + kBlock - 1;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      uint32_t c = kPartial;
+      if (kt == qt && k >= q) {
+        if (k > q) c = kEmpty;
+      } else {
+        const int reach = smax.v[k];
+        const bool first = kmin.v[k] < b.n_sink;   // some key is a first token
+        if (reach < q0) {
+          c = kEmpty;
+        } else if (!first && (reach < q1 ? b.qmin[reach] : qmin.v[q]) - kmax.v[k] >= b.window) {
+          c = kEmpty;
+        } else if (smin.v[k] >= q1 && (kmax.v[k] < b.n_sink || qmax.v[q] - kmin.v[k] < b.window)) {
+          c = kFull;
+        }
+      }
+      word |= c << (2 * (kPer * q + k));
+    }
+  }
+  return word;
 }
 
 struct WindowArgs {
@@ -155,10 +174,12 @@ __device__ void number_pairs(const WindowArgs& a, int r, int* s_warp) {
     a.row_base[r] = s_base;
   }
   __syncthreads();   // off[] too: written and read by this block alone
-  for (int kt = w; kt < a.NT; kt += 4) {
+  // eight lanes a key tile: most lists are short, and each entry takes three
+  // dependent reads
+  for (int kt = t >> 3; kt < a.NT; kt += kTile / 8) {
     const size_t at = ((size_t)r * a.NT + kt) * a.NT;
     const int n = __ldcg(a.csc_cnt + (size_t)r * a.NT + kt);
-    for (int e = lane; e < n; e += 32) {
+    for (int e = t & 7; e < n; e += 8) {
       const int qt = __ldcg(a.csc + at + e) >> 1;
       a.csc_pair[at + e] = s_base + off[qt] + __ldcg(a.crank + ((size_t)r * a.NT + qt) * a.NT + kt);
     }
@@ -227,8 +248,10 @@ extern "C" stp_status stp_count_window_tile_pairs(const int32_t* subtree_end, co
   const int NB = row_len / kBlock, NT = row_len / kTile;
   int64_t total = 0;
   try {
-    std::vector<int32_t> smin(NB), smax(NB), pmin(NB), pmax(NB), qmin(row_len);
-    const RowBlocks rb = {smin.data(), smax.data(), pmin.data(), pmax.data(), qmin.data(), clip_window(window), n_sink};
+    std::vector<Four> tiles(4 * (size_t)NT);   // four arrays of NB values
+    int32_t *smin = tiles[0].v, *smax = smin + NB, *pmin = smax + NB, *pmax = pmin + NB;
+    std::vector<int32_t> qmin(row_len);
+    const RowBlocks rb = {smin, smax, pmin, pmax, qmin.data(), clip_window(window), n_sink};
     for (int64_t r = 0; r < n_rows; ++r) {
       const int32_t *se = subtree_end + r * row_len, *pos = position_ids + r * row_len;
       for (int32_t j = 0; j < row_len; ++j) {
