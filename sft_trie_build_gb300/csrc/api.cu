@@ -78,6 +78,8 @@ static stp_status set_window(const char* name, const Window* w, const stp_attn_d
                              AttnArgs& a) {
   if (!w) return STP_OK;
   if (!w->pos) return fail(STP_EINVAL, "%s: NULL device pointer", name);
+  if ((int64_t)d->n_rows * d->row_len > 0x7fffffff)
+    return fail(STP_EUNSUPPORTED, "%s: more than 2^31 - 1 tokens", name);
   if (misaligned(w->pos, 16)) return fail(STP_EINVAL, "%s: position_ids must be 16-byte aligned", name);
   a.pos = w->pos;
   const TileMeta m = tile_meta_layout(d->n_rows, d->row_len / kTile);

@@ -294,6 +294,8 @@ extern "C" stp_status stp_classify_window(const stp_attn_desc* desc, int32_t win
   if ((reinterpret_cast<uintptr_t>(d_tile_meta) & 255) ||
       (reinterpret_cast<uintptr_t>(d_subtree_end) | reinterpret_cast<uintptr_t>(d_position_ids)) & 15)
     return fail(STP_EINVAL, "stp_classify_window: tile_meta must be 256-byte, the row arrays 16-byte aligned");
+  if ((int64_t)desc->n_rows * desc->row_len > 0x7fffffff)
+    return fail(STP_EUNSUPPORTED, "stp_classify_window: more than 2^31 - 1 tokens");
   if (desc->n_rows == 0) return STP_OK;
   const int NT = desc->row_len / kTile;
   const TileMeta m = tile_meta_layout(desc->n_rows, NT);
