@@ -222,16 +222,27 @@ def _dptr(t):
     return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
-_current_stream = None
+_raw_stream = None
+
+
+def _current_stream():
+    """The current stream's handle, without the Stream object around it where torch has a call for that."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.init()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            device = torch._C._cuda_getDevice
+            _raw_stream = lambda: raw(device())  # noqa: E731
+    return _raw_stream()
 
 
 def _stream(stream):
     if stream is None:
-        global _current_stream
-        if _current_stream is None:
-            import torch
-            _current_stream = torch.cuda.current_stream
-        return _current_stream().cuda_stream
+        return _current_stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
