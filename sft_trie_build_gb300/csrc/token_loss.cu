@@ -11,8 +11,8 @@
 // Bound by memory: forward one read of the logits, backward one read and one
 // write, the step of both one read and one write too, its second pass out of
 // L2.  C blocks share a row (C = 1 when there are rows enough for every SM):
-// they are a thread-block cluster, and their sums meet in the shared memory of
-// its first block, so one launch does a row whatever C is.  A thread streams
+// they are a thread-block cluster and send their sums into each other's shared
+// memory, so one launch does a row whatever C is.  A thread streams
 // 16-byte pieces through its own ring of slots in shared memory (asynchronous
 // copies, no barrier), which keeps 192 KB on the way per SM while other blocks
 // of the SM are at their row's end.  A row may start at any address of its
@@ -230,11 +230,10 @@ __device__ __forceinline__ Acc block_sum(Acc a, Acc* red, float sl2) {
   return a;
 }
 
-// The row's sums, from those that each of its blocks has left in its `mine`.
-__device__ __forceinline__ Acc cluster_sum(Acc* mine, int C, float sl2) {
-  cg::cluster_group cl = cg::this_cluster();
-  Acc a = *cl.map_shared_rank(mine, 0);
-  for (int r = 1; r < C; ++r) a = merge(a, *cl.map_shared_rank(mine, r), sl2);
+// The row's sums, from those that its blocks have sent (the same in each).
+__device__ __forceinline__ Acc merge_all(const Acc* sums, int C, float sl2) {
+  Acc a = sums[0];
+  for (int r = 1; r < C; ++r) a = merge(a, sums[r], sl2);
   return a;
 }
 
@@ -320,6 +319,7 @@ struct TopShared {
   __align__(16) uint64_t group[kGroups];
   __align__(16) uint64_t cand[kCand];   // first the threads' maxima, then the candidates
   uint64_t top[kMaxTop];
+  __align__(16) uint64_t lists[kMaxSplit * kMaxTop];   // first block: every block's K largest
   uint64_t bound;
   int n_strips, n_cand;
   uint16_t strip[kRowThreads];
@@ -361,14 +361,16 @@ __device__ __forceinline__ int rank_of(const uint64_t* keys, int n, uint64_t min
 // go to a warp each; the pieces of shorter ones are dealt out over the block,
 // which reads them all at once (strips of 10 pieces, 20 tokens: 12.4 us a row
 // of eight blocks against 13.4; of 75 pieces it costs, 8192 rows 426 against 408).
+// `kept`: the ring of the pass, where it still holds every piece of the block.
 template <typename T, typename F>
-__device__ __forceinline__ void each_candidate(const T* row, const Part& p, const TopShared& sh, float floor_v, F f) {
+__device__ __forceinline__ void each_candidate(const T* row, const Part& p, const uint4* kept, const TopShared& sh,
+                                               float floor_v, F f) {
   constexpr int E = Piece<T>::E;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint4* body = reinterpret_cast<const uint4*>(row + p.head);
-  auto look = [&](int at) {
+  auto look = [&](int at, const uint4* src) {
     float z[E];
-    Piece<T>::get(at < p.b1 ? body[at] : Piece<T>::lowest(), z);
+    Piece<T>::get(at < p.b1 ? *src : Piece<T>::lowest(), z);
     bool any = false;
 #pragma unroll
     for (int e = 0; e < E; ++e) any = any || (z[e] >= floor_v && z[e] > -INFINITY);
@@ -380,12 +382,16 @@ __device__ __forceinline__ void each_candidate(const T* row, const Part& p, cons
   const int len = (p.b1 - p.b0 + kRowThreads - 1) / kRowThreads;   // pieces of a strip, the last one perhaps outside
   if (len >= 32) {
     for (int i = warp; i < sh.n_strips; i += kRowWarps)
-      for (int j = 0; j < len; j += 32) look(p.b0 + sh.strip[i] + (j + lane) * kRowThreads);
+      for (int j = 0; j < len; j += 32) {
+        const int at = p.b0 + sh.strip[i] + (j + lane) * kRowThreads;
+        look(at, body + at);
+      }
   } else {
     const int total = sh.n_strips * len;
     for (int i0 = warp * 32; i0 < total; i0 += kRowThreads) {
       const int i = i0 + lane;
-      look(i < total ? p.b0 + sh.strip[i / len] + (i % len) * kRowThreads : p.b1);
+      const int in = i < total ? sh.strip[i / len] + (i % len) * kRowThreads : p.b1 - p.b0;   // piece of the block
+      look(p.b0 + in, kept ? kept + in : body + p.b0 + in);
     }
   }
   if (__any_sync(0xffffffffu, p.extra >= 0)) {
@@ -396,7 +402,7 @@ __device__ __forceinline__ void each_candidate(const T* row, const Part& p, cons
 
 // The block's K largest tokens into sh.top, descending, 0 where none is left.
 template <typename T>
-__device__ void block_top(const T* row, const Part& p, float best, int round, int K, TopShared& sh) {
+__device__ void block_top(const T* row, const Part& p, const uint4* kept, float best, int round, int K, TopShared& sh) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const uint64_t mine = best > -INFINITY ? key_of(best, (uint32_t)round) : 0;
   // groups of threads kGroups apart, so that a short row still fills them
@@ -422,7 +428,7 @@ __device__ void block_top(const T* row, const Part& p, float best, int round, in
   if (in) sh.strip[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)t;
   __syncthreads();
   const float floor_v = bound ? value_of(bound) : -INFINITY;
-  each_candidate(row, p, sh, floor_v, [&](uint64_t key) {
+  each_candidate(row, p, kept, sh, floor_v, [&](uint64_t key) {
     if (key) {
       const int i = atomicAdd(&sh.n_cand, 1);
       if (i < kCand) sh.cand[i] = key;
@@ -434,7 +440,7 @@ __device__ void block_top(const T* row, const Part& p, float best, int round, in
     // many values that tie or lie in few strips: a list of K per warp instead
     __syncthreads();
     uint64_t held = lane < K ? 0 : ~0ull, least = 0;
-    each_candidate(row, p, sh, floor_v, [&](uint64_t key) { enter(held, least, key > least, key); });
+    each_candidate(row, p, kept, sh, floor_v, [&](uint64_t key) { enter(held, least, key > least, key); });
     if (lane < K) sh.cand[warp * K + lane] = held;
     n = kRowWarps * K;
     __syncthreads();
@@ -447,26 +453,21 @@ __device__ void block_top(const T* row, const Part& p, float best, int round, in
   __syncthreads();
 }
 
-// The K largest of the C blocks' lists, each descending, into sh.top of the
-// first block: a key's place is its place in its own list and, by halving,
-// those in the others.
+// The K largest of the C blocks' lists, each descending, into sh.top: a key's
+// place is its place in its own list and, by halving, those in the others.
 __device__ __forceinline__ void merge_top(TopShared& sh, int C, int K) {
-  cg::cluster_group cl = cg::this_cluster();
   const int t = threadIdx.x, mine = t / K, at = t % K;
-  uint64_t key = 0;
-  if (t < C * K) {
-    key = cl.map_shared_rank(&sh, mine)->top[at];
-    sh.cand[t] = key;
-  }
+  const uint64_t key = t < C * K ? sh.lists[t] : 0;
+  if (t < K) sh.top[t] = 0;
   __syncthreads();
   if (key) {
-    // how many keys of each list are larger, by halving: the lists in step, so
-    // that the reads of a step are on their way together
+    // how many keys of each list are larger: the lists in step, so that the
+    // reads of a step are on their way together
     int lo[kMaxSplit] = {}, rank = 0;
     for (int step = kMaxTop; step > 0; step >>= 1)
 #pragma unroll
       for (int l = 0; l < kMaxSplit; ++l)
-        if (l < C && lo[l] + step <= K && sh.cand[l * K + lo[l] + step - 1] > key) lo[l] += step;
+        if (l < C && lo[l] + step <= K && sh.lists[l * K + lo[l] + step - 1] > key) lo[l] += step;
 #pragma unroll
     for (int l = 0; l < kMaxSplit; ++l) rank += l == mine ? at : lo[l];
     if (rank < K) sh.top[rank] = key;
@@ -511,7 +512,7 @@ __device__ __forceinline__ void check_below(int64_t n, int V, uint32_t* err, F v
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kRowThreads, kPassBlocks) stats_fwd_kernel(const StatsParams p) {
   __shared__ Acc red[kRowWarps];
-  __shared__ Acc mine;
+  __shared__ Acc sums[kMaxSplit];   // of the row's blocks
   __shared__ TopShared sh;
   extern __shared__ uint4 buffer[];
   const int C = p.C, n = (int)(blockIdx.x / C), rank = (int)(blockIdx.x % C), t = threadIdx.x;
@@ -534,6 +535,7 @@ __global__ void __launch_bounds__(kRowThreads, kPassBlocks) stats_fwd_kernel(con
   const Part part = part_of(row, p.V, rank, C);
   const auto ring = ring_of<kPassRounds>(buffer, row, part);
   ring.start(part.b0 + t);
+  if (C > 1) cg::this_cluster().barrier_arrive();   // this block runs: others may write to it
   float zt = 0.f;
   if (rank == 0 && t == 0) {
     zt = target < p.V ? to_f(row[target]) : NAN;
@@ -542,16 +544,21 @@ __global__ void __launch_bounds__(kRowThreads, kPassBlocks) stats_fwd_kernel(con
   float best = -INFINITY;
   int round = 0;
   Acc a = block_sum(pass<T, true, TOP>(row, part, ring, p.sl2, best, round), red, p.sl2);
-  if (TOP) block_top(row, part, best, round, p.K, sh);
+  if (TOP) {
+    // piece j of a thread's strip lies in slot j of its ring until the ring comes round
+    const bool all = part.b1 - part.b0 <= kPassRounds * kFlight * kRowThreads;
+    block_top(row, part, all ? buffer : nullptr, best, round, p.K, sh);
+  }
   if (C > 1) {
+    // everything goes to the first block, which then reads its own memory
     cg::cluster_group cl = cg::this_cluster();
-    if (t == 0) mine = a;
+    cl.barrier_wait();
+    if (t == 0) *cl.map_shared_rank(sums + rank, 0) = a;
+    if (TOP && t < p.K) *cl.map_shared_rank(sh.lists + rank * p.K + t, 0) = sh.top[t];
     cl.sync();
-    if (rank == 0) {
-      a = cluster_sum(&mine, C, p.sl2);
-      if (TOP) merge_top(sh, C, p.K);
-    }
-    cl.barrier_arrive();   // the first block has read the others' shared memory
+    if (rank > 0) return;
+    a = merge_all(sums, C, p.sl2);
+    if (TOP) merge_top(sh, C, p.K);
   }
   if (rank == 0) {
     const float ls = log_sum(a);
@@ -567,7 +574,6 @@ __global__ void __launch_bounds__(kRowThreads, kPassBlocks) stats_fwd_kernel(con
       p.top_lp[(int64_t)n * p.K + t] = key ? fmaf(value_of(key) - a.m, p.scale, -ls) : -INFINITY;
     }
   }
-  if (C > 1) cg::this_cluster().barrier_wait();
 }
 
 // Writes f(z, id) over the block's part of a row, whose first rounds are on
@@ -696,7 +702,7 @@ __device__ __forceinline__ float block_add(float v, float* red) {
 template <typename T, bool LSE, bool GRAD>
 __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPassBlocks) distill_kernel(const DistillParams p) {
   __shared__ Acc red[kRowWarps];
-  __shared__ Acc mine;
+  __shared__ Acc sums[kMaxSplit];   // of the row's blocks
   __shared__ TeacherShared ts;
   const int C = p.C, n = (int)(blockIdx.x / C), rank = (int)(blockIdx.x % C), t = threadIdx.x;
   const T* row = static_cast<const T*>(p.z) + (int64_t)n * p.stride;
@@ -728,6 +734,7 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
   const Part part = part_of(row, p.V, rank, C);
   const auto ring = ring_of<LSE && GRAD ? kStepRounds : kPassRounds>(buffer, row, part);
   ring.start(part.b0 + t);
+  if (LSE && C > 1) cg::this_cluster().barrier_arrive();   // this block runs: others may write to it
   const float zk = id >= 0 ? to_f(row[id]) : 0.f;
   const float top = block_max(a, ts.red);
   const float ek = id >= 0 ? ex2(a - top) : 0.f;
@@ -746,10 +753,10 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
     s = block_sum(s, red, p.sl2);
     if (C > 1) {
       cg::cluster_group cl = cg::this_cluster();
-      if (t == 0) mine = s;
+      cl.barrier_wait();
+      if (t < C) *cl.map_shared_rank(sums + rank, t) = s;
       cl.sync();
-      s = cluster_sum(&mine, C, p.sl2);
-      cl.barrier_arrive();   // the others' sums have been read
+      s = merge_all(sums, C, p.sl2);
     }
     const float ls = log_sum(s);
     lse = fmaf(s.m, p.scale, ls);
@@ -785,7 +792,6 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
       if (own && first) put(out + id, g * (ex2(fmaf(zk, scale, -lse) * kLog2eT) - qs));
     }
   }
-  if (LSE && C > 1) cg::this_cluster().barrier_wait();
 }
 
 // ------------------------------------------------------------------- host
