@@ -86,6 +86,7 @@ static stp_status set_window(const char* name, const Window* w, const stp_attn_d
   const char* base = static_cast<const char*>(tile_meta);
   a.lim = reinterpret_cast<const int32_t*>(base + m.lim);
   a.word = reinterpret_cast<const uint32_t*>(base + m.word);
+  a.crank = reinterpret_cast<const int32_t*>(base + m.crank);
   return STP_OK;
 }
 

@@ -617,6 +617,9 @@ struct BwdParams {
   const int32_t* pos;   // WIN only, as in FwdParams
   const int32_t* lim;
   const uint32_t* word;
+  const int32_t* csr_off;   // a pair's index, in place of csc_pair: row_base + csr_off + crank
+  const int32_t* row_base;
+  const int32_t* crank;
   const uint8_t* sbias; // [R][Hq][NT] bias tiles of the scores (-LSE / scale)
   const uint8_t* dbias; // [R][Hq][NT] bias tiles of dP (-Delta)
   uint8_t* ds;          // this launch's slot: [pair][slot_heads] dS^T tiles
@@ -862,9 +865,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     bool ok = run;
     for (int j = 0; ok && j < n_it; ++j) {
+      int pr_j = 0;
+      if (WIN) {
+        const int qt = list[j / p.G] >> 1;
+        if (qt < kt || qt >= p.NT) break;   // the producer reports it
+        const size_t at = (size_t)r * p.NT + qt;
+        pr_j = p.row_base[r] + p.csr_off[at] + p.crank[at * p.NT + kt];
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(&bars[C_DR], j & 1, abort_flag, p.err))) break;
       fence_after_sync();
-      const int pr_j = pairs[j / p.G];
+      if (!WIN) pr_j = pairs[j / p.G];
       uint32_t d0[32], d1[32];           // dS^T of query columns 0..63 and 64..127
       tmem_ld32(tmem + lane_base + 128 + 32, d0);
       tmem_ld32(tmem + lane_base + 192 + 32, d1);
@@ -1383,6 +1393,9 @@ cudaError_t tc_bwd(const AttnArgs& a, cudaStream_t s) {
   p.pos = a.pos;
   p.lim = a.lim;
   p.word = a.word;
+  p.csr_off = a.csr_off;
+  p.row_base = a.row_base;
+  p.crank = a.crank;
   p.sbias = static_cast<const uint8_t*>(a.sbias);
   p.dbias = static_cast<const uint8_t*>(a.dbias);
   p.dk = static_cast<__nv_bfloat16*>(a.dk);
