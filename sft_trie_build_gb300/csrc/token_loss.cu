@@ -509,13 +509,14 @@ __device__ __forceinline__ void check_below(int64_t n, int V, uint32_t* err, F v
   if (threadIdx.x == 0) *err = bad ? kErrBadList : 0;
 }
 
-template <typename T, bool TOP>
+// MANY: several blocks per row (C > 1).
+template <typename T, bool TOP, bool MANY>
 __global__ void __launch_bounds__(kRowThreads, kPassBlocks) stats_fwd_kernel(const StatsParams p) {
   __shared__ Acc red[kRowWarps];
   __shared__ Acc sums[kMaxSplit];   // of the row's blocks
   __shared__ TopShared sh;
   extern __shared__ uint4 buffer[];
-  const int C = p.C, n = (int)(blockIdx.x / C), rank = (int)(blockIdx.x % C), t = threadIdx.x;
+  const int C = MANY ? p.C : 1, n = (int)(blockIdx.x / C), rank = MANY ? (int)(blockIdx.x % C) : 0, t = threadIdx.x;
   if (n == p.N) {
     if (rank == 0) check_below(p.N, p.V, p.err, [&](int64_t i) { return p.target[i]; });
     return;
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(kRowThreads, kPassBlocks) stats_fwd_kernel(con
   const Part part = part_of(row, p.V, rank, C);
   const auto ring = ring_of<kPassRounds>(buffer, row, part);
   ring.start(part.b0 + t);
-  if (C > 1) cg::this_cluster().barrier_arrive();   // this block runs: others may write to it
+  if (MANY) cg::this_cluster().barrier_arrive();   // this block runs: others may write to it
   float zt = 0.f;
   if (rank == 0 && t == 0) {
     zt = target < p.V ? to_f(row[target]) : NAN;
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(kRowThreads, kPassBlocks) stats_fwd_kernel(con
     const bool all = part.b1 - part.b0 <= kPassRounds * kFlight * kRowThreads;
     block_top(row, part, all ? buffer : nullptr, best, round, p.K, sh);
   }
-  if (C > 1) {
+  if (MANY) {
     // everything goes to the first block, which then reads its own memory
     cg::cluster_group cl = cg::this_cluster();
     cl.barrier_wait();
@@ -846,8 +847,15 @@ int step_split_of(int64_t rows, int64_t row_bytes) {
 constexpr int64_t kCheckMost = 65536;
 
 template <typename T>
+const void* stats_fwd(bool top, bool many) {
+  return top ? (many ? (const void*)stats_fwd_kernel<T, true, true> : (const void*)stats_fwd_kernel<T, true, false>)
+             : (many ? (const void*)stats_fwd_kernel<T, false, true> : (const void*)stats_fwd_kernel<T, false, false>);
+}
+
+template <typename T>
 cudaError_t allow_rings_of() {
-  const void* pass[] = {(const void*)stats_fwd_kernel<T, false>, (const void*)stats_fwd_kernel<T, true>,
+  const void* pass[] = {stats_fwd<T>(false, false),        stats_fwd<T>(false, true),
+                        stats_fwd<T>(true, false),         stats_fwd<T>(true, true),
                         (const void*)stats_bwd_kernel<T>, (const void*)distill_kernel<T, true, false>,
                         (const void*)distill_kernel<T, false, true>};
   cudaError_t e = cudaFuncSetAttribute((const void*)distill_kernel<T, true, true>,
@@ -952,10 +960,7 @@ extern "C" stp_status stp_token_stats_fwd(const stp_stats_desc* desc, const void
     p.top_lp = top_logprob;
     p.err = static_cast<uint32_t*>(d_ws);
     p.C = split_of(p.N, row_bytes(p.V, desc->dtype));
-    const void* k = desc->dtype == STP_BF16
-                        ? (p.K ? (const void*)stats_fwd_kernel<__nv_bfloat16, true>
-                               : (const void*)stats_fwd_kernel<__nv_bfloat16, false>)
-                        : (p.K ? (const void*)stats_fwd_kernel<float, true> : (const void*)stats_fwd_kernel<float, false>);
+    const void* k = desc->dtype == STP_BF16 ? stats_fwd<__nv_bfloat16>(p.K > 0, p.C > 1) : stats_fwd<float>(p.K > 0, p.C > 1);
     e = launch(k, kPassRounds, p.N + p.check, p.C, &p, true, s);
   }
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_token_stats_fwd: %s", cudaGetErrorString(e));
