@@ -16,9 +16,13 @@ import numpy as np
 
 
 def _log_softmax(z: np.ndarray):
+    """(z - ln sum exp z, ln sum exp z); the difference to the maximum comes
+    first, so that a row of one huge value stays an even distribution."""
     mx = z.max()
-    lse = mx + np.log(np.exp(z - mx).sum()) if mx > -np.inf else -np.inf
-    return z - lse if mx > -np.inf else np.full_like(z, -np.inf), lse
+    if mx == -np.inf:
+        return np.full_like(z, -np.inf), -np.inf
+    ls = np.log(np.exp(z - mx).sum())
+    return (z - mx) - ls, mx + ls
 
 
 def stats_row(logits, target: int, top_k: int = 0, scale: float = 1.0):

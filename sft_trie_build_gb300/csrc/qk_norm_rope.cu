@@ -239,8 +239,9 @@ struct Share {
   __device__ __forceinline__ Share(int64_t units, int b0, int blocks) {
     const int64_t warps = (int64_t)blocks * (kQkThreads / 32);
     const int64_t me = (int64_t)((int)blockIdx.x - b0) * (kQkThreads / 32) + (threadIdx.x >> 5);
-    u0 = units * me / warps;
-    n = (int)(units * (me + 1) / warps - u0);
+    const int64_t each = units / warps, more = units % warps;   // the first `more` warps take one more
+    u0 = each * me + (me < more ? me : more);
+    n = (int)(each + (me < more));
   }
 };
 
@@ -340,8 +341,8 @@ __global__ void __launch_bounds__(kQkThreads, kQkFwdBlocks) qk_fwd_kernel(const 
 }
 
 // The same walk over x and dy.  A block works on the queries or on the keys
-// alone, so that a lane carries the sums of one weight; each block adds up its lanes' sums in a fixed order and writes them for
-// qk_dw_kernel.
+// alone, so that a lane carries the sums of one weight; each block adds up its
+// lanes' sums in a fixed order and writes them for qk_dw_kernel.
 template <typename T, int G, bool INTER>
 __global__ void __launch_bounds__(kQkThreads, kQkBwdBlocks) qk_bwd_kernel(const __grid_constant__ QkParams p) {
   __shared__ uint64_t freq[kQkMaxDim / 2];

@@ -82,7 +82,9 @@ struct Piece<__nv_bfloat16> {
     return make_uint4(tc::pack_bf16x2(f[0], f[1]), tc::pack_bf16x2(f[2], f[3]), tc::pack_bf16x2(f[4], f[5]),
                       tc::pack_bf16x2(f[6], f[7]));
   }
-  static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+  static __device__ __forceinline__ uint4 lowest() {   // -inf in every element
+    return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+  }
 };
 template <>
 struct Piece<float> {
@@ -96,7 +98,9 @@ struct Piece<float> {
   static __device__ __forceinline__ uint4 put(const float* f) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
   }
-  static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
+  static __device__ __forceinline__ uint4 lowest() {
+    return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+  }
 };
 
 __device__ __forceinline__ float to_f(float x) { return x; }
@@ -276,7 +280,8 @@ __device__ __forceinline__ Ring<R> ring_of(uint4* buffer, const T* row, const Pa
 // way.  With TOP, the thread's largest value and the round in which it came
 // are kept in (best, round).
 template <typename T, bool ENT, bool TOP, int R>
-__device__ __forceinline__ Acc pass(const T* row, const Part& p, const Ring<R>& ring, float sl2, float& best, int& round) {
+__device__ __forceinline__ Acc pass(const T* row, const Part& p, const Ring<R>& ring, float sl2, float& best,
+                                    int& round) {
   constexpr int E = Piece<T>::E;
   Acc a = {-INFINITY, 0.f, 0.f};
   const float extra = p.extra >= 0 ? to_f(row[p.extra]) : 0.f;
@@ -700,12 +705,13 @@ __device__ __forceinline__ float block_add(float v, float* red) {
 
 // Forward (LSE), backward (GRAD) or both.  Thread k < K holds the teacher's
 // k-th entry.  With both, the second pass finds the row in L2.
-template <typename T, bool LSE, bool GRAD>
-__global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPassBlocks) distill_kernel(const DistillParams p) {
+template <typename T, bool LSE, bool GRAD, bool MANY>
+__global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPassBlocks)
+    distill_kernel(const DistillParams p) {
   __shared__ Acc red[kRowWarps];
   __shared__ Acc sums[kMaxSplit];   // of the row's blocks
   __shared__ TeacherShared ts;
-  const int C = p.C, n = (int)(blockIdx.x / C), rank = (int)(blockIdx.x % C), t = threadIdx.x;
+  const int C = MANY ? p.C : 1, n = (int)(blockIdx.x / C), rank = MANY ? (int)(blockIdx.x % C) : 0, t = threadIdx.x;
   const T* row = static_cast<const T*>(p.z) + (int64_t)n * p.stride;
   T* out = GRAD ? static_cast<T*>(p.dz) + (int64_t)n * p.stride : nullptr;
   extern __shared__ uint4 buffer[];
@@ -724,7 +730,7 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
       if (LSE && rank == 0 && !p.check) atomicOr(p.err, kErrBadList);
       id = -1;
     }
-    if (id >= 0) a = p.tl[(int64_t)n * p.K + t] * p.sl2;
+    if (id >= 0) a = p.tl[(int64_t)n * p.K + t];
     if (a == -INFINITY) id = -1;
   }
   if (!__syncthreads_or(id >= 0)) {   // the same for every block of the row
@@ -735,10 +741,10 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
   const Part part = part_of(row, p.V, rank, C);
   const auto ring = ring_of<LSE && GRAD ? kStepRounds : kPassRounds>(buffer, row, part);
   ring.start(part.b0 + t);
-  if (LSE && C > 1) cg::this_cluster().barrier_arrive();   // this block runs: others may write to it
+  if (LSE && MANY) cg::this_cluster().barrier_arrive();   // this block runs: others may write to it
   const float zk = id >= 0 ? to_f(row[id]) : 0.f;
   const float top = block_max(a, ts.red);
-  const float ek = id >= 0 ? ex2(a - top) : 0.f;
+  const float ek = id >= 0 ? ex2((a - top) * p.sl2) : 0.f;   // the difference first, as in the sums
   const float sum = block_add(ek, ts.red);
   const float q = ek / sum;
   if (GRAD && t < kMaxTeacher) {
@@ -752,7 +758,7 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
     Acc s = pass<T, false, false>(row, part, ring, p.sl2, best, round);
     if (GRAD) ring.start(part.b0 + t);   // again, now out of L2
     s = block_sum(s, red, p.sl2);
-    if (C > 1) {
+    if (MANY) {
       cg::cluster_group cl = cg::this_cluster();
       cl.barrier_wait();
       if (t < C) *cl.map_shared_rank(sums + rank, t) = s;
@@ -762,7 +768,7 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
     const float ls = log_sum(s);
     lse = fmaf(s.m, p.scale, ls);
     if (rank == 0) {
-      const float lnq = kLn2T * (a - top - log2f(sum));
+      const float lnq = fmaf(a - top, p.scale, -kLn2T * log2f(sum));
       const float term = q != 0.f ? q * (lnq - fmaf(zk - s.m, p.scale, -ls)) : 0.f;
       const float loss = block_add(term, ts.red);
       if (t == 0) {
@@ -846,6 +852,16 @@ int step_split_of(int64_t rows, int64_t row_bytes) {
 // error word is cleared first and every row checks its own.
 constexpr int64_t kCheckMost = 65536;
 
+template <typename T, bool LSE, bool GRAD>
+const void* distill_by(bool many) {
+  return many ? (const void*)distill_kernel<T, LSE, GRAD, true> : (const void*)distill_kernel<T, LSE, GRAD, false>;
+}
+template <typename T>
+const void* distill_of(bool lse, bool grad, bool many) {
+  if (!lse) return distill_by<T, false, true>(many);
+  return grad ? distill_by<T, true, true>(many) : distill_by<T, true, false>(many);
+}
+
 template <typename T>
 const void* stats_fwd(bool top, bool many) {
   return top ? (many ? (const void*)stats_fwd_kernel<T, true, true> : (const void*)stats_fwd_kernel<T, true, false>)
@@ -854,12 +870,16 @@ const void* stats_fwd(bool top, bool many) {
 
 template <typename T>
 cudaError_t allow_rings_of() {
-  const void* pass[] = {stats_fwd<T>(false, false),        stats_fwd<T>(false, true),
-                        stats_fwd<T>(true, false),         stats_fwd<T>(true, true),
-                        (const void*)stats_bwd_kernel<T>, (const void*)distill_kernel<T, true, false>,
-                        (const void*)distill_kernel<T, false, true>};
-  cudaError_t e = cudaFuncSetAttribute((const void*)distill_kernel<T, true, true>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(kStepRounds));
+  const void* pass[] = {(const void*)stats_bwd_kernel<T>,
+                        stats_fwd<T>(false, false), stats_fwd<T>(false, true),
+                        stats_fwd<T>(true, false), stats_fwd<T>(true, true),
+                        distill_of<T>(true, false, false), distill_of<T>(true, false, true),
+                        distill_of<T>(false, true, false), distill_of<T>(false, true, true)};
+  cudaError_t e = cudaSuccess;
+  for (const bool many : {false, true})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(distill_of<T>(true, true, many), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               ring_bytes(kStepRounds));
   for (const void* k : pass)
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(kPassRounds));
@@ -960,7 +980,8 @@ extern "C" stp_status stp_token_stats_fwd(const stp_stats_desc* desc, const void
     p.top_lp = top_logprob;
     p.err = static_cast<uint32_t*>(d_ws);
     p.C = split_of(p.N, row_bytes(p.V, desc->dtype));
-    const void* k = desc->dtype == STP_BF16 ? stats_fwd<__nv_bfloat16>(p.K > 0, p.C > 1) : stats_fwd<float>(p.K > 0, p.C > 1);
+    const bool top = p.K > 0, many = p.C > 1;
+    const void* k = desc->dtype == STP_BF16 ? stats_fwd<__nv_bfloat16>(top, many) : stats_fwd<float>(top, many);
     e = launch(k, kPassRounds, p.N + p.check, p.C, &p, true, s);
   }
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_token_stats_fwd: %s", cudaGetErrorString(e));
@@ -1033,14 +1054,10 @@ static stp_status distill(const char* name, const stp_distill_desc* desc, const 
     p.err = static_cast<uint32_t*>(ws);
     p.check = check;
     const int64_t bytes = row_bytes(p.V, desc->dtype);
-    const bool both = fwd && grad, b = desc->dtype == STP_BF16;
+    const bool both = fwd && grad;
     p.C = both ? step_split_of(p.N, bytes) : split_of(p.N, bytes);
-    const void* k = both  ? (b ? (const void*)distill_kernel<__nv_bfloat16, true, true>
-                               : (const void*)distill_kernel<float, true, true>)
-                    : fwd ? (b ? (const void*)distill_kernel<__nv_bfloat16, true, false>
-                               : (const void*)distill_kernel<float, true, false>)
-                          : (b ? (const void*)distill_kernel<__nv_bfloat16, false, true>
-                               : (const void*)distill_kernel<float, false, true>);
+    const void* k = desc->dtype == STP_BF16 ? distill_of<__nv_bfloat16>(fwd, grad, p.C > 1)
+                                            : distill_of<float>(fwd, grad, p.C > 1);
     e = launch(k, both ? kStepRounds : kPassRounds, p.N + p.check, p.C, &p, fwd, s);
   }
   if (e != cudaSuccess) return fail(STP_ECUDA, "%s: %s", name, cudaGetErrorString(e));

@@ -272,6 +272,35 @@ def test_absent_repeated_and_masked_entries(how):
     _check_distill(z, ids, tl, mask, stp.STP_FP32, 1.0, how)
 
 
+@pytest.mark.parametrize("how", ["step", "two"])
+def test_rows_of_the_types_lowest_value(how):
+    """Masks that use the lowest finite value instead of -inf: probability 0 next
+    to others, and an even distribution in a row of nothing else."""
+    low, n, v, k = torch.finfo(torch.float32).min, 4, 700, 6
+    z = _logits(n, v, stp.STP_FP32, seed=3)
+    ids, tl = _teacher(n, v, k, seed=3)
+    z[0, 10:] = low
+    ids[0] = np.arange(k)
+    tl[1, 2:] = low
+    tl[2] = low
+    z[3] = low
+    g, loss, lse, dz, status = _distill(z, ids, tl, None, stp.STP_FP32, 1.5, how)
+    assert status == stp.STP_OK
+    # e of the values that count, |z| < 16 * 1.5: under 1e-5; twice that and K terms of it on the loss
+    zh = z.double().cpu().numpy()
+    for r in range(3):
+        want = OT.distill_row(zh[r], ids[r], tl[r], 1.5)[0]
+        assert abs(float(loss[r]) - want) <= 4e-5, r
+        off = np.abs(dz[r].double().cpu().numpy() - OT.distill_grad_row(zh[r], ids[r], tl[r], float(g[r]), 1.5))
+        assert off.max() <= 4e-5 * abs(float(g[r])) * 1.5, r
+    # every token alike: ln V - (entropy of q); the sum of V exponentials is exact here
+    q = OT._teacher(ids[3], tl[3], 1.5)[1]
+    assert abs(float(loss[3]) - (np.log(v) + (q * np.log(q)).sum())) < 1e-4
+    d, t, out, _ = _stats(z, [0, 1, 2, 3], 3, stp.STP_FP32, 1.5)
+    assert abs(float(out[0][3]) + np.log(v)) < 1e-5 and abs(float(out[1][3]) - np.log(v)) < 1e-5
+    assert out[3][3].tolist() == [0, 1, 2]
+
+
 def test_infinite_loss():
     z = _logits(1, 500, stp.STP_FP32, seed=1)
     z[0, 7] = -INF
