@@ -656,7 +656,8 @@ stp_status stp_token_stats_fwd(const stp_stats_desc* desc, const void* logits, c
  *   d_logits_v = scale (d_logprob ([v = target] - p_v) - d_entropy p_v (ln p_v + entropy))
  * with p = exp(z - lse); lse and entropy are the forward's.  d_entropy may be
  * NULL (zero).  d_logits (strided like logits, may be logits itself) is
- * written for every row: zeros where the target is negative or not below V.
+ * written for every row: zeros where the target is negative or not below V,
+ * or where lse is -inf (a row of nothing but -inf).
  */
 stp_status stp_token_stats_bwd(const stp_stats_desc* desc, const void* logits, const int32_t* d_targets,
                                const float* lse, const float* entropy, const float* d_logprob,
@@ -670,8 +671,9 @@ stp_status stp_token_stats_bwd(const stp_stats_desc* desc, const void* logits, c
  *   d_logits_v = d_loss[n] scale (p_v - sum_{k : id_k = v} q_k)
  * A negative id is an absent entry (as is one whose teacher logit is -inf); an
  * id may be listed twice.  A row whose loss_mask is 0 or that lists no id is
- * not read: loss = lse = 0 and a gradient of zeros.  All sums are float32 in a
- * fixed order.
+ * not read: loss = lse = 0 and a gradient of zeros.  A row whose logits are
+ * all -inf has lse = -inf, loss = +inf and a gradient of zeros.  All sums are
+ * float32 in a fixed order.
  */
 typedef struct {
   int32_t n_rows;    /* N >= 0                                                  */

@@ -636,12 +636,13 @@ __global__ void __launch_bounds__(kRowThreads, kPassBlocks) stats_bwd_kernel(con
   const int target = p.target[n];
   const T* row = static_cast<const T*>(p.z) + (int64_t)n * p.stride;
   T* out = static_cast<T*>(p.dz) + (int64_t)n * p.stride;
-  if (target < 0 || target >= p.V) {
+  const float lse = p.lse_in[n];
+  if (target < 0 || target >= p.V || lse == -INFINITY) {   // not wanted, or nothing but -inf
     zero_row(out, p.V, rank, C);
     return;
   }
   const Part part = part_of(row, p.V, rank, C);
-  const float scale = p.scale, lse = p.lse_in[n], g = p.g_lp[n] * scale, h = p.g_ent ? p.g_ent[n] * scale : 0.f;
+  const float scale = p.scale, g = p.g_lp[n] * scale, h = p.g_ent ? p.g_ent[n] * scale : 0.f;
   const float c = p.g_ent ? fmaf(h, p.ent_in[n], g) : g;
   extern __shared__ uint4 buffer[];
   const auto ring = ring_of<kPassRounds>(buffer, row, part);
@@ -769,7 +770,8 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
     lse = fmaf(s.m, p.scale, ls);
     if (rank == 0) {
       const float lnq = fmaf(a - top, p.scale, -kLn2T * log2f(sum));
-      const float term = q != 0.f ? q * (lnq - fmaf(zk - s.m, p.scale, -ls)) : 0.f;
+      const float lnp = s.s == 0.f ? -INFINITY : fmaf(zk - s.m, p.scale, -ls);
+      const float term = q != 0.f ? q * (lnq - lnp) : 0.f;
       const float loss = block_add(term, ts.red);
       if (t == 0) {
         p.loss[n] = loss;
@@ -782,6 +784,11 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
   if (GRAD) {
     const float scale = p.scale, g = p.g[n] * scale;
     __syncthreads();   // every zk is read before a logit may be overwritten
+    if (lse == -INFINITY) {   // nothing but -inf
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      zero_row(out, p.V, rank, C);
+      return;
+    }
     map_row(row, out, part, ring, [=](float* z, int, auto N) {
 #pragma unroll
       for (int e = 0; e < N(); ++e) z[e] = g * ex2(fmaf(z[e], scale, -lse) * kLog2eT);

@@ -301,6 +301,24 @@ def test_rows_of_the_types_lowest_value(how):
     assert out[3][3].tolist() == [0, 1, 2]
 
 
+@pytest.mark.parametrize("n", [2, 640])
+def test_gradients_of_rows_of_nothing(n):
+    """Rows of nothing but -inf: no distribution, a gradient of zeros, the others untouched."""
+    v = 4000
+    z = _logits(n, v, stp.STP_BF16, seed=5)
+    z[1] = -INF
+    ids, tl = _teacher(n, v, 5, seed=5)
+    for how in ("step", "two"):
+        _, loss, lse, dz, status = _distill(z, ids, tl, None, stp.STP_BF16, 1.0, how)
+        assert status == stp.STP_OK and loss[1] == INF and lse[1] == -INF
+        assert (dz[1] == 0).all() and torch.isfinite(dz).all() and (dz[0] != 0).any()
+    d, t, out, _ = _stats(z, np.zeros(n, int), 2, stp.STP_BF16, 1.0)
+    g, dz = torch.ones(n, device="cuda"), torch.full_like(z, NAN)
+    stp.stp_token_stats_bwd(d, z, t, out[2], out[1], g, g, dz)
+    torch.cuda.synchronize()
+    assert (dz[1] == 0).all() and torch.isfinite(dz).all() and (dz[0] != 0).any()
+
+
 def test_infinite_loss():
     z = _logits(1, 500, stp.STP_FP32, seed=1)
     z[0, 7] = -INF
