@@ -1057,18 +1057,30 @@ __device__ __forceinline__ uint64_t ds_desc(uint32_t addr) {
 }
 
 enum { Q_KF = 0, Q_KE = 2, Q_DF = 4, Q_DE = 8, Q_DONE = 12, Q_DRAIN = 13, Q_COUNT = 14 };
-// shared memory: [K0 | K1 | dS0 .. dS3] (1024-aligned) [barriers ...]
-constexpr int kDqBigBytes = 6 * kTileBytes;
-constexpr int kDqSmem = kDqBigBytes + kSmallBytes;
-static_assert(kDqSmem <= kSmemLimit, "dQ shared memory");
+// shared memory: [K ring | dS ring] (1024-aligned) [barriers ...].  PAIR (groups
+// of one or two heads): rings of one and two tiles and 256 TMEM columns, so that
+// two CTAs share an SM and one's start and end (5 us of a block's 12) lie under
+// the other's products: 16 rows of 4096 tokens in a window of 512, 16 / 8 heads,
+// 285 us instead of 328, 5.8 TB/s; otherwise two and four tiles, 512 columns, one CTA.
+template <bool PAIR>
+constexpr int kDqK = PAIR ? 1 : 2;
+template <bool PAIR>
+constexpr int kDqD = PAIR ? 2 : 4;
+template <bool PAIR>
+constexpr int kDqBigBytes = (kDqK<PAIR> + kDqD<PAIR>) * kTileBytes;
+template <bool PAIR>
+constexpr int kDqSmem = kDqBigBytes<PAIR> + kSmallBytes;
+static_assert(kDqSmem<false> <= kSmemLimit && 2 * (kDqSmem<true> + 1024) <= 228 * 1024, "dQ shared memory");
 constexpr int kDqThreads = 256;  // warp 0 loads, warp 1 MMA, warps 4-7 write dQ
 
-__global__ void __launch_bounds__(kDqThreads, 1)
+template <bool PAIR>
+__global__ void __launch_bounds__(kDqThreads, PAIR ? 2 : 1)
     dq_tc_kernel(const __grid_constant__ CUtensorMap tk, const DqParams p) {
+  constexpr int KS = kDqK<PAIR>, DS = kDqD<PAIR>, kColumns = PAIR ? 256 : 512;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* big = smem_raw;
   const uint32_t big_s = smem_u32(smem_raw);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + kDqBigBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + kDqBigBytes<PAIR>);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Q_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -1098,7 +1110,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
+    tmem_alloc(tmem_slot, kColumns);
     tmem_relinquish();
   }
   fence_before_sync();
@@ -1110,40 +1122,38 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   if (warp == 0 && lane == 0 && run) {
     // ------------------------------------------------------------ loads
     tma_prefetch_desc(&tk);
-    int issued_k[2] = {-1, -1}, issued_d[4] = {-1, -1, -1, -1};
+    int issued_k = -1, issued_d = -1;   // the last entry and dS tile under way
     int d = 0;
     for (int e = 0; e < cnt; ++e) {
-      const int kt = list[e] >> 1, sk = e & 1;
+      const int kt = list[e] >> 1, sk = e % KS;
       const int64_t pair = pbase + e;
       if (kt > qt || pair >= p.cap) {
         *abort_flag = 1;
         atomicOr(p.err, kt > qt ? kErrBadList : kErrCapacity);
         break;
       }
-      if (e >= 2 && !mbar_wait(&bars[Q_KE + sk], ((e >> 1) - 1) & 1, abort_flag, p.err)) break;
+      if (e >= KS && !mbar_wait(&bars[Q_KE + sk], (e / KS - 1) & 1, abort_flag, p.err)) break;
       mbar_expect_tx(&bars[Q_KF + sk], kTileBytes);
       for (int hf = 0; hf < 2; ++hf)
         tma_load_3d(big + sk * kTileBytes + hf * kHalfTile, &tk, &bars[Q_KF + sk], hf * 64, g, row0 + kt * 128);
-      issued_k[sk] = e >> 1;
+      issued_k = e;
       bool ok = true;
       for (int hh = 0; hh < nh; ++hh, ++d) {
-        const int sd = d & 3;
-        if (d >= 4 && !mbar_wait(&bars[Q_DE + sd], ((d >> 2) - 1) & 1, abort_flag, p.err)) {
+        const int sd = d % DS;
+        if (d >= DS && !mbar_wait(&bars[Q_DE + sd], (d / DS - 1) & 1, abort_flag, p.err)) {
           ok = false;
           break;
         }
         mbar_expect_tx(&bars[Q_DF + sd], (uint32_t)kDsTileBytes);
-        bulk_load(big + (2 + sd) * kTileBytes,
+        bulk_load(big + (KS + sd) * kTileBytes,
                   p.ds + ((size_t)pair * p.slot_heads + gl * p.G + 4 * quad + hh) * kDsTileBytes,
                   (uint32_t)kDsTileBytes, &bars[Q_DF + sd]);
-        issued_d[sd] = d >> 2;
+        issued_d = d;
       }
       if (!ok) break;
     }
-    for (int s = 0; s < 2; ++s)
-      if (issued_k[s] >= 0) mbar_wait_drain(&bars[Q_KF + s], issued_k[s] & 1);
-    for (int s = 0; s < 4; ++s)
-      if (issued_d[s] >= 0) mbar_wait_drain(&bars[Q_DF + s], issued_d[s] & 1);
+    for (int e = max(issued_k - KS + 1, 0); e <= issued_k; ++e) mbar_wait_drain(&bars[Q_KF + e % KS], (e / KS) & 1);
+    for (int t = max(issued_d - DS + 1, 0); t <= issued_d; ++t) mbar_wait_drain(&bars[Q_DF + t % DS], (t / DS) & 1);
   } else if (warp == 1 && lane == 0 && run) {
     // ------------------------------------------------------------ MMA
     constexpr uint32_t id_nn = idesc_bf16(128, 128, 1, 1);  // A = dS (queries contiguous), B = K
@@ -1151,21 +1161,21 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     bool ok = true;
     int d = 0;
     for (int e = 0; ok && e < cnt; ++e) {
-      const int sk = e & 1;
-      if (!mbar_wait(&bars[Q_KF + sk], (e >> 1) & 1, abort_flag, p.err)) {
+      const int sk = e % KS;
+      if (!mbar_wait(&bars[Q_KF + sk], (e / KS) & 1, abort_flag, p.err)) {
         ok = false;
         break;
       }
       const uint32_t k_mn = desc_lo_mnmajor(big_s + sk * kTileBytes);
       for (int hh = 0; hh < nh; ++hh, ++d) {
-        const int sd = d & 3;
-        if (!mbar_wait(&bars[Q_DF + sd], (d >> 2) & 1, abort_flag, p.err)) {
+        const int sd = d % DS;
+        if (!mbar_wait(&bars[Q_DF + sd], (d / DS) & 1, abort_flag, p.err)) {
           ok = false;
           break;
         }
         fence_after_sync();
         // slice kk = keys 16 kk .. 16 kk + 15: two core matrices along K, 256 bytes further
-        const uint64_t ds_a = ds_desc(big_s + (2 + sd) * kTileBytes);
+        const uint64_t ds_a = ds_desc(big_s + (KS + sd) * kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ss_a64(tmem + hh * 128, ds_a + (uint64_t)(kk * 16), k_mn + mn(kk), id_nn, (e > 0 || kk > 0));
@@ -1207,7 +1217,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc(tmem, kColumns);
 }
 
 // Delta[r,h,i] = sum_d dO . O (bf16 in, f32) for every (row, token, head);
@@ -1424,7 +1434,9 @@ cudaError_t tc_bwd(const AttnArgs& a, cudaStream_t s) {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(bwd_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(dq_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqSmem);
+      e = cudaFuncSetAttribute(dq_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqSmem<false>);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(dq_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqSmem<true>);
     if (e != cudaSuccess) return e;
     attr = true;
   }
@@ -1462,7 +1474,11 @@ cudaError_t tc_bwd(const AttnArgs& a, cudaStream_t s) {
       bwd_tc_kernel<true><<<(unsigned)(p.NT * p.R * p.ng), kBwdThreads, kBwdSmem, sg>>>(mq, mk, mv, mdo, p);
     else
       bwd_tc_kernel<false><<<(unsigned)(p.NT * p.R * p.ng), kBwdThreads, kBwdSmem, sg>>>(mq, mk, mv, mdo, p);
-    dq_tc_kernel<<<(unsigned)(p.NT * p.R * q.ng * q.nquad), kDqThreads, kDqSmem, sg>>>(mk, q);
+    const unsigned n_dq = (unsigned)(p.NT * p.R * q.ng * q.nquad);
+    if (p.G <= 2)
+      dq_tc_kernel<true><<<n_dq, kDqThreads, kDqSmem<true>, sg>>>(mk, q);
+    else
+      dq_tc_kernel<false><<<n_dq, kDqThreads, kDqSmem<false>, sg>>>(mk, q);
     if (n_groups > 1) {
       cudaError_t e = cudaEventRecord(bs->join[slot], sg);
       if (e == cudaSuccess) e = cudaStreamWaitEvent(s, bs->join[slot], 0);
