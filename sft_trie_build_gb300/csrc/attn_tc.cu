@@ -1240,52 +1240,46 @@ __global__ void __launch_bounds__(256) bwd_delta_kernel(const __nv_bfloat16* __r
                                                         uint8_t* __restrict__ sbias,
                                                         uint8_t* __restrict__ dbias, float inv_scale, int R,
                                                         int T, int Hq) {
-  // 16 lanes per (token, head) row of 128 values, 16 bytes of O and of dO per
-  // lane; each half-warp takes kRowsPer rows per pass with all their loads
-  // issued first, so that enough bytes are in flight to stream O and dO
+  // A warp takes one head's eight tokens of a core matrix, so that it writes
+  // whole 128-byte lines, and neighbouring warps take neighbouring heads; 16
+  // lanes per row of 128 values, 16 bytes of O and of dO per lane, four rows per
+  // half-warp with all their loads issued first, so that enough bytes are in
+  // flight to stream O and dO (65536 tokens of 16 heads: 88 us, 6.9 TB/s, 128 us
+  // with the two 16-byte pieces of a row written by themselves).
   constexpr int kRowsPer = 4;
-  const int hl = threadIdx.x & 15;
-  const unsigned hmask = 0xffffu << (threadIdx.x & 16);   // the half-warps loop independently
-  const size_t rows = (size_t)R * T * Hq;
+  const int lane = threadIdx.x & 31, hl = lane & 15, half = lane >> 4;
   const int NT = T / 128;
-  const size_t n_half = (size_t)gridDim.x * (blockDim.x / 16);
-  for (size_t w0 = ((size_t)blockIdx.x * (blockDim.x / 16) + (threadIdx.x >> 4)) * kRowsPer; w0 < rows;
-       w0 += n_half * kRowsPer) {
+  const size_t tasks = (size_t)R * T / 8 * Hq, step = (size_t)gridDim.x * (blockDim.x / 32);
+  for (size_t task = (size_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); task < tasks; task += step) {
+    const int h = (int)(task % Hq);
+    const size_t ri = task / Hq * 8;                 // the first of the eight tokens
+    const size_t rr = ri / T, i = ri - rr * T;
     uint4 a[kRowsPer], b[kRowsPer];
 #pragma unroll
     for (int k = 0; k < kRowsPer; ++k) {
-      const size_t w = w0 + k;
-      a[k] = b[k] = make_uint4(0, 0, 0, 0);
-      if (w < rows) {
-        a[k] = reinterpret_cast<const uint4*>(o + w * 128)[hl];
-        b[k] = reinterpret_cast<const uint4*>(dout + w * 128)[hl];
-      }
+      const size_t w = (ri + kRowsPer * half + k) * Hq + h;
+      a[k] = reinterpret_cast<const uint4*>(o + w * 128)[hl];
+      b[k] = reinterpret_cast<const uint4*>(dout + w * 128)[hl];
     }
+    // lane hl writes 16 bytes of token q: its terms in sbias, in dbias, zeros in each
+    const int what = hl >> 2, q = kRowsPer * half + (hl & 3);
+    float x = what == 0 ? -lse[(rr * Hq + h) * T + i + q] * inv_scale : 0.f;
 #pragma unroll
     for (int k = 0; k < kRowsPer; ++k) {
-      const size_t w = w0 + k;
       const uint32_t wa[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, wb[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
       float acc = 0.f;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        acc = fmaf(__uint_as_float(wa[q] << 16), __uint_as_float(wb[q] << 16), acc);
-        acc = fmaf(__uint_as_float(wa[q] & 0xffff0000u), __uint_as_float(wb[q] & 0xffff0000u), acc);
+      for (int v = 0; v < 4; ++v) {
+        acc = fmaf(__uint_as_float(wa[v] << 16), __uint_as_float(wb[v] << 16), acc);
+        acc = fmaf(__uint_as_float(wa[v] & 0xffff0000u), __uint_as_float(wb[v] & 0xffff0000u), acc);
       }
 #pragma unroll
-      for (int sft = 8; sft > 0; sft >>= 1) acc += __shfl_xor_sync(hmask, acc, sft);
-      if (w < rows && hl < 2) {
-        const int h = (int)(w % Hq);
-        const size_t ri = w / Hq;
-        const size_t rr = ri / T, i = ri - rr * T;
-        const size_t tile = ((rr * Hq + h) * NT + i / 128) * kBiasTileBytes;
-        const int q = (int)(i & 127);
-        const size_t at = tile + (q >> 3) * 256 + (q & 7) * 16;
-        uint8_t* dst = hl == 0 ? sbias : dbias;
-        const float x = hl == 0 ? -lse[(rr * Hq + h) * T + i] * inv_scale : -acc;
-        *reinterpret_cast<uint4*>(dst + at) = bias_row(x);
-        *reinterpret_cast<uint4*>(dst + at + 128) = make_uint4(0u, 0u, 0u, 0u);
-      }
+      for (int sft = 8; sft > 0; sft >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, sft);
+      if (what == 1 && (hl & 3) == k) x = -acc;
     }
+    uint8_t* tile = ((what & 1) ? dbias : sbias) + ((rr * Hq + h) * NT + i / 128) * kBiasTileBytes;
+    *reinterpret_cast<uint4*>(tile + ((i & 127) >> 3) * 256 + (what >> 1) * 128 + q * 16) =
+        what < 2 ? bias_row(x) : make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
