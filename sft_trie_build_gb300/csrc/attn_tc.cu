@@ -926,6 +926,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
     bool ok = run;
     uint32_t vis[2] = {~0u, ~0u};
+    bool cut[2] = {false, false};        // WIN: not all of the block is visible, the same for the warp
     int ent = run ? list[0] : 0;
     for (int j = 0; ok && j < n_it; ++j) {
       const int qt = ent >> 1, part = ent & 1;
@@ -940,6 +941,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int w = 0; w < 2; ++w) {
           const int cls = (word >> (8 * (2 * half + w))) & 3;
           vis[w] = cls == kEmpty ? 0u : ~0u;
+          cut[w] = cls != kFull;
           if (cls == kPartial) {
             const int4* pos4 = reinterpret_cast<const int4*>(p.pos + (size_t)row0 + q0 + 32 * w);
             uint32_t bits = 0;
@@ -971,16 +973,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[C_SR]);
+      if (WIN && part) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          if (cut[w]) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((vis[w] >> c) & 1u)) u[32 * w + c] = 0xff800000u;
+          }
+      }
 #pragma unroll
       for (int col = 0; col < 64; col += 4) {
 #pragma unroll
         for (int u2 = 0; u2 < 2; ++u2) {
           const int cc = col + 2 * u2;
           float2 y = __fmul2_rn(make_float2(__uint_as_float(u[cc]), __uint_as_float(u[cc + 1])), sl2);
-          if (WIN && part) {
-            if (!((vis[cc >> 5] >> (cc & 31)) & 1u)) y.x = -INFINITY;
-            if (!((vis[cc >> 5] >> ((cc + 1) & 31)) & 1u)) y.y = -INFINITY;
-          } else if (part) {
+          if (!WIN && part) {
             const int i = q0 + cc;
             if (!(jk <= i && se_j >= i)) y.x = -INFINITY;
             if (!(jk <= i + 1 && se_j >= i + 1)) y.y = -INFINITY;
