@@ -540,13 +540,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[B_PF + hs]);
     }
-    if (ok && __all_sync(0xffffffffu, mbar_wait(&bars[B_OD + hs], (cnt - 1) & 1, abort_flag, p.err))) {
+    if constexpr (WIN) {
+      if (ok && __all_sync(0xffffffffu, mbar_wait(&bars[B_OD + hs], (cnt - 1) & 1, abort_flag, p.err))) {
+        fence_after_sync();
+        const int h = h0 + hs;
+        // the head's Q tile was last read by the products of its last scores
+        store_rows(o_addr, 1.f / l_run, big + hs * kTileBytes + (warp & 3) * 8192,
+                   p.o + (((size_t)row0 + qt * 128 + 32 * (warp & 3)) * p.Hq + h) * 128, (size_t)p.Hq * 128, lane);
+        p.lse[((size_t)r * p.Hq + h) * p.T + i] = (m_run + log2f(l_run)) * kLn2;
+      }
+    } else if (ok && mbar_wait(&bars[B_OD + hs], (cnt - 1) & 1, abort_flag, p.err)) {
+      // straight from the lanes: with long lists the loop counts, which
+      // store_rows behind it makes spill (256 tiles: 2 % slower)
       fence_after_sync();
       const int h = h0 + hs;
+      __nv_bfloat16* orow = p.o + (((size_t)row0 + i) * p.Hq + h) * 128;
       const float inv = 1.f / l_run;
-      // the head's Q tile was last read by the products of its last scores
-      store_rows(o_addr, inv, big + hs * kTileBytes + (warp & 3) * 8192,
-                 p.o + (((size_t)row0 + qt * 128 + 32 * (warp & 3)) * p.Hq + h) * 128, (size_t)p.Hq * 128, lane);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t u[32];
+        tmem_ld32(o_addr + c * 32, u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint4 v;
+          v.x = pack_bf16x2(__uint_as_float(u[8 * k + 0]) * inv, __uint_as_float(u[8 * k + 1]) * inv);
+          v.y = pack_bf16x2(__uint_as_float(u[8 * k + 2]) * inv, __uint_as_float(u[8 * k + 3]) * inv);
+          v.z = pack_bf16x2(__uint_as_float(u[8 * k + 4]) * inv, __uint_as_float(u[8 * k + 5]) * inv);
+          v.w = pack_bf16x2(__uint_as_float(u[8 * k + 6]) * inv, __uint_as_float(u[8 * k + 7]) * inv);
+          *reinterpret_cast<uint4*>(orow + c * 32 + 8 * k) = v;
+        }
+      }
       p.lse[((size_t)r * p.Hq + h) * p.T + i] = (m_run + log2f(l_run)) * kLn2;
     }
   }
