@@ -45,14 +45,13 @@ __device__ __forceinline__ void stage_rows(float* dst, int ld, const Tin* src, s
   }
 }
 
-template <typename Tin, int D, bool WIN>
+template <typename Tin, int D>
 __global__ void __launch_bounds__(256) fwd_simt_kernel(AttnArgs a) {
   constexpr int DH = D / 2;
   extern __shared__ float sm[];
   float* Ks = sm;                  // [128][D]
   float* Vs = Ks + kTile * D;      // [128][D]
   int* se_s = reinterpret_cast<int*>(Vs + kTile * D);
-  int* lim_s = se_s + kTile;       // windowed attention only
   const int qt = blockIdx.x, h = blockIdx.y, r = blockIdx.z;
   const int tid = threadIdx.x, t = tid >> 1, half = tid & 1;
   const int T = a.T, NT = T / kTile, G = a.Hq / a.Hkv, g = h / G;
@@ -62,7 +61,6 @@ __global__ void __launch_bounds__(256) fwd_simt_kernel(AttnArgs a) {
   const Tin* K = static_cast<const Tin*>(a.k);
   const Tin* V = static_cast<const Tin*>(a.v);
   const float qs = a.scale * kLog2e;
-  const int pos_i = WIN ? a.pos[rowT + i] : 0;
   float qv[DH], o[DH];
 #pragma unroll
   for (int d = 0; d < DH; ++d) {
@@ -82,7 +80,6 @@ __global__ void __launch_bounds__(256) fwd_simt_kernel(AttnArgs a) {
     stage_rows<Tin, D>(Ks, D, K, rowT + k0, a.Hkv, g, kTile, tid, 256);
     stage_rows<Tin, D>(Vs, D, V, rowT + k0, a.Hkv, g, kTile, tid, 256);
     if (tid < kTile) se_s[tid] = a.se[rowT + k0 + tid];
-    if (WIN && tid < kTile) lim_s[tid] = a.lim[rowT + k0 + tid];
     __syncthreads();
     for (int c0 = 0; c0 < kTile; c0 += 32) {
       float s[32];
@@ -95,8 +92,7 @@ __global__ void __launch_bounds__(256) fwd_simt_kernel(AttnArgs a) {
         for (int d = 0; d < DH; ++d) acc = fmaf(qv[d], kr[d], acc);
         acc += __shfl_xor_sync(0xffffffffu, acc, 1);
         const int j = k0 + c0 + c;
-        const bool vis = !part || (j <= i && se_s[c0 + c] >= i &&
-                                   (!WIN || pos_i < lim_s[c0 + c]));
+        const bool vis = !part || (j <= i && se_s[c0 + c] >= i);
         s[c] = vis ? acc : -INFINITY;
         mx = fmaxf(mx, s[c]);
       }
@@ -147,7 +143,7 @@ __global__ void __launch_bounds__(256) delta_kernel(AttnArgs a) {
 
 constexpr int kChunk = 32;  // query / key rows staged per step in the backward
 
-template <typename Tin, int D, bool WIN>
+template <typename Tin, int D>
 __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
   constexpr int DH = D / 2, LD = D + 1;
   extern __shared__ float sm[];
@@ -157,7 +153,6 @@ __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
   float* dOc = Qc + kChunk * D;     // [32][D]
   float* lse2 = dOc + kChunk * D;   // [32]
   float* dlt = lse2 + kChunk;       // [32]
-  int* pos_c = reinterpret_cast<int*>(dlt + kChunk);  // [32], windowed attention only
   const int kt = blockIdx.x, g = blockIdx.y, r = blockIdx.z;
   const int tid = threadIdx.x, t = tid >> 1, half = tid & 1;
   const int T = a.T, NT = T / kTile, G = a.Hq / a.Hkv;
@@ -170,7 +165,6 @@ __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
   stage_rows<Tin, D>(Kown, LD, K, rowT + kt * kTile, a.Hkv, g, kTile, tid, 256);
   stage_rows<Tin, D>(Vown, LD, V, rowT + kt * kTile, a.Hkv, g, kTile, tid, 256);
   const int sej = a.se[rowT + j];
-  const int lim_j = WIN ? a.lim[rowT + j] : 0;
   const float qs = a.scale * kLog2e;
   float dk[DH], dv[DH];
 #pragma unroll
@@ -195,7 +189,6 @@ __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
         if (tid < kChunk) {
           lse2[tid] = a.lse[((size_t)r * a.Hq + h) * T + i0 + tid] * kLog2e;
           dlt[tid] = a.delta[((size_t)r * a.Hq + h) * T + i0 + tid];
-          if (WIN) pos_c[tid] = a.pos[rowT + i0 + tid];
         }
         __syncthreads();
         for (int c = 0; c < kChunk; ++c) {
@@ -210,7 +203,7 @@ __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
           }
           s += __shfl_xor_sync(0xffffffffu, s, 1);
           dp += __shfl_xor_sync(0xffffffffu, dp, 1);
-          const bool vis = !part || (j <= i && sej >= i && (!WIN || pos_c[c] < lim_j));
+          const bool vis = !part || (j <= i && sej >= i);
           const float p = vis ? exp2f(s * qs - lse2[c]) : 0.f;
           const float ds = p * (dp - dlt[c]);
 #pragma unroll
@@ -231,7 +224,7 @@ __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
   }
 }
 
-template <typename Tin, int D, bool WIN>
+template <typename Tin, int D>
 __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
   constexpr int DH = D / 2, LD = D + 1;
   extern __shared__ float sm[];
@@ -240,7 +233,6 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
   float* Kc = dOown + kTile * LD;     // [32][D]
   float* Vc = Kc + kChunk * D;        // [32][D]
   int* sec = reinterpret_cast<int*>(Vc + kChunk * D);
-  int* lim_c = sec + kChunk;          // [32], windowed attention only
   const int qt = blockIdx.x, h = blockIdx.y, r = blockIdx.z;
   const int tid = threadIdx.x, t = tid >> 1, half = tid & 1;
   const int T = a.T, NT = T / kTile, G = a.Hq / a.Hkv, g = h / G;
@@ -255,7 +247,6 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
   const float qs = a.scale * kLog2e;
   const float lse2 = a.lse[((size_t)r * a.Hq + h) * T + i] * kLog2e;
   const float dlt = a.delta[((size_t)r * a.Hq + h) * T + i];
-  const int pos_i = WIN ? a.pos[rowT + i] : 0;
   float dq[DH];
 #pragma unroll
   for (int d = 0; d < DH; ++d) dq[d] = 0.f;
@@ -275,7 +266,6 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
       stage_rows<Tin, D>(Kc, D, K, rowT + j0, a.Hkv, g, kChunk, tid, 256);
       stage_rows<Tin, D>(Vc, D, V, rowT + j0, a.Hkv, g, kChunk, tid, 256);
       if (tid < kChunk) sec[tid] = a.se[rowT + j0 + tid];
-      if (WIN && tid < kChunk) lim_c[tid] = a.lim[rowT + j0 + tid];
       __syncthreads();
       for (int c = 0; c < kChunk; ++c) {
         const int j = j0 + c;
@@ -289,7 +279,7 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
         }
         s += __shfl_xor_sync(0xffffffffu, s, 1);
         dp += __shfl_xor_sync(0xffffffffu, dp, 1);
-        const bool vis = !part || (j <= i && sec[c] >= i && (!WIN || pos_i < lim_c[c]));
+        const bool vis = !part || (j <= i && sec[c] >= i);
         const float p = vis ? exp2f(s * qs - lse2) : 0.f;
         const float ds = p * (dp - dlt);
 #pragma unroll
@@ -302,40 +292,289 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
   for (int d = 0; d < DH; ++d) dQ[((rowT + i) * a.Hq + h) * D + half * DH + d] = from_f<Tin>(dq[d] * a.scale);
 }
 
-template <typename Tin, int D, bool WIN>
-cudaError_t launch_fwd(const AttnArgs& a, cudaStream_t s) {
-  const size_t smem = 2 * kTile * D * sizeof(float) + (WIN ? 2 : 1) * kTile * sizeof(int);
-  cudaFuncSetAttribute(fwd_simt_kernel<Tin, D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  fwd_simt_kernel<Tin, D, WIN><<<dim3(a.T / kTile, a.Hq, a.R), 256, smem, s>>>(a);
+// ------------------------------------------------------------------------
+// Windowed attention in float32.  A window and short branches leave many of a
+// tile pair's 32 x 32 blocks EMPTY, and rows in float32 are short, so a block
+// here takes 32 queries (dK / dV: 32 keys) with eight threads each, every eighth
+// channel a thread, and walks the listed tile pairs by their 32 x 32 blocks: four
+// times the thread blocks, an eighth of the channels in a dot product's chain,
+// and no work for an EMPTY block.  The own rows stay in registers, the other
+// side's pass through shared memory 32 at a time.  Two rows of 768 tokens, two
+// heads of 128 channels, window 76: forward and backward 390 us.
+// ------------------------------------------------------------------------
+constexpr int kPart = 8;
+
+__device__ __forceinline__ float join8(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  x += __shfl_xor_sync(0xffffffffu, x, 2);
+  return x + __shfl_xor_sync(0xffffffffu, x, 4);
+}
+// the classes of a listed pair's blocks
+__device__ __forceinline__ uint32_t pair_word(const AttnArgs& a, int r, int NT, int qt, int kt, int part) {
+  return part ? a.word[((size_t)r * NT + qt) * NT + kt] : 0xaaaaaaaau;
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) win_fwd_kernel(AttnArgs a) {
+  constexpr int DP = D / kPart;
+  __shared__ float Kc[kChunk * D], Vc[kChunk * D];
+  __shared__ int sec[kChunk], lim[kChunk];
+  const int qb = blockIdx.x, h = blockIdx.y, r = blockIdx.z, qt = qb >> 2;
+  const int tid = threadIdx.x, part = tid & (kPart - 1);
+  const int T = a.T, NT = T / kTile, g = h / (a.Hq / a.Hkv);
+  const int i = qb * kChunk + tid / kPart;
+  const size_t rowT = (size_t)r * T, own = ((rowT + i) * a.Hq + h) * D + part;
+  const float *Q = static_cast<const float*>(a.q), *K = static_cast<const float*>(a.k),
+              *V = static_cast<const float*>(a.v);
+  const float qs = a.scale * kLog2e;
+  const int pos_i = a.pos[rowT + i];
+  float q[DP], o[DP];
+#pragma unroll
+  for (int d = 0; d < DP; ++d) {
+    q[d] = Q[own + d * kPart] * qs;
+    o[d] = 0.f;
+  }
+  float m = -INFINITY, l = 0.f;
+  const int cnt = a.csr_cnt[(size_t)r * NT + qt];
+  const int32_t* list = a.csr + ((size_t)r * NT + qt) * NT;
+  for (int e = 0; e < cnt; ++e) {
+    const int kt = list[e] >> 1;
+    if (kt < 0 || kt >= NT) {
+      if (tid == 0) atomicOr(a.err, kErrBadList);
+      break;
+    }
+    const uint32_t word = pair_word(a, r, NT, qt, kt, list[e] & 1) >> (8 * (qb & 3));
+    for (int kb = 0; kb < 4; ++kb) {
+      const int cls = (word >> (2 * kb)) & 3, k0 = kt * kTile + kb * kChunk;
+      if (cls == kEmpty) continue;
+      __syncthreads();
+      stage_rows<float, D>(Kc, D, K, rowT + k0, a.Hkv, g, kChunk, tid, 256);
+      stage_rows<float, D>(Vc, D, V, rowT + k0, a.Hkv, g, kChunk, tid, 256);
+      if (tid < kChunk) {
+        sec[tid] = a.se[rowT + k0 + tid];
+        lim[tid] = a.lim[rowT + k0 + tid];
+      }
+      __syncthreads();
+      float s[kChunk], mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < kChunk; ++c) {
+        float acc = 0.f;
+#pragma unroll
+        for (int d = 0; d < DP; ++d) acc = fmaf(q[d], Kc[c * D + d * kPart + part], acc);
+        acc = join8(acc);
+        const bool vis = cls == kFull || (k0 + c <= i && sec[c] >= i && pos_i < lim[c]);
+        s[c] = vis ? acc : -INFINITY;
+        mx = fmaxf(mx, s[c]);
+      }
+      const float mn = fmaxf(m, mx);
+      if (mn == -INFINITY) continue;
+      const float alpha = exp2f(m - mn);
+      l *= alpha;
+#pragma unroll
+      for (int d = 0; d < DP; ++d) o[d] *= alpha;
+#pragma unroll
+      for (int c = 0; c < kChunk; ++c) {
+        const float p = exp2f(s[c] - mn);
+        l += p;
+#pragma unroll
+        for (int d = 0; d < DP; ++d) o[d] = fmaf(p, Vc[c * D + d * kPart + part], o[d]);
+      }
+      m = mn;
+    }
+  }
+  float* O = static_cast<float*>(a.o);
+  const float inv = 1.f / l;
+#pragma unroll
+  for (int d = 0; d < DP; ++d) O[own + d * kPart] = o[d] * inv;
+  if (part == 0) a.lse[((size_t)r * a.Hq + h) * T + i] = (m + log2f(l)) * kLn2;
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) win_dkdv_kernel(AttnArgs a) {
+  constexpr int DP = D / kPart;
+  __shared__ float Qc[kChunk * D], dOc[kChunk * D], lse2[kChunk], dlt[kChunk];
+  __shared__ int pos[kChunk];
+  const int kb = blockIdx.x, g = blockIdx.y, r = blockIdx.z, kt = kb >> 2;
+  const int tid = threadIdx.x, part = tid & (kPart - 1);
+  const int T = a.T, NT = T / kTile, G = a.Hq / a.Hkv;
+  const int j = kb * kChunk + tid / kPart;
+  const size_t rowT = (size_t)r * T, own = ((rowT + j) * a.Hkv + g) * D + part;
+  const float *Q = static_cast<const float*>(a.q), *K = static_cast<const float*>(a.k),
+              *V = static_cast<const float*>(a.v), *dO = static_cast<const float*>(a.dout);
+  const float qs = a.scale * kLog2e;
+  const int sej = a.se[rowT + j], lim_j = a.lim[rowT + j];
+  float k[DP], v[DP], dk[DP], dv[DP];
+#pragma unroll
+  for (int d = 0; d < DP; ++d) {
+    k[d] = K[own + d * kPart];
+    v[d] = V[own + d * kPart];
+    dk[d] = dv[d] = 0.f;
+  }
+  const int cnt = a.csc_cnt[(size_t)r * NT + kt];
+  const int32_t* list = a.csc + ((size_t)r * NT + kt) * NT;
+  for (int e = 0; e < cnt; ++e) {
+    const int qt = list[e] >> 1;
+    if (qt < 0 || qt >= NT) {
+      if (tid == 0) atomicOr(a.err, kErrBadList);
+      break;
+    }
+    const uint32_t word = pair_word(a, r, NT, qt, kt, list[e] & 1) >> (2 * (kb & 3));
+    for (int hq = 0; hq < 4 * G; ++hq) {
+      const int qb = hq & 3, h = g * G + (hq >> 2), cls = (word >> (8 * qb)) & 3, i0 = qt * kTile + qb * kChunk;
+      if (cls == kEmpty) continue;
+      __syncthreads();
+      stage_rows<float, D>(Qc, D, Q, rowT + i0, a.Hq, h, kChunk, tid, 256);
+      stage_rows<float, D>(dOc, D, dO, rowT + i0, a.Hq, h, kChunk, tid, 256);
+      if (tid < kChunk) {
+        lse2[tid] = a.lse[((size_t)r * a.Hq + h) * T + i0 + tid] * kLog2e;
+        dlt[tid] = a.delta[((size_t)r * a.Hq + h) * T + i0 + tid];
+        pos[tid] = a.pos[rowT + i0 + tid];
+      }
+      __syncthreads();
+#pragma unroll 4
+      for (int c = 0; c < kChunk; ++c) {
+        const float *qr = Qc + c * D + part, *gr = dOc + c * D + part;
+        float s = 0.f, dp = 0.f;
+#pragma unroll
+        for (int d = 0; d < DP; ++d) {
+          s = fmaf(qr[d * kPart], k[d], s);
+          dp = fmaf(gr[d * kPart], v[d], dp);
+        }
+        s = join8(s);
+        dp = join8(dp);
+        const bool vis = cls == kFull || (j <= i0 + c && sej >= i0 + c && pos[c] < lim_j);
+        const float p = vis ? exp2f(s * qs - lse2[c]) : 0.f;
+        const float ds = p * (dp - dlt[c]);
+#pragma unroll
+        for (int d = 0; d < DP; ++d) {
+          dv[d] = fmaf(p, gr[d * kPart], dv[d]);
+          dk[d] = fmaf(ds, qr[d * kPart], dk[d]);
+        }
+      }
+    }
+  }
+  float *dK = static_cast<float*>(a.dk), *dV = static_cast<float*>(a.dv);
+#pragma unroll
+  for (int d = 0; d < DP; ++d) {
+    dK[own + d * kPart] = dk[d] * a.scale;
+    dV[own + d * kPart] = dv[d];
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) win_dq_kernel(AttnArgs a) {
+  constexpr int DP = D / kPart;
+  __shared__ float Kc[kChunk * D], Vc[kChunk * D];
+  __shared__ int sec[kChunk], lim[kChunk];
+  const int qb = blockIdx.x, h = blockIdx.y, r = blockIdx.z, qt = qb >> 2;
+  const int tid = threadIdx.x, part = tid & (kPart - 1);
+  const int T = a.T, NT = T / kTile, g = h / (a.Hq / a.Hkv);
+  const int i = qb * kChunk + tid / kPart;
+  const size_t rowT = (size_t)r * T, own = ((rowT + i) * a.Hq + h) * D + part;
+  const float *Q = static_cast<const float*>(a.q), *K = static_cast<const float*>(a.k),
+              *V = static_cast<const float*>(a.v), *dO = static_cast<const float*>(a.dout);
+  const float qs = a.scale * kLog2e;
+  const float lse2 = a.lse[((size_t)r * a.Hq + h) * T + i] * kLog2e, dlt = a.delta[((size_t)r * a.Hq + h) * T + i];
+  const int pos_i = a.pos[rowT + i];
+  float q[DP], go[DP], dq[DP];
+#pragma unroll
+  for (int d = 0; d < DP; ++d) {
+    q[d] = Q[own + d * kPart];
+    go[d] = dO[own + d * kPart];
+    dq[d] = 0.f;
+  }
+  const int cnt = a.csr_cnt[(size_t)r * NT + qt];
+  const int32_t* list = a.csr + ((size_t)r * NT + qt) * NT;
+  for (int e = 0; e < cnt; ++e) {
+    const int kt = list[e] >> 1;
+    if (kt < 0 || kt >= NT) {
+      if (tid == 0) atomicOr(a.err, kErrBadList);
+      break;
+    }
+    const uint32_t word = pair_word(a, r, NT, qt, kt, list[e] & 1) >> (8 * (qb & 3));
+    for (int kb = 0; kb < 4; ++kb) {
+      const int cls = (word >> (2 * kb)) & 3, k0 = kt * kTile + kb * kChunk;
+      if (cls == kEmpty) continue;
+      __syncthreads();
+      stage_rows<float, D>(Kc, D, K, rowT + k0, a.Hkv, g, kChunk, tid, 256);
+      stage_rows<float, D>(Vc, D, V, rowT + k0, a.Hkv, g, kChunk, tid, 256);
+      if (tid < kChunk) {
+        sec[tid] = a.se[rowT + k0 + tid];
+        lim[tid] = a.lim[rowT + k0 + tid];
+      }
+      __syncthreads();
+#pragma unroll 4
+      for (int c = 0; c < kChunk; ++c) {
+        const float *kr = Kc + c * D + part, *vr = Vc + c * D + part;
+        float s = 0.f, dp = 0.f;
+#pragma unroll
+        for (int d = 0; d < DP; ++d) {
+          s = fmaf(q[d], kr[d * kPart], s);
+          dp = fmaf(go[d], vr[d * kPart], dp);
+        }
+        s = join8(s);
+        dp = join8(dp);
+        const bool vis = cls == kFull || (k0 + c <= i && sec[c] >= i && pos_i < lim[c]);
+        const float p = vis ? exp2f(s * qs - lse2) : 0.f;
+        const float ds = p * (dp - dlt);
+#pragma unroll
+        for (int d = 0; d < DP; ++d) dq[d] = fmaf(ds, kr[d * kPart], dq[d]);
+      }
+    }
+  }
+  float* dQ = static_cast<float*>(a.dq);
+#pragma unroll
+  for (int d = 0; d < DP; ++d) dQ[own + d * kPart] = dq[d] * a.scale;
+}
+
+template <int D>
+cudaError_t launch_win_fwd(const AttnArgs& a, cudaStream_t s) {
+  win_fwd_kernel<D><<<dim3(a.T / kChunk, a.Hq, a.R), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename Tin, int D, bool WIN>
+template <int D>
+cudaError_t launch_win_bwd(const AttnArgs& a, cudaStream_t s) {
+  delta_kernel<float, D><<<1024, 256, 0, s>>>(a);
+  win_dkdv_kernel<D><<<dim3(a.T / kChunk, a.Hkv, a.R), 256, 0, s>>>(a);
+  win_dq_kernel<D><<<dim3(a.T / kChunk, a.Hq, a.R), 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename Tin, int D>
+cudaError_t launch_fwd(const AttnArgs& a, cudaStream_t s) {
+  const size_t smem = 2 * kTile * D * sizeof(float) + kTile * sizeof(int);
+  cudaFuncSetAttribute(fwd_simt_kernel<Tin, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  fwd_simt_kernel<Tin, D><<<dim3(a.T / kTile, a.Hq, a.R), 256, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename Tin, int D>
 cudaError_t launch_bwd(const AttnArgs& a, cudaStream_t s) {
   delta_kernel<Tin, D><<<1024, 256, 0, s>>>(a);
   const size_t smem_kv =
-      (2 * kTile * (D + 1) + 2 * kChunk * D + 2 * kChunk) * sizeof(float) + (WIN ? kChunk * sizeof(int) : 0);
-  cudaFuncSetAttribute(dkdv_simt_kernel<Tin, D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_kv);
-  dkdv_simt_kernel<Tin, D, WIN><<<dim3(a.T / kTile, a.Hkv, a.R), 256, smem_kv, s>>>(a);
+      (2 * kTile * (D + 1) + 2 * kChunk * D + 2 * kChunk) * sizeof(float);
+  cudaFuncSetAttribute(dkdv_simt_kernel<Tin, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_kv);
+  dkdv_simt_kernel<Tin, D><<<dim3(a.T / kTile, a.Hkv, a.R), 256, smem_kv, s>>>(a);
   const size_t smem_q =
-      (2 * kTile * (D + 1) + 2 * kChunk * D) * sizeof(float) + (WIN ? 2 : 1) * kChunk * sizeof(int);
-  cudaFuncSetAttribute(dq_simt_kernel<Tin, D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_q);
-  dq_simt_kernel<Tin, D, WIN><<<dim3(a.T / kTile, a.Hq, a.R), 256, smem_q, s>>>(a);
+      (2 * kTile * (D + 1) + 2 * kChunk * D) * sizeof(float) + kChunk * sizeof(int);
+  cudaFuncSetAttribute(dq_simt_kernel<Tin, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_q);
+  dq_simt_kernel<Tin, D><<<dim3(a.T / kTile, a.Hq, a.R), 256, smem_q, s>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t simt_fwd(const AttnArgs& a, bool bf16, cudaStream_t s) {
-  if (bf16) return a.D == 64 ? launch_fwd<__nv_bfloat16, 64, false>(a, s) : launch_fwd<__nv_bfloat16, 128, false>(a, s);
-  if (a.pos) return a.D == 64 ? launch_fwd<float, 64, true>(a, s) : launch_fwd<float, 128, true>(a, s);
-  return a.D == 64 ? launch_fwd<float, 64, false>(a, s) : launch_fwd<float, 128, false>(a, s);
+  if (bf16) return a.D == 64 ? launch_fwd<__nv_bfloat16, 64>(a, s) : launch_fwd<__nv_bfloat16, 128>(a, s);
+  if (a.pos) return a.D == 64 ? launch_win_fwd<64>(a, s) : launch_win_fwd<128>(a, s);
+  return a.D == 64 ? launch_fwd<float, 64>(a, s) : launch_fwd<float, 128>(a, s);
 }
 
 cudaError_t simt_bwd(const AttnArgs& a, bool bf16, cudaStream_t s) {
-  if (bf16) return a.D == 64 ? launch_bwd<__nv_bfloat16, 64, false>(a, s) : launch_bwd<__nv_bfloat16, 128, false>(a, s);
-  if (a.pos) return a.D == 64 ? launch_bwd<float, 64, true>(a, s) : launch_bwd<float, 128, true>(a, s);
-  return a.D == 64 ? launch_bwd<float, 64, false>(a, s) : launch_bwd<float, 128, false>(a, s);
+  if (bf16) return a.D == 64 ? launch_bwd<__nv_bfloat16, 64>(a, s) : launch_bwd<__nv_bfloat16, 128>(a, s);
+  if (a.pos) return a.D == 64 ? launch_win_bwd<64>(a, s) : launch_win_bwd<128>(a, s);
+  return a.D == 64 ? launch_bwd<float, 64>(a, s) : launch_bwd<float, 128>(a, s);
 }
 
 }  // namespace stp
