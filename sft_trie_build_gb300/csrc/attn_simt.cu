@@ -295,14 +295,29 @@ __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
 // ------------------------------------------------------------------------
 // Windowed attention in float32.  A window and short branches leave many of a
 // tile pair's 32 x 32 blocks EMPTY, and rows in float32 are short, so a block
-// here takes 32 queries (dK / dV: 32 keys) with eight threads each, every eighth
-// channel a thread, and walks the listed tile pairs by their 32 x 32 blocks: four
+// here takes 32 queries (dK / dV: 32 keys) with eight threads each, an
+// eighth of the channels a thread, and walks the listed tile pairs by their 32 x 32 blocks: four
 // times the thread blocks, an eighth of the channels in a dot product's chain,
 // and no work for an EMPTY block.  The own rows stay in registers, the other
 // side's pass through shared memory 32 at a time.  Two rows of 768 tokens, two
-// heads of 128 channels, window 76: forward and backward 390 us.
+// heads of 128 channels, window 76: forward and backward 380 us.
 // ------------------------------------------------------------------------
 constexpr int kPart = 8;
+
+// channel d of a thread, and its channels of a row in shared memory: four
+// neighbours at a time, 16 bytes, so that a warp's eight parts read a whole line
+__device__ __forceinline__ int chan(int d, int part) { return (d >> 2) * 4 * kPart + part * 4 + (d & 3); }
+template <int DP>
+__device__ __forceinline__ void row_of(float* x, const float* row, int part) {
+#pragma unroll
+  for (int d = 0; d < DP; d += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(row + chan(d, part));
+    x[d] = v.x;
+    x[d + 1] = v.y;
+    x[d + 2] = v.z;
+    x[d + 3] = v.w;
+  }
+}
 
 __device__ __forceinline__ float join8(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 1);
@@ -317,13 +332,13 @@ __device__ __forceinline__ uint32_t pair_word(const AttnArgs& a, int r, int NT, 
 template <int D>
 __global__ void __launch_bounds__(256) win_fwd_kernel(AttnArgs a) {
   constexpr int DP = D / kPart;
-  __shared__ float Kc[kChunk * D], Vc[kChunk * D];
+  __shared__ __align__(16) float Kc[kChunk * D], Vc[kChunk * D];
   __shared__ int sec[kChunk], lim[kChunk];
   const int qb = blockIdx.x, h = blockIdx.y, r = blockIdx.z, qt = qb >> 2;
   const int tid = threadIdx.x, part = tid & (kPart - 1);
   const int T = a.T, NT = T / kTile, g = h / (a.Hq / a.Hkv);
   const int i = qb * kChunk + tid / kPart;
-  const size_t rowT = (size_t)r * T, own = ((rowT + i) * a.Hq + h) * D + part;
+  const size_t rowT = (size_t)r * T, own = ((rowT + i) * a.Hq + h) * D;
   const float *Q = static_cast<const float*>(a.q), *K = static_cast<const float*>(a.k),
               *V = static_cast<const float*>(a.v);
   const float qs = a.scale * kLog2e;
@@ -331,7 +346,7 @@ __global__ void __launch_bounds__(256) win_fwd_kernel(AttnArgs a) {
   float q[DP], o[DP];
 #pragma unroll
   for (int d = 0; d < DP; ++d) {
-    q[d] = Q[own + d * kPart] * qs;
+    q[d] = Q[own + chan(d, part)] * qs;
     o[d] = 0.f;
   }
   float m = -INFINITY, l = 0.f;
@@ -358,9 +373,10 @@ __global__ void __launch_bounds__(256) win_fwd_kernel(AttnArgs a) {
       float s[kChunk], mx = -INFINITY;
 #pragma unroll
       for (int c = 0; c < kChunk; ++c) {
-        float acc = 0.f;
+        float acc = 0.f, kr[DP];
+        row_of<DP>(kr, Kc + c * D, part);
 #pragma unroll
-        for (int d = 0; d < DP; ++d) acc = fmaf(q[d], Kc[c * D + d * kPart + part], acc);
+        for (int d = 0; d < DP; ++d) acc = fmaf(q[d], kr[d], acc);
         acc = join8(acc);
         const bool vis = cls == kFull || (k0 + c <= i && sec[c] >= i && pos_i < lim[c]);
         s[c] = vis ? acc : -INFINITY;
@@ -376,8 +392,10 @@ __global__ void __launch_bounds__(256) win_fwd_kernel(AttnArgs a) {
       for (int c = 0; c < kChunk; ++c) {
         const float p = exp2f(s[c] - mn);
         l += p;
+        float vr[DP];
+        row_of<DP>(vr, Vc + c * D, part);
 #pragma unroll
-        for (int d = 0; d < DP; ++d) o[d] = fmaf(p, Vc[c * D + d * kPart + part], o[d]);
+        for (int d = 0; d < DP; ++d) o[d] = fmaf(p, vr[d], o[d]);
       }
       m = mn;
     }
@@ -385,20 +403,21 @@ __global__ void __launch_bounds__(256) win_fwd_kernel(AttnArgs a) {
   float* O = static_cast<float*>(a.o);
   const float inv = 1.f / l;
 #pragma unroll
-  for (int d = 0; d < DP; ++d) O[own + d * kPart] = o[d] * inv;
+  for (int d = 0; d < DP; ++d) O[own + chan(d, part)] = o[d] * inv;
   if (part == 0) a.lse[((size_t)r * a.Hq + h) * T + i] = (m + log2f(l)) * kLn2;
 }
 
 template <int D>
 __global__ void __launch_bounds__(256) win_dkdv_kernel(AttnArgs a) {
   constexpr int DP = D / kPart;
-  __shared__ float Qc[kChunk * D], dOc[kChunk * D], lse2[kChunk], dlt[kChunk];
+  __shared__ __align__(16) float Qc[kChunk * D], dOc[kChunk * D];
+  __shared__ float lse2[kChunk], dlt[kChunk];
   __shared__ int pos[kChunk];
   const int kb = blockIdx.x, g = blockIdx.y, r = blockIdx.z, kt = kb >> 2;
   const int tid = threadIdx.x, part = tid & (kPart - 1);
   const int T = a.T, NT = T / kTile, G = a.Hq / a.Hkv;
   const int j = kb * kChunk + tid / kPart;
-  const size_t rowT = (size_t)r * T, own = ((rowT + j) * a.Hkv + g) * D + part;
+  const size_t rowT = (size_t)r * T, own = ((rowT + j) * a.Hkv + g) * D;
   const float *Q = static_cast<const float*>(a.q), *K = static_cast<const float*>(a.k),
               *V = static_cast<const float*>(a.v), *dO = static_cast<const float*>(a.dout);
   const float qs = a.scale * kLog2e;
@@ -406,8 +425,8 @@ __global__ void __launch_bounds__(256) win_dkdv_kernel(AttnArgs a) {
   float k[DP], v[DP], dk[DP], dv[DP];
 #pragma unroll
   for (int d = 0; d < DP; ++d) {
-    k[d] = K[own + d * kPart];
-    v[d] = V[own + d * kPart];
+    k[d] = K[own + chan(d, part)];
+    v[d] = V[own + chan(d, part)];
     dk[d] = dv[d] = 0.f;
   }
   const int cnt = a.csc_cnt[(size_t)r * NT + kt];
@@ -431,14 +450,16 @@ __global__ void __launch_bounds__(256) win_dkdv_kernel(AttnArgs a) {
         pos[tid] = a.pos[rowT + i0 + tid];
       }
       __syncthreads();
-#pragma unroll 4
+#pragma unroll 2
       for (int c = 0; c < kChunk; ++c) {
-        const float *qr = Qc + c * D + part, *gr = dOc + c * D + part;
+        float qr[DP], gr[DP];
+        row_of<DP>(qr, Qc + c * D, part);
+        row_of<DP>(gr, dOc + c * D, part);
         float s = 0.f, dp = 0.f;
 #pragma unroll
         for (int d = 0; d < DP; ++d) {
-          s = fmaf(qr[d * kPart], k[d], s);
-          dp = fmaf(gr[d * kPart], v[d], dp);
+          s = fmaf(qr[d], k[d], s);
+          dp = fmaf(gr[d], v[d], dp);
         }
         s = join8(s);
         dp = join8(dp);
@@ -447,8 +468,8 @@ __global__ void __launch_bounds__(256) win_dkdv_kernel(AttnArgs a) {
         const float ds = p * (dp - dlt[c]);
 #pragma unroll
         for (int d = 0; d < DP; ++d) {
-          dv[d] = fmaf(p, gr[d * kPart], dv[d]);
-          dk[d] = fmaf(ds, qr[d * kPart], dk[d]);
+          dv[d] = fmaf(p, gr[d], dv[d]);
+          dk[d] = fmaf(ds, qr[d], dk[d]);
         }
       }
     }
@@ -456,21 +477,21 @@ __global__ void __launch_bounds__(256) win_dkdv_kernel(AttnArgs a) {
   float *dK = static_cast<float*>(a.dk), *dV = static_cast<float*>(a.dv);
 #pragma unroll
   for (int d = 0; d < DP; ++d) {
-    dK[own + d * kPart] = dk[d] * a.scale;
-    dV[own + d * kPart] = dv[d];
+    dK[own + chan(d, part)] = dk[d] * a.scale;
+    dV[own + chan(d, part)] = dv[d];
   }
 }
 
 template <int D>
 __global__ void __launch_bounds__(256) win_dq_kernel(AttnArgs a) {
   constexpr int DP = D / kPart;
-  __shared__ float Kc[kChunk * D], Vc[kChunk * D];
+  __shared__ __align__(16) float Kc[kChunk * D], Vc[kChunk * D];
   __shared__ int sec[kChunk], lim[kChunk];
   const int qb = blockIdx.x, h = blockIdx.y, r = blockIdx.z, qt = qb >> 2;
   const int tid = threadIdx.x, part = tid & (kPart - 1);
   const int T = a.T, NT = T / kTile, g = h / (a.Hq / a.Hkv);
   const int i = qb * kChunk + tid / kPart;
-  const size_t rowT = (size_t)r * T, own = ((rowT + i) * a.Hq + h) * D + part;
+  const size_t rowT = (size_t)r * T, own = ((rowT + i) * a.Hq + h) * D;
   const float *Q = static_cast<const float*>(a.q), *K = static_cast<const float*>(a.k),
               *V = static_cast<const float*>(a.v), *dO = static_cast<const float*>(a.dout);
   const float qs = a.scale * kLog2e;
@@ -479,8 +500,8 @@ __global__ void __launch_bounds__(256) win_dq_kernel(AttnArgs a) {
   float q[DP], go[DP], dq[DP];
 #pragma unroll
   for (int d = 0; d < DP; ++d) {
-    q[d] = Q[own + d * kPart];
-    go[d] = dO[own + d * kPart];
+    q[d] = Q[own + chan(d, part)];
+    go[d] = dO[own + chan(d, part)];
     dq[d] = 0.f;
   }
   const int cnt = a.csr_cnt[(size_t)r * NT + qt];
@@ -503,14 +524,16 @@ __global__ void __launch_bounds__(256) win_dq_kernel(AttnArgs a) {
         lim[tid] = a.lim[rowT + k0 + tid];
       }
       __syncthreads();
-#pragma unroll 4
+#pragma unroll 2
       for (int c = 0; c < kChunk; ++c) {
-        const float *kr = Kc + c * D + part, *vr = Vc + c * D + part;
+        float kr[DP], vr[DP];
+        row_of<DP>(kr, Kc + c * D, part);
+        row_of<DP>(vr, Vc + c * D, part);
         float s = 0.f, dp = 0.f;
 #pragma unroll
         for (int d = 0; d < DP; ++d) {
-          s = fmaf(q[d], kr[d * kPart], s);
-          dp = fmaf(go[d], vr[d * kPart], dp);
+          s = fmaf(q[d], kr[d], s);
+          dp = fmaf(go[d], vr[d], dp);
         }
         s = join8(s);
         dp = join8(dp);
@@ -518,13 +541,13 @@ __global__ void __launch_bounds__(256) win_dq_kernel(AttnArgs a) {
         const float p = vis ? exp2f(s * qs - lse2) : 0.f;
         const float ds = p * (dp - dlt);
 #pragma unroll
-        for (int d = 0; d < DP; ++d) dq[d] = fmaf(ds, kr[d * kPart], dq[d]);
+        for (int d = 0; d < DP; ++d) dq[d] = fmaf(ds, kr[d], dq[d]);
       }
     }
   }
   float* dQ = static_cast<float*>(a.dq);
 #pragma unroll
-  for (int d = 0; d < DP; ++d) dQ[own + d * kPart] = dq[d] * a.scale;
+  for (int d = 0; d < DP; ++d) dQ[own + chan(d, part)] = dq[d] * a.scale;
 }
 
 template <int D>
