@@ -52,8 +52,8 @@ constexpr int kFlight = 4;          // pieces of a round per thread
 // Rounds on their way per thread, and blocks per SM: forward and backward 3
 // and 4 (48 KB in flight per block), the step of both passes 4 and 3, where
 // fewer rows in work keep more of them in L2.  Of 2..12 rounds and 1..8 blocks,
-// these measured best on rows of 151936 bf16 logits: 8192 rows' statistics 418 us,
-// 6.0 TB/s (462 without the ring), 4096 rows' step 416 us, 5.7 TB/s.
+// these measured best on rows of 151936 bf16 logits: 8192 rows' statistics 406 us,
+// 6.1 TB/s (462 without the ring), 4096 rows' step 410 us, 5.8 TB/s.
 constexpr int kPassRounds = 3, kPassBlocks = 4;
 constexpr int kStepRounds = 4, kStepBlocks = 3;
 constexpr int ring_bytes(int rounds) { return rounds * kFlight * kRowThreads * 16; }
@@ -838,7 +838,7 @@ bool off_type(const void* x, int dtype) {
 
 // Blocks of a row: more than one where the rows alone do not fill the GPU, while
 // a block keeps 16 KB; a cluster's meeting costs more than that of a block
-// (2048 rows: 99 us with one block each, 111 with two).
+// (2048 rows: 98 us with one block each, 111 with two).
 int split_of(int64_t rows, int64_t row_bytes) {
   int c = 1;
   while (c < kMaxSplit && rows * c < 608 && row_bytes / (2 * c) >= 16384) c *= 2;
@@ -847,7 +847,7 @@ int split_of(int64_t rows, int64_t row_bytes) {
 
 // For the step of both passes: the rows in work, kStepBlocks of 152 SMs over C,
 // have to stay in L2 from one pass to the next; beyond about 72 MB of its
-// 129 they do not (4096 rows of 304 KB: 507 us with one block, 416 with two, 551
+// 129 they do not (4096 rows of 304 KB: 507 us with one block, 410 with two, 551
 // with four, which meet too often).
 int step_split_of(int64_t rows, int64_t row_bytes) {
   int c = split_of(rows, row_bytes);
