@@ -138,8 +138,9 @@ __device__ __forceinline__ Part part_of(const T* row, int V, int rank, int C) {
 // ------------------------------------------------------------------ sums
 
 // m: largest raw logit; s, t: sums of 2^d and 2^d d, d = (logit - m) sl2.  The
-// difference comes first: it is near exact where 2^d counts, and a row of the
-// type's lowest value, as masks have it, overflows nowhere.
+// difference comes first: it is near exact where 2^d counts.  Beside a large
+// negative mask value (the type's lowest) d is huge or -inf and 2^d is 0; the
+// factor d of a sum is then held at kLowest, so that 0 times it is 0.
 struct Acc {
   float m, s, t;
 };
@@ -147,7 +148,7 @@ struct Acc {
 // Brings the sums of `a` to the reference of a larger maximum.
 __device__ __forceinline__ void rebase(Acc& a, float m, float sl2) {
   if (a.m != -INFINITY) {
-    const float dl = (a.m - m) * sl2, f = ex2(dl);
+    const float dl = fmaxf((a.m - m) * sl2, kLowest), f = ex2(dl);
     a.t = f * fmaf(dl, a.s, a.t);
     a.s *= f;
   }
