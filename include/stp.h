@@ -538,7 +538,7 @@ typedef struct {
   int32_t rotary_dim;  /* rotated channels, a multiple of 16 in [0, D]           */
   int32_t interleaved; /* 0: pairs (i, i + rotary_dim / 2); 1: pairs (2i, 2i + 1) */
   int32_t dtype;       /* STP_BF16 or STP_FP32, of every tensor but the weights  */
-  float eps;           /* in [0, 1]                                              */
+  float eps;           /* in [0, 1]; with 0 a vector of zeros has no norm (NaN)  */
   int64_t q_stride;    /* elements between tokens of q and dx_q: at least Hq * D, */
   int64_t k_stride;    /* of k and dx_k: at least Hkv * D; multiples of 16 bytes */
 } stp_qk_desc;

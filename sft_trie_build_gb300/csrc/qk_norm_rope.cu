@@ -424,7 +424,8 @@ __global__ void __launch_bounds__(kQkThreads, kQkBwdBlocks) qk_bwd_kernel(const 
     slot = slot + 1 == DEPTH ? 0 : slot + 1;
     const float ss = sum_group<G>(ss2.x + ss2.y);
     const float dot = sum_group<G>(dot2.x + dot2.y);
-    const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+    // a lane group without a head adds 0 to dw: with eps = 0 its r would be infinite
+    const float r = live ? rsqrtf(fmaf(ss, inv_d, p.eps)) : 0.f;
     const float m = -dot * inv_d * r * r * r;   // dx = g w r + x m
     const float2 r2 = make_float2(r, r), m2 = make_float2(m, m);
 #pragma unroll
