@@ -657,7 +657,10 @@ stp_status stp_token_stats_fwd(const stp_stats_desc* desc, const void* logits, c
  * with p = exp(z - lse); lse and entropy are the forward's.  d_entropy may be
  * NULL (zero).  d_logits (strided like logits, may be logits itself) is
  * written for every row: zeros where the target is negative or not below V,
- * or where lse is -inf (a row of nothing but -inf).
+ * or where lse is -inf (a row of nothing but -inf).  p follows lse as it is
+ * given, so it is exact to |lse| 2^-24 relative: 6e-5 at 1000; rows whose
+ * lse is beyond 10^5 or beyond float32 (all of a type's lowest value) have to be
+ * shifted towards zero before the forward.
  */
 stp_status stp_token_stats_bwd(const stp_stats_desc* desc, const void* logits, const int32_t* d_targets,
                                const float* lse, const float* entropy, const float* d_logprob,
@@ -699,7 +702,9 @@ stp_status stp_distill_workspace_size(const stp_distill_desc* desc, size_t* ws_b
  *                   counts as absent
  * stp_distill_bwd takes the forward's lse.  stp_distill_step is the forward
  * and the backward in one launch, for weights that are known beforehand: each
- * row's logits are read from memory once.
+ * row's logits are read from memory once, and p follows the differences to the
+ * row's maximum, at any size of the logits.  In stp_distill_bwd p is exact to
+ * |lse| 2^-24 relative, as in stp_token_stats_bwd.
  */
 stp_status stp_distill_fwd(const stp_distill_desc* desc, const void* logits, const int32_t* teacher_ids,
                            const float* teacher_logits, const uint8_t* d_loss_mask, float* loss, float* lse,

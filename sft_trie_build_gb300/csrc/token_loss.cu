@@ -753,7 +753,11 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
     ts.id[t] = id;
     ts.q[t] = q;
   }
-  float lse = 0.f;
+  // p = exp(x - ref) with x = scale z and ref = lse; with both passes at hand
+  // x = scale (z - m) and ref = ln s, which hold for logits of any size: lse
+  // itself carries p to |lse| 2^-24 only
+  float m = 0.f, ref;
+  bool none;   // nothing but -inf
   if (LSE) {
     float best;
     int round;
@@ -768,31 +772,37 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
       s = merge_all(sums, C, p.sl2);
     }
     const float ls = log_sum(s);
-    lse = fmaf(s.m, p.scale, ls);
+    m = s.m;
+    ref = ls;
+    none = s.s == 0.f;
     if (rank == 0) {
       const float lnq = fmaf(a - top, p.scale, -kLn2T * log2f(sum));
-      const float lnp = s.s == 0.f ? -INFINITY : fmaf(zk - s.m, p.scale, -ls);
+      const float lnp = none ? -INFINITY : fmaf(zk - m, p.scale, -ls);
       const float term = q != 0.f ? q * (lnq - lnp) : 0.f;
       const float loss = block_add(term, ts.red);
       if (t == 0) {
         p.loss[n] = loss;
-        p.lse[n] = lse;
+        p.lse[n] = fmaf(m, p.scale, ls);
       }
     }
   } else {
-    lse = p.lse_in[n];
+    ref = p.lse_in[n];
+    none = ref == -INFINITY;
   }
   if (GRAD) {
     const float scale = p.scale, g = p.g[n] * scale;
     __syncthreads();   // every zk is read before a logit may be overwritten
-    if (lse == -INFINITY) {   // nothing but -inf
+    if (none) {
       asm volatile("cp.async.wait_all;" ::: "memory");
       zero_row(out, p.V, rank, C);
       return;
     }
+    const auto prob = [=](float x) {
+      return LSE ? ex2(fmaf(x - m, p.sl2, -ref * kLog2eT)) : ex2(fmaf(x, scale, -ref) * kLog2eT);
+    };
     map_row(row, out, part, ring, [=](float* z, int, auto N) {
 #pragma unroll
-      for (int e = 0; e < N(); ++e) z[e] = g * ex2(fmaf(z[e], scale, -lse) * kLog2eT);
+      for (int e = 0; e < N(); ++e) z[e] = g * prob(z[e]);
     });
     __syncthreads();   // the block's stores before those of the listed ids
     const bool own = id >= part.lo && id < part.hi;
@@ -804,7 +814,7 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
           qs += ts.q[j];
           first = first && j >= t;
         }
-      if (own && first) put(out + id, g * (ex2(fmaf(zk, scale, -lse) * kLog2eT) - qs));
+      if (own && first) put(out + id, g * (prob(zk) - qs));
     }
   }
 }
