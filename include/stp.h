@@ -287,7 +287,9 @@ stp_status stp_read_tile_classes(const stp_attn_desc* desc, const void* d_tile_m
  *   q, k, v   device, dtype of desc, layouts above, 16-byte aligned
  *   o         device [R, T, Hq, D], same dtype;  lse device float32 [R, Hq, T]
  *   d_ws      device, fwd_ws_bytes
- * d_tile_meta must come from stp_classify on the same subtree_end.
+ * d_tile_meta must come from stp_classify on the same subtree_end; one that
+ * stp_classify_window wrote last sets the device error word here, in
+ * stp_attn_bwd and in stp_index_topk, and no output is valid.
  */
 stp_status stp_attn_fwd(const stp_attn_desc* desc, const void* q, const void* k, const void* v,
                         const int32_t* d_subtree_end, const void* d_tile_meta, void* o,
@@ -589,7 +591,9 @@ stp_status stp_qk_norm_rope_bwd(const stp_qk_desc* desc, const void* q, const vo
  * exactly what the sequence alone would see under the same window.  Outputs,
  * types, layouts, workspaces and errors are those of stp_classify,
  * stp_attn_fwd and stp_attn_bwd; window >= 1 and n_sink >= 0 (STP_EINVAL), and
- * all three calls of a batch take the same two.
+ * all three calls of a batch take the same two: the attention calls set their
+ * device error word, and write nothing, where tile_meta was last written for
+ * other values or by stp_classify.
  *   d_position_ids  device int32 [R, T] as written by stp_plan_write, 16-byte
  *                   aligned; a value outside [0, 2^30) sets tile_meta's device
  *                   error word

@@ -54,6 +54,7 @@ static stp_status fill_common(const stp_attn_desc* d, const int32_t* se, const v
   a.se = se;
   const TileMeta m = tile_meta_layout(d->n_rows, d->row_len / kTile);
   const char* base = static_cast<const char*>(tile_meta);
+  a.meta.kind = reinterpret_cast<const int32_t*>(base + m.kind);
   a.csr_cnt = reinterpret_cast<const int32_t*>(base + m.csr_cnt);
   a.csr = reinterpret_cast<const int32_t*>(base + m.csr);
   a.csc_cnt = reinterpret_cast<const int32_t*>(base + m.csc_cnt);
@@ -82,6 +83,8 @@ static stp_status set_window(const char* name, const Window* w, const stp_attn_d
     return fail(STP_EUNSUPPORTED, "%s: more than 2^31 - 1 tokens", name);
   if (misaligned(w->pos, 16)) return fail(STP_EINVAL, "%s: position_ids must be 16-byte aligned", name);
   a.pos = w->pos;
+  a.meta.window = clip_window(w->window);
+  a.meta.n_sink = w->n_sink;
   const TileMeta m = tile_meta_layout(d->n_rows, d->row_len / kTile);
   const char* base = static_cast<const char*>(tile_meta);
   a.lim = reinterpret_cast<const int32_t*>(base + m.lim);

@@ -45,8 +45,16 @@ __device__ __forceinline__ void stage_rows(float* dst, int ld, const Tin* src, s
   }
 }
 
+// A tile_meta of the other kind: reported, and the block returns.
+__device__ __forceinline__ bool refused(const AttnArgs& a) {
+  const bool other = other_kind(a.meta);
+  if (other && threadIdx.x == 0) atomicOr(a.err, kErrBadMeta);
+  return other;
+}
+
 template <typename Tin, int D>
 __global__ void __launch_bounds__(256) fwd_simt_kernel(AttnArgs a) {
+  if (refused(a)) return;
   constexpr int DH = D / 2;
   extern __shared__ float sm[];
   float* Ks = sm;                  // [128][D]
@@ -145,6 +153,7 @@ constexpr int kChunk = 32;  // query / key rows staged per step in the backward
 
 template <typename Tin, int D>
 __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
+  if (refused(a)) return;
   constexpr int DH = D / 2, LD = D + 1;
   extern __shared__ float sm[];
   float* Kown = sm;                 // [128][D+1]
@@ -226,6 +235,7 @@ __global__ void __launch_bounds__(256) dkdv_simt_kernel(AttnArgs a) {
 
 template <typename Tin, int D>
 __global__ void __launch_bounds__(256) dq_simt_kernel(AttnArgs a) {
+  if (refused(a)) return;
   constexpr int DH = D / 2, LD = D + 1;
   extern __shared__ float sm[];
   float* Qown = sm;                   // [128][D+1]
@@ -331,6 +341,7 @@ __device__ __forceinline__ uint32_t pair_word(const AttnArgs& a, int r, int NT, 
 
 template <int D>
 __global__ void __launch_bounds__(256) win_fwd_kernel(AttnArgs a) {
+  if (refused(a)) return;
   constexpr int DP = D / kPart;
   __shared__ __align__(16) float Kc[kChunk * D], Vc[kChunk * D];
   __shared__ int sec[kChunk], lim[kChunk];
@@ -409,6 +420,7 @@ __global__ void __launch_bounds__(256) win_fwd_kernel(AttnArgs a) {
 
 template <int D>
 __global__ void __launch_bounds__(256) win_dkdv_kernel(AttnArgs a) {
+  if (refused(a)) return;
   constexpr int DP = D / kPart;
   __shared__ __align__(16) float Qc[kChunk * D], dOc[kChunk * D];
   __shared__ float lse2[kChunk], dlt[kChunk];
@@ -484,6 +496,7 @@ __global__ void __launch_bounds__(256) win_dkdv_kernel(AttnArgs a) {
 
 template <int D>
 __global__ void __launch_bounds__(256) win_dq_kernel(AttnArgs a) {
+  if (refused(a)) return;
   constexpr int DP = D / kPart;
   __shared__ __align__(16) float Kc[kChunk * D], Vc[kChunk * D];
   __shared__ int sec[kChunk], lim[kChunk];

@@ -128,6 +128,7 @@ __device__ __forceinline__ void store_rows(uint32_t tm, float sc, uint8_t* stage
 struct FwdParams {
   int R, T, Hq, Hkv, NT, G, npairs;
   float scale_log2;
+  MetaKind meta;
   const int32_t* se;
   const int32_t* csr_cnt;
   const int32_t* csr;
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int h0 = g * p.G + 2 * pair;
   const int nh = min(2, p.G - 2 * pair);
   const int cnt = p.csr_cnt[(size_t)r * p.NT + qt];
+  const bool other = other_kind(p.meta);   // read along with cnt
   const int32_t* list = p.csr + ((size_t)r * p.NT + qt) * p.NT;
   const int row0 = r * p.T;  // first row of this packed row in the [R*T] views
 
@@ -206,6 +208,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (pad + kSmall + kFwdBigBytes > kSmemLimit || cnt <= 0 || cnt > p.NT) {
       *abort_flag = 1;
       atomicOr(p.err, cnt <= 0 || cnt > p.NT ? kErrBadList : kErrTmem);
+    }
+    if (other) {
+      *abort_flag = 1;
+      atomicOr(p.err, kErrBadMeta);
     }
     fence_mbar_init();
   }
@@ -653,6 +659,7 @@ struct BwdParams {
   int slot_heads;       // query heads per pair in a dS slot
   float scale_log2;
   int64_t cap;          // dS pairs per slot
+  MetaKind meta;
   const int32_t* se;
   const int32_t* csc_cnt;
   const int32_t* csc;
@@ -722,6 +729,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int gl = (int)(blockIdx.x % p.ng);  // kv head within this launch
   const int g = p.g0 + gl;
   const int cnt = p.csc_cnt[(size_t)r * p.NT + kt];
+  const bool other = other_kind(p.meta);   // read along with cnt
   const int32_t* list = p.csc + ((size_t)r * p.NT + kt) * p.NT;
   const int32_t* pairs = p.csc_pair + ((size_t)r * p.NT + kt) * p.NT;
   const int n_it = cnt * p.G;
@@ -735,6 +743,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if ((big_s & 1023u) != 0 || cnt <= 0 || cnt > p.NT) {
       *abort_flag = 1;
       atomicOr(p.err, (big_s & 1023u) != 0 ? kErrTmem : kErrBadList);
+    }
+    if (other) {
+      *abort_flag = 1;
+      atomicOr(p.err, kErrBadMeta);
     }
     fence_mbar_init();
   }
@@ -1073,6 +1085,7 @@ struct DqParams {
   int g0, ng;           // kv heads [g0, g0 + ng) of this launch
   int slot_heads;       // query heads per pair in a dS slot
   int64_t cap;          // dS pairs per slot
+  MetaKind meta;
   const int32_t* csr_cnt;
   const int32_t* csr;
   const int32_t* csr_off;
@@ -1132,6 +1145,7 @@ __global__ void __launch_bounds__(kDqThreads, PAIR ? 2 : 1)
   const int h0 = g * p.G + 4 * quad;
   const int nh = min(4, p.G - 4 * quad);
   const int cnt = p.csr_cnt[(size_t)r * p.NT + qt];
+  const bool other = other_kind(p.meta);   // read along with cnt
   const int32_t* list = p.csr + ((size_t)r * p.NT + qt) * p.NT;
   const int64_t pbase = (int64_t)p.row_base[r] + p.csr_off[(size_t)r * p.NT + qt];
   const int row0 = r * p.T;
@@ -1142,6 +1156,10 @@ __global__ void __launch_bounds__(kDqThreads, PAIR ? 2 : 1)
     if ((big_s & 1023u) != 0 || cnt <= 0 || cnt > p.NT) {
       *abort_flag = 1;
       atomicOr(p.err, (big_s & 1023u) != 0 ? kErrTmem : kErrBadList);
+    }
+    if (other) {
+      *abort_flag = 1;
+      atomicOr(p.err, kErrBadMeta);
     }
     fence_mbar_init();
   }
@@ -1322,6 +1340,7 @@ cudaError_t tc_fwd(const AttnArgs& a, cudaStream_t s) {
   p.G = a.Hq / a.Hkv;
   p.npairs = (p.G + 1) / 2;
   p.scale_log2 = a.scale * kLog2e;
+  p.meta = a.meta;
   p.se = a.se;
   p.csr_cnt = a.csr_cnt;
   p.csr = a.csr;
@@ -1412,6 +1431,7 @@ cudaError_t tc_bwd(const AttnArgs& a, cudaStream_t s) {
   p.scale_log2 = a.scale * kLog2e;
   p.scale = a.scale;
   p.cap = a.ds_cap;
+  p.meta = a.meta;
   p.se = a.se;
   p.csc_cnt = a.csc_cnt;
   p.csc = a.csc;
@@ -1437,6 +1457,7 @@ cudaError_t tc_bwd(const AttnArgs& a, cudaStream_t s) {
   q.nquad = (p.G + 3) / 4;
   q.slot_heads = grp.group_heads;
   q.cap = a.ds_cap;
+  q.meta = a.meta;
   q.csr_cnt = a.csr_cnt;
   q.csr = a.csr;
   q.csr_off = a.csr_off;

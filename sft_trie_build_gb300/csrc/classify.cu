@@ -271,7 +271,7 @@ extern "C" stp_status stp_classify(const stp_attn_desc* desc, const int32_t* d_s
   char* base = static_cast<char*>(d_tile_meta);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint32_t* err = reinterpret_cast<uint32_t*>(base + m.err);
-  cudaMemsetAsync(err, 0, 4, s);
+  cudaMemsetAsync(err, 0, m.kind + 8 - m.err, s);   // and the kind: no window
   dim3 grid(NT, desc->n_rows);
   tile_minmax_kernel<<<grid, 128, 0, s>>>(d_subtree_end, desc->row_len, NT,
                                           reinterpret_cast<int32_t*>(base + m.kmin),
@@ -377,7 +377,7 @@ extern "C" stp_status stp_classify_noalloc(const stp_attn_desc* desc, const int3
   char* base = static_cast<char*>(d_tile_meta);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint32_t* err = reinterpret_cast<uint32_t*>(base + m.err);
-  cudaMemsetAsync(err, 0, 4, s);
+  cudaMemsetAsync(err, 0, m.kind + 8 - m.err, s);   // and the kind: no window
   // every min / max entry is written before it is read: nothing to clear
   int32_t* kmin = scratch;
   int32_t* kmax = scratch + kNoAllocMaxTiles;

@@ -92,7 +92,7 @@ struct WindowArgs {
   int32_t *smin, *smax, *pmin, *pmax, *qmin, *lim;
   uint32_t* word;
   int8_t* cls;
-  int32_t *csr_cnt, *csr, *csc_cnt, *csc, *crank, *csr_off, *row_base, *pair_count, *ticket;
+  int32_t *csr_cnt, *csr, *csc_cnt, *csc, *crank, *csr_off, *row_base, *pair_count, *ticket, *kind;
   uint32_t* err;
 };
 
@@ -128,7 +128,11 @@ __global__ void __launch_bounds__(kTile) window_blocks_kernel(const WindowArgs a
   }
   if (tile == 0 && t == 0) {
     a.ticket[r] = 0;
-    if (r == 0) *a.pair_count = 0;
+    if (r == 0) {
+      *a.pair_count = 0;
+      a.kind[0] = a.window;
+      a.kind[1] = a.n_sink;
+    }
   }
 }
 
@@ -316,6 +320,7 @@ extern "C" stp_status stp_classify_window(const stp_attn_desc* desc, int32_t win
   a.row_base = ints(m.row_base);
   a.pair_count = ints(m.pair_count);
   a.ticket = ints(m.ticket);
+  a.kind = ints(m.kind);
   a.err = reinterpret_cast<uint32_t*>(base + m.err);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaMemsetAsync(a.err, 0, 4, s);

@@ -56,6 +56,7 @@ constexpr int kIdxPiece = 8;           // key tiles of one query tile's list per
 struct IdxParams {
   int R, T, NT, H, D, top_k, splits;   // splits: scoring CTAs per query tile
   int64_t cap;
+  MetaKind meta;
   const int32_t* se;
   const int32_t* csr_cnt;
   const int32_t* csr;
@@ -132,6 +133,7 @@ __global__ void __launch_bounds__(kIdxThreads, 1)
   const int qt = p.NT - 1 - rest / p.R;   // longest lists first
   const int r = rest % p.R;
   const int cnt = p.csr_cnt[(size_t)r * p.NT + qt];
+  const bool other = other_kind(p.meta);   // read along with cnt
   const int e0 = piece * kIdxPiece, e1 = cnt < e0 + kIdxPiece ? cnt : e0 + kIdxPiece;
   if (piece > 0 && e0 >= cnt) return;   // uniform over the CTA; piece 0 always checks the list
   const int32_t* list = p.csr + ((size_t)r * p.NT + qt) * p.NT;
@@ -145,6 +147,10 @@ __global__ void __launch_bounds__(kIdxThreads, 1)
     if ((big_s & 1023u) != 0 || cnt <= 0 || cnt > p.NT) {
       *abort_flag = 1;
       atomicOr(p.err, (big_s & 1023u) != 0 ? kErrTmem : kErrBadList);
+    }
+    if (other) {
+      *abort_flag = 1;
+      atomicOr(p.err, kErrBadMeta);
     }
     fence_mbar_init();
   }
@@ -343,8 +349,9 @@ __global__ void __launch_bounds__(kSelWarps * 32) index_select_kernel(const IdxP
   const int k = p.top_k;
   int32_t* oi = p.out_idx + ((size_t)r * p.T + i) * k;
   float* os = p.out_score + ((size_t)r * p.T + i) * k;
-  if (cnt <= 0 || cnt > p.NT || pbase + cnt > p.cap) {   // uniform over the CTA
-    if (threadIdx.x == 0) atomicOr(p.err, cnt <= 0 || cnt > p.NT ? kErrBadList : kErrCapacity);
+  const bool other = other_kind(p.meta);
+  if (other || cnt <= 0 || cnt > p.NT || pbase + cnt > p.cap) {   // uniform over the CTA
+    if (threadIdx.x == 0) atomicOr(p.err, other ? kErrBadMeta : cnt <= 0 || cnt > p.NT ? kErrBadList : kErrCapacity);
     for (int n = lane; n < k; n += 32) {
       oi[n] = -1;
       os[n] = -INFINITY;
@@ -522,6 +529,7 @@ extern "C" stp_status stp_index_topk(const stp_index_desc* desc, const void* q, 
   p.D = desc->head_dim;
   p.top_k = desc->top_k;
   p.cap = pair_capacity(desc->n_rows, NT, desc->max_tile_pairs);
+  p.meta = {reinterpret_cast<const int32_t*>(tm + m.kind), 0, 0};
   p.se = d_subtree_end;
   p.csr_cnt = reinterpret_cast<const int32_t*>(tm + m.csr_cnt);
   p.csr = reinterpret_cast<const int32_t*>(tm + m.csr);

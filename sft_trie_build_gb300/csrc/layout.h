@@ -3,6 +3,8 @@
 // tile_meta (caller-owned, written by stp_classify), for R rows of NT = T/128
 // tiles, each array 256-byte aligned:
 //   err        uint32                 device error word
+//   kind       int32 [2]              window and n_sink of stp_classify_window, 0 and 0 of
+//                                     stp_classify; 16 bytes after err
 //   cls        int8  [R][NT][NT]      0 EMPTY, 1 PARTIAL, 2 FULL (q-tile major)
 //   csr_cnt    int32 [R][NT]          non-empty key tiles per query tile
 //   csr        int32 [R][NT][NT]      (kt << 1) | partial, kt ascending
@@ -52,14 +54,16 @@ enum : int8_t { kEmpty = 0, kPartial = 1, kFull = 2 };
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct TileMeta {
-  size_t err, cls, csr_cnt, csr, csc_cnt, csc, kmin, kmax, crank, csr_off, row_base, csc_pair,
+  size_t err, kind, cls, csr_cnt, csr, csc_cnt, csc, kmin, kmax, crank, csr_off, row_base, csc_pair,
       pair_count, smin, smax, pmin, pmax, qmin, lim, word, ticket, total;
 };
 
 inline TileMeta tile_meta_layout(int64_t R, int64_t NT) {
   TileMeta m;
   size_t o = 0;
-  m.err = o;     o += 256;
+  m.err = o;
+  m.kind = o + 16;
+  o += 256;
   m.cls = o;     o += align256(size_t(R * NT * NT));
   m.csr_cnt = o; o += align256(size_t(R * NT) * 4);
   m.csr = o;     o += align256(size_t(R * NT * NT) * 4);
@@ -154,7 +158,20 @@ enum : uint32_t {
   kErrBadList = 1u << 2,        // a tile list entry out of range
   kErrTmem = 1u << 3,           // tensor-memory allocation returned an unusable address
   kErrBadPosition = 1u << 5,    // a position outside [0, 2^30)
-  kErrCapacity = 1u << 4        // more non-empty tile pairs than the dS workspace holds
+  kErrCapacity = 1u << 4,       // more non-empty tile pairs than the dS workspace holds
+  kErrBadMeta = 1u << 6         // tile_meta of the other kind, or of another window
 };
+
+// The classification that tile_meta holds, and the one that a call is for
+// (window and n_sink, 0 and 0 without a window).
+struct MetaKind {
+  const int32_t* kind;
+  int32_t window, n_sink;
+};
+#ifdef __CUDACC__
+__device__ __forceinline__ bool other_kind(const MetaKind& m) {
+  return m.kind[0] != m.window || m.kind[1] != m.n_sink;
+}
+#endif
 
 }  // namespace stp

@@ -5,6 +5,8 @@
 
 #include <cstdint>
 
+#include "layout.h"
+
 namespace stp {
 
 struct AttnArgs {
@@ -25,6 +27,7 @@ struct AttnArgs {
   const int32_t* lim;    // [R, T]: key j is near the queries at positions below lim[j]
   const uint32_t* word;  // [R, NT, NT]: classes of a tile's 32 x 32 blocks
   const int32_t* crank;  // [R, NT, NT]: place of a key tile in a query tile's list
+  MetaKind meta;         // tile_meta's classification and the call's
   const int32_t* csr_cnt;
   const int32_t* csr;
   const int32_t* csc_cnt;
