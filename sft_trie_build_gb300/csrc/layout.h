@@ -15,15 +15,15 @@
 //                                     csr list of qt (set for non-empty pairs)
 //   csr_off    int32 [R][NT]          non-empty pairs of the row before query tile qt
 //   row_base   int32 [R]              first pair index of the row
-//   csc_pair   int32 [R][NT][NT]      pair index of each csc entry
+//   csc_pair   int32 [R][NT][NT]      pair index of each csc entry (not with a window)
 //   pair_count int32                  non-empty pairs over all rows
 // and, written by stp_classify_window alone, with blocks of 32 tokens:
+//   word       uint32 [R][NT][NT]     classes of the 4 x 4 blocks of a tile (q-tile major):
+//                                     bits 2 (4 qb + kb) and up; in csc_pair's place
 //   smin, smax int32 [R][T/32]        min / max subtree_end over each block
 //   pmin, pmax int32 [R][T/32]        min / max position over each block
 //   qmin       int32 [R][T]           min position from the token's block start up to it
 //   lim        int32 [R][T]           a key's window: queries at positions below lim are near
-//   word       uint32 [R][NT][NT]     classes of the 4 x 4 blocks of a tile (q-tile major):
-//                                     bits 2 (4 qb + kb) and up
 //   ticket     int32 [R]              blocks of the row that have written their lists
 // A non-empty (query tile, key tile) pair has the index
 // row_base[r] + csr_off[r][qt] + (position of kt in the csr list of qt):
@@ -74,7 +74,7 @@ inline TileMeta tile_meta_layout(int64_t R, int64_t NT) {
   m.crank = o;   o += align256(size_t(R * NT * NT) * 4);
   m.csr_off = o; o += align256(size_t(R * NT) * 4);
   m.row_base = o; o += align256(size_t(R) * 4);
-  m.csc_pair = o; o += align256(size_t(R * NT * NT) * 4);
+  m.csc_pair = m.word = o; o += align256(size_t(R * NT * NT) * 4);
   m.pair_count = o; o += 256;
   m.smin = o;    o += align256(size_t(R * NT) * 16);
   m.smax = o;    o += align256(size_t(R * NT) * 16);
@@ -82,7 +82,6 @@ inline TileMeta tile_meta_layout(int64_t R, int64_t NT) {
   m.pmax = o;    o += align256(size_t(R * NT) * 16);
   m.qmin = o;    o += align256(size_t(R * NT) * kTile * 4);
   m.lim = o;     o += align256(size_t(R * NT) * kTile * 4);
-  m.word = o;    o += align256(size_t(R * NT * NT) * 4);
   m.ticket = o;  o += align256(size_t(R) * 4);
   m.total = o;
   return m;
