@@ -34,6 +34,7 @@
 
 #include "internal.h"
 #include "layout.h"
+#include "per_device.h"
 #include "tc.h"
 #include "tc_ptx.cuh"
 
@@ -1350,15 +1351,15 @@ cudaError_t tc_fwd(const AttnArgs& a, cudaStream_t s) {
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.lse = a.lse;
   p.err = a.err;
-  static bool attr = false;
-  if (!attr) {
+  static PerDevice limits;
+  const cudaError_t el = limits([] {
     cudaError_t e = cudaFuncSetAttribute(fwd_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmemLimit);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(fwd_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+    return e;
+  });
+  if (el != cudaSuccess) return el;
   const unsigned grid = (unsigned)(p.NT * p.R * p.Hkv * p.npairs);
   if (a.pos)
     fwd_tc_kernel<true><<<grid, kThreads, kSmemLimit, s>>>(mq, mk, mv, p);
@@ -1465,8 +1466,8 @@ cudaError_t tc_bwd(const AttnArgs& a, cudaStream_t s) {
   q.dq = static_cast<__nv_bfloat16*>(a.dq);
   q.scale = a.scale;
   q.err = a.err;
-  static bool attr = false;
-  if (!attr) {
+  static PerDevice limits;
+  const cudaError_t el = limits([] {
     cudaError_t e = cudaFuncSetAttribute(bwd_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(bwd_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
@@ -1474,9 +1475,9 @@ cudaError_t tc_bwd(const AttnArgs& a, cudaStream_t s) {
       e = cudaFuncSetAttribute(dq_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqSmem<false>);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(dq_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqSmem<true>);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+    return e;
+  });
+  if (el != cudaSuccess) return el;
   // The kv heads in grp.n groups, each on its own stream: a group's dQ pass
   // (HBM-bound) starts as soon as that group's dK/dV kernel is done and runs
   // while the other groups compute.  Group gi keeps its dS tiles in slot

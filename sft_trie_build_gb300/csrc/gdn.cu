@@ -45,6 +45,7 @@
 #include "gdn_common.h"
 #include "internal.h"
 #include "layout.h"
+#include "per_device.h"
 #include "tc_ptx.cuh"
 
 namespace stp {
@@ -1115,16 +1116,15 @@ stp_status gdn_forward(const stp_gdn_desc* desc, const void* plan, const void* d
        !make_map_2d(&mkt, p.kt, (int64_t)n_chunk * H * kGc, kGd, kGc) ||
        !make_map_2d(&mpm, p.pm, (int64_t)n_chunk * H * kGc, kGc, kGc)))
     return fail(STP_ECUDA, "stp_gdn_fwd: tensor map encoding failed");
-  static std::once_flag attr_once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(attr_once, [] {
-    attr_err = cudaFuncSetAttribute(gdn_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem);
-    if (attr_err == cudaSuccess)
-      attr_err = cudaFuncSetAttribute(gdn_conv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kConvSmem);
-    if (attr_err == cudaSuccess)
-      attr_err = cudaFuncSetAttribute(gdn_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStSmem);
+  static PerDevice limits;
+  cudaError_t e = limits([] {
+    cudaError_t err = cudaFuncSetAttribute(gdn_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrepSmem);
+    if (err == cudaSuccess)
+      err = cudaFuncSetAttribute(gdn_conv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kConvSmem);
+    if (err == cudaSuccess)
+      err = cudaFuncSetAttribute(gdn_state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStSmem);
+    return err;
   });
-  cudaError_t e = attr_err;
   if (e == cudaSuccess) e = cudaMemsetAsync(p.err, 0, 4, s);
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_gdn_fwd: %s", cudaGetErrorString(e));
   if (N > 0) {

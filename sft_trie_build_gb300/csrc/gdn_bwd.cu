@@ -40,6 +40,7 @@
 #include "gdn_common.h"
 #include "internal.h"
 #include "layout.h"
+#include "per_device.h"
 #include "tc_ptx.cuh"
 
 namespace stp {
@@ -1416,16 +1417,16 @@ extern "C" stp_status stp_gdn_bwd(const stp_gdn_desc* desc, const void* plan, co
        !map_2d(&mkt, p.kt, (int64_t)n_chunk * H * kC, kD, kC) ||
        !map_2d(&mpm, p.pm, (int64_t)n_chunk * H * kC, kC, kC)))
     return fail(STP_ECUDA, "stp_gdn_bwd: tensor map encoding failed");
-  static std::once_flag attr_once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(attr_once, [] {
-    attr_err = cudaFuncSetAttribute(gdn_bwd_walk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWkSmem);
-    if (attr_err == cudaSuccess)
-      attr_err = cudaFuncSetAttribute(gdn_bwd_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCkSmem);
-    if (attr_err == cudaSuccess)
-      attr_err = cudaFuncSetAttribute(gdn_bwd_token_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTkSmem);
+  static PerDevice limits;
+  e = limits([] {
+    cudaError_t err = cudaFuncSetAttribute(gdn_bwd_walk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWkSmem);
+    if (err == cudaSuccess)
+      err = cudaFuncSetAttribute(gdn_bwd_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCkSmem);
+    if (err == cudaSuccess)
+      err = cudaFuncSetAttribute(gdn_bwd_token_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTkSmem);
+    return err;
   });
-  if (attr_err != cudaSuccess) return fail(STP_ECUDA, "stp_gdn_bwd: %s", cudaGetErrorString(attr_err));
+  if (e != cudaSuccess) return fail(STP_ECUDA, "stp_gdn_bwd: %s", cudaGetErrorString(e));
   // pads keep dq^, dk^, dv = 0 (the chunk kernel writes real tokens only)
   e = cudaMemsetAsync(p.dqkv, 0, (size_t)N * C * 4, s);
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_gdn_bwd: %s", cudaGetErrorString(e));

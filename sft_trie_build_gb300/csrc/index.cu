@@ -37,6 +37,7 @@
 
 #include "internal.h"
 #include "layout.h"
+#include "per_device.h"
 #include "tc_ptx.cuh"
 
 namespace stp {
@@ -547,12 +548,12 @@ extern "C" stp_status stp_index_topk(const stp_index_desc* desc, const void* q, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaMemsetAsync(p.err, 0, 4, s);
   const int smem = p.H * 128 * p.D * 2 + 2 * 128 * p.D * 2 + kIdxSmallBytes;
-  static bool attr = false;
-  if (e == cudaSuccess && !attr) {
-    e = cudaFuncSetAttribute(index_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kIdxQBytesMax + 2 * 128 * 128 * 2 + kIdxSmallBytes);
-    attr = e == cudaSuccess;
-  }
+  static PerDevice limit;
+  if (e == cudaSuccess)
+    e = limit([] {
+      return cudaFuncSetAttribute(index_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  kIdxQBytesMax + 2 * 128 * 128 * 2 + kIdxSmallBytes);
+    });
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_index_topk: %s", cudaGetErrorString(e));
   const unsigned grid = (unsigned)(NT * desc->n_rows);
   p.splits = (NT + kIdxPiece - 1) / kIdxPiece;

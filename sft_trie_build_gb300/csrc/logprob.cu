@@ -29,6 +29,7 @@
 
 #include "internal.h"
 #include "layout.h"
+#include "per_device.h"
 #include "tc_ptx.cuh"
 
 namespace stp {
@@ -424,12 +425,11 @@ extern "C" stp_status stp_logprob_gather(const stp_logprob_desc* desc, const voi
   int dev = 0, n_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
-  static std::once_flag attr_once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(attr_once, [] {
-    attr_err = cudaFuncSetAttribute(logprob_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpSmem);
-  });
-  if (e == cudaSuccess) e = attr_err;
+  static PerDevice limit;
+  if (e == cudaSuccess)
+    e = limit([] {
+      return cudaFuncSetAttribute(logprob_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpSmem);
+    });
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (e == cudaSuccess) e = cudaMemsetAsync(ws, 0, 512, s);
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_logprob_gather: %s", cudaGetErrorString(e));

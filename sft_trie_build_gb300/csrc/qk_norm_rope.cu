@@ -31,6 +31,7 @@
 
 #include "internal.h"
 #include "layout.h"
+#include "per_device.h"
 #include "tc_ptx.cuh"
 
 namespace stp {
@@ -531,7 +532,7 @@ bool off16(const void* x) { return reinterpret_cast<uintptr_t>(x) & 15; }
 
 // Launches KERNEL<T, G, INTER> for the descriptor's type, vector width and
 // pairs; the dynamic shared memory RING(T) may pass the default limit, which is
-// raised once per kernel.
+// raised once per kernel and device.
 #define STP_QK_LAUNCH(KERNEL, GRID, RING)                                                          \
   do {                                                                                             \
     const int units = desc->head_dim / 16;                                                         \
@@ -555,8 +556,10 @@ bool off16(const void* x) { return reinterpret_cast<uintptr_t>(x) & 15; }
   } while (0)
 #define STP_QK_RUN(K, GRID, SMEM)                                                                  \
   do {                                                                                             \
-    static const cudaError_t allowed =                                                             \
-        cudaFuncSetAttribute((const void*)K, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);   \
+    static PerDevice limit;                                                                        \
+    const cudaError_t allowed = limit([] {                                                         \
+      return cudaFuncSetAttribute((const void*)K, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM); \
+    });                                                                                            \
     if (allowed != cudaSuccess) return fail(STP_ECUDA, "q/k norm: %s", cudaGetErrorString(allowed)); \
     K<<<GRID, kQkThreads, SMEM, s>>>(p);                                                           \
   } while (0)

@@ -29,11 +29,11 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <mutex>
 #include <type_traits>
 
 #include "internal.h"
 #include "layout.h"
+#include "per_device.h"
 #include "tc_ptx.cuh"
 
 namespace cg = cooperative_groups;
@@ -904,15 +904,13 @@ cudaError_t allow_rings_of() {
   return e;
 }
 
-// The kernels' dynamic shared memory, above the default limit: set once.
+// The kernels' dynamic shared memory, above the default limit.
 cudaError_t allow_rings() {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  std::call_once(once, [] {
-    err = allow_rings_of<__nv_bfloat16>();
-    if (err == cudaSuccess) err = allow_rings_of<float>();
+  static PerDevice limits;
+  return limits([] {
+    const cudaError_t e = allow_rings_of<__nv_bfloat16>();
+    return e == cudaSuccess ? allow_rings_of<float>() : e;
   });
-  return err;
 }
 
 cudaError_t launch(const void* kernel, int rounds, int64_t rows, int C, void* params, bool cluster, cudaStream_t s) {
