@@ -1108,10 +1108,11 @@ __device__ __forceinline__ uint64_t ds_desc(uint32_t addr) {
 
 enum { Q_KF = 0, Q_KE = 2, Q_DF = 4, Q_DE = 8, Q_DONE = 12, Q_DRAIN = 13, Q_COUNT = 14 };
 // shared memory: [K ring | dS ring] (1024-aligned) [barriers ...].  PAIR (groups
-// of one or two heads): rings of one and two tiles and 256 TMEM columns, so that
-// two CTAs share an SM and one's start and end (5 us of a block's 12) lie under
-// the other's products: 16 rows of 4096 tokens in a window of 512, 16 / 8 heads,
-// 285 us instead of 328, 5.8 TB/s; otherwise two and four tiles, 512 columns, one CTA.
+// of one or two heads, many short lists: tc_bwd): rings of one and two tiles and
+// 256 TMEM columns, so that two CTAs share an SM and one's start and end (5 us of
+// a block's 12) lie under the other's products: 16 rows of 4096 tokens in a window
+// of 512, 16 / 8 heads, 285 us instead of 328, 5.8 TB/s; otherwise two and four
+// tiles, 512 columns, one CTA.  The sums and their order are the same.
 template <bool PAIR>
 constexpr int kDqK = PAIR ? 1 : 2;
 template <bool PAIR>
@@ -1513,7 +1514,15 @@ cudaError_t tc_bwd(const AttnArgs& a, cudaStream_t s) {
     else
       bwd_tc_kernel<false><<<(unsigned)(p.NT * p.R * p.ng), kBwdThreads, kBwdSmem, sg>>>(mq, mk, mv, mdo, p);
     const unsigned n_dq = (unsigned)(p.NT * p.R * q.ng * q.nquad);
-    if (p.G <= 2)
+    // PAIR where its blocks are many and their lists short.  What it covers is
+    // the blocks' starts and ends, once for every two blocks in turn on an SM; its
+    // shorter rings cost some of every list entry, and a launch that fits the
+    // SMs as it is has nothing to cover.  Backward, groups of one head, 8 kv heads,
+    // in us, PAIR against one block per SM, by blocks of a launch and mean list:
+    // 256, 3: 238 / 254; 512, 5: 643 / 675; 512, 16: 1498 / 1541; 160, 5: 221 / 225;
+    // and the other way 128, 64: 1337 / 1274; 256, 16: 771 / 763; 192, 32: 1057 / 1045;
+    // 256, 64: 2520 / 2471; 512, 32 and 64 alike.
+    if (p.G <= 2 && 25 * p.cap <= (int64_t)n_dq * p.R * p.NT)
       dq_tc_kernel<true><<<n_dq, kDqThreads, kDqSmem<true>, sg>>>(mk, q);
     else
       dq_tc_kernel<false><<<n_dq, kDqThreads, kDqSmem<false>, sg>>>(mk, q);
