@@ -52,8 +52,8 @@ constexpr int kFlight = 4;          // pieces of a round per thread
 // Rounds on their way per thread, and blocks per SM: forward and backward 3
 // and 4 (48 KB in flight per block), the step of both passes 4 and 3, where
 // fewer rows in work keep more of them in L2.  Of 2..12 rounds and 1..8 blocks,
-// these measured best on rows of 151936 bf16 logits: 8192 rows' statistics 406 us,
-// 6.1 TB/s (462 without the ring), 4096 rows' step 410 us, 5.8 TB/s.
+// these measured best on rows of 151936 bf16 logits: 8192 rows' statistics 415 us,
+// 6.0 TB/s (462 without the ring), 4096 rows' step 411 us, 5.8 TB/s.
 constexpr int kPassRounds = 3, kPassBlocks = 4;
 constexpr int kStepRounds = 4, kStepBlocks = 3;
 constexpr int ring_bytes(int rounds) { return rounds * kFlight * kRowThreads * 16; }
