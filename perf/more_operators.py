@@ -366,9 +366,10 @@ def _kept64(x):
     n, c = x.shape
     x = torch.nn.functional.pad(x.double(), (0, -c % 32)).reshape(n, -1, 32)
     top = x.abs().amax(-1, keepdim=True)
-    scale = torch.exp2(torch.ceil(torch.log2(top / 448)).clamp(min=-117.0))
+    tiny = 1e-9   # beyond the error of log2 at powers of two, below the distance of any other value
+    scale = torch.exp2(torch.ceil(torch.log2(top / 448) - tiny).clamp(min=-117.0))
     v = x / scale
-    step = torch.exp2(torch.floor(torch.log2(v.abs())).clamp(min=-6.0) - 3)
+    step = torch.exp2(torch.floor(torch.log2(v.abs()) + tiny).clamp(min=-6.0) - 3)
     return (torch.round(v / step) * step * scale).reshape(n, -1)[:, :c]
 
 
