@@ -721,6 +721,161 @@ stp_status stp_distill_step(const stp_distill_desc* desc, const void* logits, co
                             float* loss, float* lse, void* d_logits, void* d_ws, void* stream);
 
 /*
+ * Clipped policy loss on rows of logits ([P1] materialization section: the
+ * loss mask marks the positions that score a trainable token; position x
+ * scores token x + 1).  With z = scale * logits[n], lp = z_target - ln sum_v
+ * exp(z_v), p = softmax(z) and H the entropy, as stp_token_stats_fwd defines
+ * them, and A = advantage[n]:
+ *   r = exp(lp - old_logprob[n])
+ *   kl[n] = exp(ref_logprob[n] - lp) - (ref_logprob[n] - lp) - 1
+ *   loss[n] = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A)
+ *             + kl_coef kl[n] - entropy_coef H
+ * and its gradient, with g = -A r where the minimum is r A, else 0 (at a
+ * border: -A r), plus kl_coef (1 - exp(ref_logprob[n] - lp)):
+ *   d_logits_v = d_loss[n] scale (g ([v = target] - p_v) + entropy_coef p_v (ln p_v + H))
+ * A negative target is a row that is not read: zeros in every output.  A row
+ * whose target has probability 0 (logprob -inf) has a gradient of zeros; a row
+ * that holds NaN or +inf gives NaN.  All sums are float32 in a fixed order.
+ */
+typedef struct {
+  int32_t n_rows;     /* N >= 0                                                  */
+  int32_t vocab;      /* V in [1, 2^24]                                          */
+  int64_t stride;     /* elements between rows of logits (and of d_logits), >= V */
+  int32_t dtype;      /* STP_BF16 or STP_FP32, of logits and d_logits            */
+  float scale;        /* positive, e.g. 1 / temperature                          */
+  float clip_low;     /* in [0, 1]                                               */
+  float clip_high;    /* in [0, 1e4]                                             */
+  float kl_coef;      /* in [0, 1e4]                                             */
+  float entropy_coef; /* in [-1e4, 1e4]                                          */
+} stp_policy_desc;
+
+/* Device workspace of stp_policy_fwd and stp_policy_step (their error word). */
+stp_status stp_policy_workspace_size(const stp_policy_desc* desc, size_t* ws_bytes);
+
+/*
+ *   logits        device [N, V], rows stride elements apart, any alignment of their type
+ *   d_targets     device int32 [N]
+ *   old_logprob   device float32 [N]: under the policy that sampled the tokens
+ *   ref_logprob   device float32 [N], or NULL: no KL term (kl_coef must be 0
+ *                 then, and kl is zeros)
+ *   advantage     device float32 [N]
+ *   loss, logprob, entropy, lse, kl   device float32 [N]; kl may be NULL
+ *   d_loss        device float32 [N]: the weight of each row's loss
+ *   d_logits      device, strided like logits; may be logits itself; every row
+ *                 is written
+ *   d_ws          device, 256-byte aligned; its first word is the device error
+ *                 word: a target >= V sets it; the row is not read, gives NaN
+ *                 and a gradient of zeros
+ * stp_policy_bwd takes the forward's logprob, entropy and lse.
+ * stp_policy_step is both in one launch, for weights that are known
+ * beforehand: each row's logits are read from memory once, and p follows the
+ * differences to the row's maximum, at any size of the logits.  In
+ * stp_policy_bwd p is exact to |lse| 2^-24 relative, as in stp_token_stats_bwd.
+ */
+stp_status stp_policy_fwd(const stp_policy_desc* desc, const void* logits, const int32_t* d_targets,
+                          const float* old_logprob, const float* ref_logprob, const float* advantage, float* loss,
+                          float* logprob, float* entropy, float* lse, float* kl, void* d_ws, void* stream);
+stp_status stp_policy_bwd(const stp_policy_desc* desc, const void* logits, const int32_t* d_targets,
+                          const float* old_logprob, const float* ref_logprob, const float* advantage,
+                          const float* logprob, const float* entropy, const float* lse, const float* d_loss,
+                          void* d_logits, void* stream);
+stp_status stp_policy_step(const stp_policy_desc* desc, const void* logits, const int32_t* d_targets,
+                           const float* old_logprob, const float* ref_logprob, const float* advantage,
+                           const float* d_loss, float* loss, float* logprob, float* entropy, float* lse, float* kl,
+                           void* d_logits, void* d_ws, void* stream);
+
+/*
+ * Token vectors of packed rows from a table, and the table's gradient ([P1]
+ * materialization section: rows carry token ids, pads the id 0):
+ *   out[n] = scale table[token[n]],
+ *   d_table[v] (+)= scale sum over n with token[n] = v of d_out[n].
+ * A negative token has a vector of zeros and no gradient.  Each output is
+ * rounded once; the gradient's sums are float32 in a fixed order (repeated
+ * calls give the same bits).
+ */
+typedef struct {
+  int32_t n_tokens; /* N in [0, 2^28] (rows of a batch back to back)          */
+  int32_t vocab;    /* V in [1, 2^24]                                         */
+  int32_t dim;      /* C, a multiple of 16 bytes in [16 bytes, 65536 elements] */
+  int32_t dtype;    /* STP_BF16 or STP_FP32, of table, out and d_out          */
+  float scale;      /* in [-1e6, 1e6]                                         */
+  int64_t stride;   /* elements between tokens of out and d_out: at least C, a
+                       multiple of 16 bytes                                   */
+} stp_embed_desc;
+
+/* Device workspace of stp_embed_bwd (its error word, the sorted tokens and the
+ * sums of tokens that occur often: about 16 N + N C / 4 bytes); stp_embed_fwd
+ * uses its first 256 bytes only. */
+stp_status stp_embed_workspace_size(const stp_embed_desc* desc, size_t* ws_bytes);
+
+/*
+ *   table         device [V, C];  out, d_out  device [N, C], rows stride apart
+ *   d_token_ids   device int32 [N]
+ *   accumulate    0: d_table is written in full, zeros for tokens that do not
+ *                 occur; else the sums are added to it, and rows of tokens that
+ *                 do not occur are not touched
+ *   d_table       device float32 [V, C]
+ *   d_ws          device, 256-byte aligned; its first word is the device error
+ *                 word: a token >= V sets it, and counts as negative
+ * table, out, d_out and d_table are 16-byte aligned.
+ */
+stp_status stp_embed_fwd(const stp_embed_desc* desc, const void* table, const int32_t* d_token_ids, void* out,
+                         void* d_ws, void* stream);
+stp_status stp_embed_bwd(const stp_embed_desc* desc, const void* d_out, const int32_t* d_token_ids,
+                         int32_t accumulate, float* d_table, void* d_ws, void* stream);
+
+/*
+ * Activations kept in 8 bits between the forward and the backward pass.  A
+ * checkpoint holds x [N, C] as e4m3 codes with one power-of-two scale for 32
+ * successive channels of a token (33/32 bytes an element): with a the largest
+ * magnitude of the 32 and s the smallest power of two, from 2^-117 on, with
+ * a <= 448 s,
+ *   x^ = s round_e4m3(x / s)   (to nearest, ties to even),
+ * so |x^ - x| <= max(2^-4 |x|, 2^-10 s).  32 channels that hold an infinity or a
+ * NaN return as NaN.  x^ is exact in bf16 (a magnitude that rounds to 2^128 is an
+ * infinity there, as in any rounding).  The layout is the library's own.
+ */
+typedef struct {
+  int32_t n_tokens; /* N in [0, 2^24]                         */
+  int32_t dim;      /* C in [1, 65536]                        */
+  int32_t dtype;    /* STP_BF16 or STP_FP32, of x             */
+  int64_t stride;   /* elements between tokens of x, >= C     */
+} stp_ckpt_desc;
+
+/* Bytes of a checkpoint: 2112 for every 64 tokens x 32 channels begun. */
+stp_status stp_ckpt_size(const stp_ckpt_desc* desc, size_t* ckpt_bytes);
+
+/*
+ * stp_ckpt_save stores x, stp_ckpt_load restores x^ (a part of a fused tensor
+ * may be read and written in place; what lies between is not touched).
+ *   x        device, rows stride elements apart, any alignment of its type
+ *   d_ckpt   device, stp_ckpt_size bytes, 256-byte aligned
+ * No workspace and no device checks.
+ */
+stp_status stp_ckpt_save(const stp_ckpt_desc* desc, const void* x, void* d_ckpt, void* stream);
+stp_status stp_ckpt_load(const stp_ckpt_desc* desc, const void* d_ckpt, void* x, void* stream);
+
+/*
+ * Weight gradient of a projection y = x W from its kept input:
+ *   d_w[c, m] (+)= sum_n x^[n, c] d_y[n, m]
+ * on the tensor cores: products of bf16 values (x^ is exact in bf16), float32
+ * sums in a fixed order for a given GPU.
+ *   cols         M in [1, 2^20]
+ *   d_ckpt       device, written by stp_ckpt_save (desc->dtype and stride are those
+ *                of x and not used here)
+ *   d_y          device bf16 [N, M], 16-byte aligned, rows y_stride elements
+ *                apart: at least M, a multiple of 8 (a part of a fused gradient
+ *                is read in place)
+ *   accumulate   0: d_w is written in full; else the products are added to it
+ *   d_w          device float32 [C, M]
+ *   d_ws         device, stp_ckpt_wgrad_workspace_size bytes for the current
+ *                device, 256-byte aligned; its first word is the device error word
+ */
+stp_status stp_ckpt_wgrad_workspace_size(const stp_ckpt_desc* desc, int32_t cols, size_t* ws_bytes);
+stp_status stp_ckpt_wgrad(const stp_ckpt_desc* desc, int32_t cols, const void* d_ckpt, const void* d_y,
+                          int64_t y_stride, int32_t accumulate, float* d_w, void* d_ws, void* stream);
+
+/*
  * Read the device error word of a workspace (fwd_ws or bwd_ws): synchronizes
  * the stream, then *out = STP_OK or STP_EDEVICE (a device check tripped or a
  * bounded wait ran out; the kernel returned early and its outputs are invalid).

@@ -1,0 +1,331 @@
+// Clipped policy loss on rows of logits, with a KL term towards a reference
+// policy and an entropy term: loss, gradient, and both in one launch.
+//
+// Per row, from one pass (logit_rows.cuh): lp = z_t - lse and the entropy H;
+//   r = exp(lp - old),  k = exp(ref - lp) - (ref - lp) - 1,
+//   loss = -min(r A, clip(r, 1 - lo, 1 + hi) A) + beta k - gamma H.
+// Its derivatives by lp and H are two numbers of the row,
+//   g = -A r [r not clipped] + beta (1 - exp(ref - lp))  and  -gamma,
+// so the gradient by a logit is
+//   dz_v = w scale (g ([v = t] - p_v) + gamma p_v (ln p_v + H)).
+//
+// Bound by memory, as token_loss.cu: forward one read, backward one read and
+// one write, the step one read and one write, its second pass out of L2.  The
+// token's own logit is put right by one store after the pass, so that the pass
+// compares no ids.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+#include "layout.h"
+#include "logit_rows.cuh"
+#include "per_device.h"
+#include "tc_ptx.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace stp {
+namespace {
+
+using namespace rows;
+using tc::ex2;
+
+struct PolicyParams {
+  int N, V, C;
+  int64_t stride;
+  float scale, sl2, low, high, beta, gamma;   // low = 1 - clip_low, high = 1 + clip_high
+  const void* z;
+  const int32_t* target;
+  const float* old_lp;
+  const float* ref_lp;   // may be null
+  const float* adv;
+  const float* w;
+  float* loss;
+  float* logprob;
+  float* entropy;
+  float* lse;
+  float* kl;             // may be null
+  // backward
+  const float* lp_in;
+  const float* ent_in;
+  const float* lse_in;
+  void* dz;
+  uint32_t* err;
+  bool check;   // a block past the rows checks all targets
+};
+
+// exp(x) - x - 1 without the cancellation near 0: its series to x^9 / 9!, which
+// is within 2^-24 of it on [-1/2, 1/2].  Far up the rest is below exp(x)'s last
+// bit (and infinity stays one).
+__device__ __forceinline__ float exp_rest(float x) {
+  if (x > 40.f) return expm1f(x);
+  if (fabsf(x) > 0.5f) return expm1f(x) - x;
+  float s = 1.f / 362880;
+  s = fmaf(s, x, 1.f / 40320);
+  s = fmaf(s, x, 1.f / 5040);
+  s = fmaf(s, x, 1.f / 720);
+  s = fmaf(s, x, 1.f / 120);
+  s = fmaf(s, x, 1.f / 24);
+  s = fmaf(s, x, 1.f / 6);
+  s = fmaf(s, x, 0.5f);
+  return s * x * x;
+}
+
+// The terms of a row and their derivative by lp.
+struct Terms {
+  float loss, kl, g;   // loss without the entropy term
+};
+
+__device__ __forceinline__ Terms terms_of(const PolicyParams& p, int n, float lp) {
+  const float a = p.adv[n], r = expf(lp - p.old_lp[n]);
+  const float bound = a >= 0.f ? p.high : p.low;
+  const bool out = a >= 0.f ? r > bound : r < bound;
+  Terms t;
+  t.loss = -a * (out ? bound : r);
+  t.g = out ? 0.f : -a * r;
+  t.kl = 0.f;
+  if (p.ref_lp) {
+    const float x = p.ref_lp[n] - lp;
+    t.kl = exp_rest(x);
+    if (p.beta != 0.f) {   // 0 times an infinite term is no term
+      t.loss = fmaf(p.beta, t.kl, t.loss);
+      t.g = fmaf(-p.beta, expm1f(x), t.g);
+    }
+  }
+  return t;
+}
+
+// Forward (LSE), backward (GRAD) or both.  MANY: several blocks per row.
+template <typename T, bool LSE, bool GRAD, bool MANY>
+__global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPassBlocks)
+    policy_kernel(const PolicyParams p) {
+  __shared__ Acc red[kRowWarps];
+  __shared__ Acc sums[kMaxSplit];   // of the row's blocks
+  extern __shared__ uint4 buffer[];
+  const int C = MANY ? p.C : 1, n = (int)(blockIdx.x / C), rank = MANY ? (int)(blockIdx.x % C) : 0, t = threadIdx.x;
+  if (LSE && n == p.N) {
+    if (rank == 0) check_below(p.N, p.V, p.err, [&](int64_t i) { return p.target[i]; });
+    return;
+  }
+  const T* row = static_cast<const T*>(p.z) + (int64_t)n * p.stride;
+  T* out = GRAD ? static_cast<T*>(p.dz) + (int64_t)n * p.stride : nullptr;
+  const int target = p.target[n];
+  if (target < 0 || target >= p.V) {   // the same for every block of the row
+    if (LSE && rank == 0 && t == 0) {
+      const float x = target < 0 ? 0.f : NAN;
+      p.loss[n] = p.logprob[n] = p.entropy[n] = p.lse[n] = x;
+      if (p.kl) p.kl[n] = x;
+      if (!p.check && target >= p.V) atomicOr(p.err, kErrBadList);
+    }
+    if (GRAD) zero_row(out, p.V, rank, C);
+    return;
+  }
+  const Part part = part_of(row, p.V, rank, C);
+  const auto ring = ring_of<LSE && GRAD ? kStepRounds : kPassRounds>(buffer, row, part);
+  ring.start(part.b0 + t);
+  if (LSE && MANY) cg::this_cluster().barrier_arrive();   // this block runs: others may write to it
+  const bool mine = target >= part.lo && target < part.hi;
+  // backward alone: other blocks may write over what is not their part already
+  const float zt = LSE || mine ? to_f(row[target]) : 0.f;
+  // ln p = scale (x - m) - ref: with both passes at hand m is the row's maximum
+  // and ref = ln sum exp(z - scale m), which hold for logits of any size
+  float m = 0.f, ref, ent, lp;
+  if (LSE) {
+    float best;
+    int round;
+    Acc s = pass<T, true, false>(row, part, ring, p.sl2, best, round);
+    if (GRAD) ring.start(part.b0 + t);   // again, now out of L2
+    s = block_sum(s, red, p.sl2);
+    if (MANY) {
+      cg::cluster_group cl = cg::this_cluster();
+      cl.barrier_wait();
+      if (t < C) *cl.map_shared_rank(sums + rank, t) = s;
+      cl.sync();
+      s = merge_all(sums, C, p.sl2);
+    }
+    const bool none = s.m == -INFINITY && s.s == 0.f;   // nothing but -inf
+    m = s.m;
+    ref = log_sum(s);
+    lp = none && !isnan(zt) ? -INFINITY : fmaf(zt - m, p.scale, -ref);
+    ent = none ? 0.f : kLn2T * (log2f(s.s) - s.t / s.s);
+    if (rank == 0 && t == 0) {
+      p.lse[n] = none ? -INFINITY : fmaf(m, p.scale, ref);
+      p.logprob[n] = lp;
+      p.entropy[n] = ent;
+    }
+  } else {
+    ref = p.lse_in[n];
+    lp = p.lp_in[n];
+    ent = p.ent_in[n];
+  }
+  const Terms term = terms_of(p, n, lp);
+  if (LSE && rank == 0 && t == 0) {
+    p.loss[n] = p.gamma != 0.f ? fmaf(-p.gamma, ent, term.loss) : term.loss;
+    if (p.kl) p.kl[n] = term.kl;
+  }
+  if (GRAD) {
+    __syncthreads();   // every zt is read before a logit may be overwritten
+    if (lp == -INFINITY) {   // no step can raise it
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      zero_row(out, p.V, rank, C);
+      return;
+    }
+    const float w = p.w[n] * p.scale, g = w * term.g;
+    // dz = p (h ln p + c), and g more for the token itself
+    const float h = w * p.gamma, c = p.gamma != 0.f ? fmaf(h, ent, -g) : -g;
+    const float shift = -ref * kLog2eT, scale = p.scale, sl2 = p.sl2, h2 = h * kLn2T;
+    const auto grad = [=](float x) {
+      const float l2 = LSE ? fmaf(x - m, sl2, shift) : fmaf(x, scale, -ref) * kLog2eT;
+      return ex2(l2) * fmaf(h2, fmaxf(l2, -1e30f), c);
+    };
+    map_row(row, out, part, ring, [=](float* z, int, auto N) {
+#pragma unroll
+      for (int e = 0; e < N(); ++e) z[e] = grad(z[e]);
+    });
+    __syncthreads();   // the block's stores before that of the token
+    if (mine && t == 0) put(out + target, grad(zt) + g);
+  }
+}
+
+// ------------------------------------------------------------------- host
+
+stp_status check_policy(const stp_policy_desc* d) {
+  if (!d) return fail(STP_EINVAL, "policy descriptor is NULL");
+  if (!(d->clip_low >= 0.f && d->clip_low <= 1.f) || !(d->clip_high >= 0.f && d->clip_high <= 1e4f))
+    return fail(STP_EINVAL, "clip_low must lie in [0, 1] and clip_high in [0, 1e4]");
+  if (!(d->kl_coef >= 0.f && d->kl_coef <= 1e4f) || !(d->entropy_coef >= -1e4f && d->entropy_coef <= 1e4f))
+    return fail(STP_EINVAL, "kl_coef must lie in [0, 1e4] and entropy_coef in [-1e4, 1e4]");
+  return check_rows(d->n_rows, d->vocab, d->stride, d->dtype, d->scale);
+}
+
+template <typename T>
+const void* policy_of(bool lse, bool grad, bool many) {
+  if (!lse) return (const void*)policy_kernel<T, false, true, true>;
+  if (!grad) return many ? (const void*)policy_kernel<T, true, false, true> : (const void*)policy_kernel<T, true, false, false>;
+  return many ? (const void*)policy_kernel<T, true, true, true> : (const void*)policy_kernel<T, true, true, false>;
+}
+
+// The kernels' dynamic shared memory, above the default limit.
+cudaError_t allow_policy() {
+  static PerDevice limits;
+  return limits([] {
+    cudaError_t e = cudaSuccess;
+    for (const bool lse : {false, true})
+      for (const bool grad : {false, true})
+        for (const bool many : {false, true})
+          for (const void* k : {policy_of<__nv_bfloat16>(lse, grad, many), policy_of<float>(lse, grad, many)})
+            if (e == cudaSuccess)
+              e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       ring_bytes(lse && grad ? kStepRounds : kPassRounds));
+    return e;
+  });
+}
+
+// What the three calls share; p holds the pointers.
+stp_status policy(const char* name, const stp_policy_desc* d, PolicyParams p, void* ws, bool fwd, bool grad,
+                  void* stream) {
+  clear_error();
+  stp_status st = check_policy(d);
+  if (st) return st;
+  if (fwd && (!ws || reinterpret_cast<uintptr_t>(ws) & 255))
+    return fail(STP_EINVAL, "%s: the workspace must be 256-byte aligned", name);
+  if (d->n_rows > 0 &&
+      (!p.z || !p.target || !p.old_lp || !p.adv || (fwd && (!p.loss || !p.logprob || !p.entropy || !p.lse)) ||
+       (grad && (!p.w || !p.dz)) || (!fwd && (!p.lp_in || !p.ent_in || !p.lse_in))))
+    return fail(STP_EINVAL, "%s: NULL device pointer", name);
+  if (d->kl_coef != 0.f && d->n_rows > 0 && !p.ref_lp)
+    return fail(STP_EINVAL, "%s: kl_coef needs ref_logprob", name);
+  if (off_type(p.z, d->dtype) || off_type(p.dz, d->dtype))
+    return fail(STP_EINVAL, "%s: logits misaligned for their type", name);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  p.check = fwd && d->n_rows > 0 && d->n_rows <= kCheckMost;
+  cudaError_t e = fwd && !p.check ? cudaMemsetAsync(ws, 0, 4, s) : cudaSuccess;
+  if (e == cudaSuccess && d->n_rows > 0) {
+    p.N = d->n_rows;
+    p.V = d->vocab;
+    p.stride = d->stride;
+    p.scale = d->scale;
+    p.sl2 = d->scale * kLog2eT;
+    p.low = 1.f - d->clip_low;
+    p.high = 1.f + d->clip_high;
+    p.beta = d->kl_coef;
+    p.gamma = d->entropy_coef;
+    p.err = static_cast<uint32_t*>(ws);
+    const int64_t bytes = row_bytes(p.V, d->dtype);
+    const bool both = fwd && grad;
+    p.C = both ? step_split_of(p.N, bytes) : split_of(p.N, bytes);
+    const void* k = d->dtype == STP_BF16 ? policy_of<__nv_bfloat16>(fwd, grad, p.C > 1)
+                                         : policy_of<float>(fwd, grad, p.C > 1);
+    e = allow_policy();
+    if (e == cudaSuccess) e = launch_rows(k, both ? kStepRounds : kPassRounds, p.N + p.check, p.C, &p, fwd, s);
+  }
+  if (e != cudaSuccess) return fail(STP_ECUDA, "%s: %s", name, cudaGetErrorString(e));
+  return STP_OK;
+}
+
+PolicyParams given(const void* logits, const int32_t* targets, const float* old_lp, const float* ref_lp,
+                   const float* adv) {
+  PolicyParams p{};
+  p.z = logits;
+  p.target = targets;
+  p.old_lp = old_lp;
+  p.ref_lp = ref_lp;
+  p.adv = adv;
+  return p;
+}
+
+}  // namespace
+}  // namespace stp
+
+using namespace stp;
+
+extern "C" stp_status stp_policy_workspace_size(const stp_policy_desc* desc, size_t* ws_bytes) {
+  clear_error();
+  stp_status st = check_policy(desc);
+  if (st) return st;
+  if (!ws_bytes) return fail(STP_EINVAL, "stp_policy_workspace_size: NULL output");
+  *ws_bytes = 256;
+  return STP_OK;
+}
+
+extern "C" stp_status stp_policy_fwd(const stp_policy_desc* desc, const void* logits, const int32_t* d_targets,
+                                     const float* old_logprob, const float* ref_logprob, const float* advantage,
+                                     float* loss, float* logprob, float* entropy, float* lse, float* kl, void* d_ws,
+                                     void* stream) {
+  PolicyParams p = given(logits, d_targets, old_logprob, ref_logprob, advantage);
+  p.loss = loss;
+  p.logprob = logprob;
+  p.entropy = entropy;
+  p.lse = lse;
+  p.kl = kl;
+  return policy("stp_policy_fwd", desc, p, d_ws, true, false, stream);
+}
+
+extern "C" stp_status stp_policy_bwd(const stp_policy_desc* desc, const void* logits, const int32_t* d_targets,
+                                     const float* old_logprob, const float* ref_logprob, const float* advantage,
+                                     const float* logprob, const float* entropy, const float* lse,
+                                     const float* d_loss, void* d_logits, void* stream) {
+  PolicyParams p = given(logits, d_targets, old_logprob, ref_logprob, advantage);
+  p.lp_in = logprob;
+  p.ent_in = entropy;
+  p.lse_in = lse;
+  p.w = d_loss;
+  p.dz = d_logits;
+  return policy("stp_policy_bwd", desc, p, nullptr, false, true, stream);
+}
+
+extern "C" stp_status stp_policy_step(const stp_policy_desc* desc, const void* logits, const int32_t* d_targets,
+                                      const float* old_logprob, const float* ref_logprob, const float* advantage,
+                                      const float* d_loss, float* loss, float* logprob, float* entropy, float* lse,
+                                      float* kl, void* d_logits, void* d_ws, void* stream) {
+  PolicyParams p = given(logits, d_targets, old_logprob, ref_logprob, advantage);
+  p.loss = loss;
+  p.logprob = logprob;
+  p.entropy = entropy;
+  p.lse = lse;
+  p.kl = kl;
+  p.w = d_loss;
+  p.dz = d_logits;
+  return policy("stp_policy_step", desc, p, d_ws, true, true, stream);
+}

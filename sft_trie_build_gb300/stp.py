@@ -35,6 +35,9 @@ EXPORTED = ["stp_pack", "stp_plan_info", "stp_plan_write", "stp_plan_rows_of", "
             "stp_count_window_tile_pairs", "stp_classify_window", "stp_attn_window_fwd", "stp_attn_window_bwd",
             "stp_token_stats_workspace_size", "stp_token_stats_fwd", "stp_token_stats_bwd",
             "stp_distill_workspace_size", "stp_distill_fwd", "stp_distill_bwd", "stp_distill_step",
+            "stp_policy_workspace_size", "stp_policy_fwd", "stp_policy_bwd", "stp_policy_step",
+            "stp_embed_workspace_size", "stp_embed_fwd", "stp_embed_bwd",
+            "stp_ckpt_size", "stp_ckpt_save", "stp_ckpt_load", "stp_ckpt_wgrad_workspace_size", "stp_ckpt_wgrad",
             "stp_device_status", "stp_last_error", "stp_version"]
 
 
@@ -81,6 +84,22 @@ class StatsDesc(ctypes.Structure):
 class DistillDesc(ctypes.Structure):
     _fields_ = [("n_rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("stride", ctypes.c_int64),
                 ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("n_teacher", ctypes.c_int32)]
+
+
+class PolicyDesc(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("clip_low", ctypes.c_float),
+                ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float), ("entropy_coef", ctypes.c_float)]
+
+
+class EmbedDesc(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("vocab", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("stride", ctypes.c_int64)]
+
+
+class CkptDesc(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("stride", ctypes.c_int64)]
 
 
 class AttnDesc(ctypes.Structure):
@@ -198,6 +217,16 @@ def lib():
         L.stp_distill_bwd.restype = st
         L.stp_distill_step.argtypes = [ctypes.POINTER(DistillDesc)] + [_P] * 10
         L.stp_distill_step.restype = st
+        policy, embed, ckpt = (ctypes.POINTER(x) for x in (PolicyDesc, EmbedDesc, CkptDesc))
+        for call, args in (("stp_policy_workspace_size", [policy, _SZ]), ("stp_policy_fwd", [policy] + [_P] * 12),
+                           ("stp_policy_bwd", [policy] + [_P] * 11), ("stp_policy_step", [policy] + [_P] * 14),
+                           ("stp_embed_workspace_size", [embed, _SZ]), ("stp_embed_fwd", [embed] + [_P] * 5),
+                           ("stp_embed_bwd", [embed, _P, _P, i32, _P, _P, _P]),
+                           ("stp_ckpt_size", [ckpt, _SZ]), ("stp_ckpt_save", [ckpt] + [_P] * 3),
+                           ("stp_ckpt_load", [ckpt] + [_P] * 3), ("stp_ckpt_wgrad_workspace_size", [ckpt, i32, _SZ]),
+                           ("stp_ckpt_wgrad", [ckpt, i32, _P, _P, ctypes.c_int64, i32, _P, _P, _P])):
+            getattr(L, call).argtypes = args
+            getattr(L, call).restype = st
         L.stp_device_status.argtypes = [_P, _P, ctypes.POINTER(ctypes.c_int32)]
         L.stp_device_status.restype = st
         L.stp_last_error.argtypes = []
@@ -691,6 +720,93 @@ def stp_distill_step(desc: DistillDesc, logits, teacher_ids, teacher_logits, los
     _check(lib().stp_distill_step(ctypes.byref(desc), _dptr(logits), _dptr(teacher_ids), _dptr(teacher_logits),
                                   _dptr(loss_mask), _dptr(d_loss), _dptr(loss), _dptr(lse), _dptr(d_logits),
                                   _dptr(ws), _stream(stream)), "stp_distill_step")
+
+
+def policy_desc(n_rows, vocab, dtype=STP_BF16, scale=1.0, clip_low=0.2, clip_high=0.2, kl_coef=0.0, entropy_coef=0.0,
+                stride=None) -> PolicyDesc:
+    return PolicyDesc(n_rows, vocab, vocab if stride is None else stride, dtype, scale, clip_low, clip_high, kl_coef,
+                      entropy_coef)
+
+
+def stp_policy_workspace_size(desc: PolicyDesc) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().stp_policy_workspace_size(ctypes.byref(desc), ctypes.byref(out)), "stp_policy_workspace_size")
+    return out.value
+
+
+def stp_policy_fwd(desc: PolicyDesc, logits, targets, old_logprob, ref_logprob, advantage, loss, logprob, entropy, lse,
+                   kl, ws, stream=None):
+    """ref_logprob None: no KL term; kl may be None."""
+    _check(lib().stp_policy_fwd(ctypes.byref(desc), _dptr(logits), _dptr(targets), _dptr(old_logprob),
+                                _dptr(ref_logprob), _dptr(advantage), _dptr(loss), _dptr(logprob), _dptr(entropy),
+                                _dptr(lse), _dptr(kl), _dptr(ws), _stream(stream)), "stp_policy_fwd")
+
+
+def stp_policy_bwd(desc: PolicyDesc, logits, targets, old_logprob, ref_logprob, advantage, logprob, entropy, lse, d_loss,
+                   d_logits, stream=None):
+    _check(lib().stp_policy_bwd(ctypes.byref(desc), _dptr(logits), _dptr(targets), _dptr(old_logprob),
+                                _dptr(ref_logprob), _dptr(advantage), _dptr(logprob), _dptr(entropy), _dptr(lse),
+                                _dptr(d_loss), _dptr(d_logits), _stream(stream)), "stp_policy_bwd")
+
+
+def stp_policy_step(desc: PolicyDesc, logits, targets, old_logprob, ref_logprob, advantage, d_loss, loss, logprob,
+                    entropy, lse, kl, d_logits, ws, stream=None):
+    _check(lib().stp_policy_step(ctypes.byref(desc), _dptr(logits), _dptr(targets), _dptr(old_logprob),
+                                 _dptr(ref_logprob), _dptr(advantage), _dptr(d_loss), _dptr(loss), _dptr(logprob),
+                                 _dptr(entropy), _dptr(lse), _dptr(kl), _dptr(d_logits), _dptr(ws), _stream(stream)),
+           "stp_policy_step")
+
+
+def embed_desc(n_tokens, vocab, dim, dtype=STP_BF16, scale=1.0, stride=None) -> EmbedDesc:
+    return EmbedDesc(n_tokens, vocab, dim, dtype, scale, dim if stride is None else stride)
+
+
+def stp_embed_workspace_size(desc: EmbedDesc) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().stp_embed_workspace_size(ctypes.byref(desc), ctypes.byref(out)), "stp_embed_workspace_size")
+    return out.value
+
+
+def stp_embed_fwd(desc: EmbedDesc, table, token_ids, out, ws, stream=None):
+    _check(lib().stp_embed_fwd(ctypes.byref(desc), _dptr(table), _dptr(token_ids), _dptr(out), _dptr(ws),
+                               _stream(stream)), "stp_embed_fwd")
+
+
+def stp_embed_bwd(desc: EmbedDesc, d_out, token_ids, accumulate, d_table, ws, stream=None):
+    """accumulate: add to d_table (float32 [vocab, dim]) instead of writing it in full."""
+    _check(lib().stp_embed_bwd(ctypes.byref(desc), _dptr(d_out), _dptr(token_ids), int(accumulate), _dptr(d_table),
+                               _dptr(ws), _stream(stream)), "stp_embed_bwd")
+
+
+def ckpt_desc(n_tokens, dim, dtype=STP_BF16, stride=None) -> CkptDesc:
+    return CkptDesc(n_tokens, dim, dtype, dim if stride is None else stride)
+
+
+def stp_ckpt_size(desc: CkptDesc) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().stp_ckpt_size(ctypes.byref(desc), ctypes.byref(out)), "stp_ckpt_size")
+    return out.value
+
+
+def stp_ckpt_save(desc: CkptDesc, x, ckpt, stream=None):
+    _check(lib().stp_ckpt_save(ctypes.byref(desc), _dptr(x), _dptr(ckpt), _stream(stream)), "stp_ckpt_save")
+
+
+def stp_ckpt_load(desc: CkptDesc, ckpt, x, stream=None):
+    _check(lib().stp_ckpt_load(ctypes.byref(desc), _dptr(ckpt), _dptr(x), _stream(stream)), "stp_ckpt_load")
+
+
+def stp_ckpt_wgrad_workspace_size(desc: CkptDesc, cols: int) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().stp_ckpt_wgrad_workspace_size(ctypes.byref(desc), cols, ctypes.byref(out)),
+           "stp_ckpt_wgrad_workspace_size")
+    return out.value
+
+
+def stp_ckpt_wgrad(desc: CkptDesc, cols: int, ckpt, d_y, y_stride: int, accumulate, d_w, ws, stream=None):
+    """accumulate: add to d_w (float32 [dim, cols]) instead of writing it in full."""
+    _check(lib().stp_ckpt_wgrad(ctypes.byref(desc), cols, _dptr(ckpt), _dptr(d_y), y_stride, int(accumulate), _dptr(d_w),
+                                _dptr(ws), _stream(stream)), "stp_ckpt_wgrad")
 
 
 def stp_device_status(ws, stream=None) -> int:
