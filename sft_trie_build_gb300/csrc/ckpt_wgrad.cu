@@ -6,16 +6,29 @@
 // float32 on the tensor cores (tcgen05, M = 128 channels, N <= 256 columns of
 // dY, K = tokens).
 //
-// Operand A is never in shared memory: a warp owns 32 channels, a lane one of them
-// (a TMEM lane, too), reads its codes of 64 tokens straight from the checkpoint, turns them to bf16
-// (ckpt.h) and stores them to TMEM.  dY arrives by TMA as it lies, tokens x
-// columns (MN-major, 128-byte swizzle).  TMEM: 256 columns of sums, then one
-// 32-column stage of A for every stage of dY in shared memory.
+// Two blocks of a cluster multiply a tile of 256 channels x up to 256 columns
+// together (cta_group::2): each holds the sums of its 128 channels in TMEM and half of
+// dY's columns in shared memory.  Operand A is in TMEM, too: a warp owns 32
+// channels, a lane one of them (a TMEM lane), reads the codes of 64 tokens from
+// shared memory, turns them to bf16 (ckpt.h) and stores them to TMEM, eight stages of 32
+// columns behind the 256 columns of sums.  So shared memory carries the codes and half a tile of dY, by
+// bulk and tensor copies, and is read for operand B only.  dY lies there as in memory, tokens x columns
+// (MN-major, 128-byte swizzle).
 //
-// Work: whole tiles first, one per block and wave, all blocks at the same
-// tokens, so that what they read together stays in L2; the tiles of the last, partial wave
-// are cut along the tokens into equal parts for all blocks.  Parts of a tile go
-// to the workspace and wgrad_join_kernel adds them in order.
+// The tensor core's accumulator drops bits below its own last one in every step,
+// which adds up over thousands of tokens (8e-6 of the result over 16384, where
+// float32 sums are at 6e-7).  So the sums are taken out every kChunk stages and
+// added in registers: warp group w keeps columns [w W / 2, (w + 1) W / 2) of its
+// 128 channels.  The same two warp groups convert, one the even and one the odd
+// stages, and are some stages ahead when they turn to the sums, so that the
+// tensor core waits for the reading of TMEM alone; results leave for memory
+// while it works on.
+//
+// Work: whole tiles first, one per pair of blocks and wave, all pairs at the
+// same tokens, so that what they read together stays in L2; the tiles of the
+// last, partial wave are cut along the tokens into equal parts for all pairs.
+// Parts of a tile go to the workspace and wgrad_join_kernel adds them in order.
+#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -28,6 +41,8 @@
 #include "per_device.h"
 #include "tc_ptx.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace stp {
 
 stp_status check_ckpt_desc(const stp_ckpt_desc* d);
@@ -36,28 +51,38 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 192;       // warps 0-3 convert and store results, 4 loads, 5 multiplies
-constexpr int kStages = 6;
-constexpr int kTileC = 128, kTileM = 256;
+constexpr int kThreads = 384;       // warps 0-7 convert and add up, 8 loads, 9 multiplies
+// Registers of a thread: 168 at launch (65536 / 384), of which the warps that keep no sums give theirs up:
+// 2 x 232 + 40 = 3 x 168.
+constexpr int kRegsSums = 232, kRegsRest = 40;
+constexpr int kGroups = 2;          // warp groups among them
+constexpr int kStages = 8;
+constexpr int kAhead = 6;           // stages converted ahead when sums are taken: less than kStages
+constexpr int kChunk = 32;          // stages between two takings
+constexpr int kTileC = 256, kHalfC = 128, kTileM = 256;
 constexpr int kBoxBytes = 64 * 64 * 2;              // 64 tokens x 64 columns
-constexpr int kStageBytes = 4 * kBoxBytes;
-constexpr int kSmem = kStages * kStageBytes + 1024 + 256;
+constexpr int kYBytes = 2 * kBoxBytes;              // a block's half of the columns
+constexpr int kCodeBytes = 4 * kCkBlock;            // 64 tokens x 128 channels
+constexpr int kStageRow = 20;       // floats of a row of results on their way: 16, and 4 so that rows lie in other banks
+constexpr int kOffCodes = kStages * kYBytes, kOffStage = kOffCodes + kStages * kCodeBytes,
+              kOffBars = kOffStage + 8 * 32 * kStageRow * 4;
+constexpr int kSmem = kOffBars + 512 + 1024;
 constexpr int kColA = 256;          // first TMEM column of A's stages
-constexpr size_t kPartBytes = (size_t)kTileC * kTileM * 4;
-constexpr int kLeastBlocks = 4;     // token blocks of a part at least
+constexpr size_t kPartBytes = (size_t)kHalfC * kTileM * 4;   // of a block
+constexpr int kLeastBlocks = 12;    // token blocks of a part at least
 
 struct WgradParams {
-  int N, C, M, CB, KB, W;       // W: columns of a tile, a multiple of 16
+  int N, C, M, CB, KB, W;       // W: columns of a tile, a multiple of 32
   int CT, MT;                   // tiles along channels and columns
-  int whole, rest, parts;       // waves of whole tiles; tiles of the last wave, and blocks that share them
+  int whole, rest, parts;       // waves of whole tiles; tiles of the last wave, and pairs that share them
   bool add, vec;                // vec: rows of dW start at whole 16 bytes
   const uint8_t* ck;
   float* dw;
-  float* part;                  // [2 * parts][64][128][4]: column / 4, channel, column % 4
+  float* part;                  // [parts][2][2][64][128][4]: pair, its first or second part, block, column / 4, channel, column % 4
   uint32_t* err;
 };
 
-// The share of block g in the last wave: token blocks [at, end) of `rest` tiles of KB each.
+// The share of pair g in the last wave: token blocks [at, end) of `rest` tiles of KB each.
 __host__ __device__ __forceinline__ int64_t share(const WgradParams& p, int g) {
   return (int64_t)p.rest * p.KB * g / p.parts;
 }
@@ -66,248 +91,345 @@ struct Segment {
   int tile, kb0, kb1, slot;   // slot: of the workspace, -1 when the tile is whole
 };
 
-// Segment i of block g; false when there is none.
-__device__ __forceinline__ bool segment(const WgradParams& p, int g, int grid, int i, Segment& s) {
-  if (i < p.whole) {
-    s = {i * grid + g, 0, p.KB, -1};
-    return true;
-  }
-  if (g >= p.parts) return false;
+// The one or two segments of pair g in the last wave; returns how many.
+__device__ __forceinline__ int last_segments(const WgradParams& p, int g, int pairs, Segment* to) {
+  if (g >= p.parts) return 0;
   const int64_t at = share(p, g), end = share(p, g + 1);
-  const int64_t first = at / p.KB, tile = first + (i - p.whole);
-  const int64_t a = tile * p.KB > at ? tile * p.KB : at, b = (tile + 1) * p.KB < end ? (tile + 1) * p.KB : end;
-  if (a >= b) return false;
-  s.tile = p.whole * grid + (int)tile;
-  s.kb0 = (int)(a - tile * p.KB);
-  s.kb1 = (int)(b - tile * p.KB);
-  s.slot = s.kb0 == 0 && s.kb1 == p.KB ? -1 : 2 * g + (tile != first);
-  return true;
+  const int first = (int)(at / p.KB);
+  int n = 0;
+  for (int tile = first; n < 2 && (int64_t)tile * p.KB < end; ++tile, ++n) {
+    const int64_t t0 = (int64_t)tile * p.KB;
+    Segment& s = to[n];
+    s.tile = p.whole * pairs + tile;
+    s.kb0 = (int)(max(t0, at) - t0);
+    s.kb1 = (int)(min(t0 + p.KB, end) - t0);
+    s.slot = s.kb0 == 0 && s.kb1 == p.KB ? -1 : 2 * g + n;
+  }
+  return n;
 }
 
-enum { W_BF = 0, W_AF = kStages, W_E = 2 * kStages, W_DF = 3 * kStages, W_DE, W_DRAIN, W_COUNT };
+// Barriers: the codes of a stage have landed (both blocks'), dY of both blocks
+// has landed and A of both is in place (first block's), the stage is free
+// (both); the sums of a chunk are ready (both) and taken by both (first block's).
+enum { W_CF = 0, W_BF = kStages, W_AF = 2 * kStages, W_E = 3 * kStages, W_DF = 4 * kStages, W_DE, W_DRAIN, W_COUNT };
 
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+// ---- a pair's instructions
+
+__device__ __forceinline__ uint32_t in_block(uint32_t addr, int block) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(block));
+  return r;
+}
+
+// Arrives on a barrier of either block.  What the barriers between the blocks
+// order lies in TMEM, which tcgen05's own waits and fences order, so no wider
+// scope is asked for: a release at cluster scope waits for all memory (1250 us
+// against 783 for the 16384-token projection).
+__device__ __forceinline__ void arrive_in(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Tile load whose bytes count on a barrier of either block of the pair.
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
       : "memory");
 }
 
-// 64 tokens of a channel and their scales on their way to a lane's registers.
-struct Codes {
-  uint4 code[4], scale[4];
-  __device__ __forceinline__ void get(const WgradParams& p, int tb, int cb, int lane) {
-    if (cb < p.CB) {
-      const uint4* block = reinterpret_cast<const uint4*>(p.ck + ((int64_t)tb * p.CB + cb) * kCkBlock);
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tmov.b64 db, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(kDescHi));
+}
+
+// Arrives on the barrier of both blocks once all products issued so far are done.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// A channel's codes of 32 tokens (the first or the second of a block's) in
+// shared memory to bf16 pairs of successive tokens.
+__device__ __forceinline__ void convert(const uint8_t* block, int lane, int part, uint32_t* r) {
+  const uint4* from = reinterpret_cast<const uint4*>(block);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        code[q] = __ldg(block + q * 32 + lane);
-        scale[q] = __ldg(block + kCkCodes / 16 + q);
-      }
-    } else {
+  for (int q = 0; q < 2; ++q) {
+    const uint4 c4 = from[(part * 2 + q) * 32 + lane], s4 = from[kCkCodes / 16 + part * 2 + q];
+    const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) code[q] = scale[q] = make_uint4(0, 0, 0, 0);
+    for (int w = 0; w < 4; ++w) {
+      r[q * 8 + w * 2] = mul_bf16x2(codes_bf16x2(__byte_perm(c[w], 0, 0x1404)), scales_bf16x2(__byte_perm(s[w], 0, 0x4140)));
+      r[q * 8 + w * 2 + 1] =
+          mul_bf16x2(codes_bf16x2(__byte_perm(c[w], 0, 0x3424)), scales_bf16x2(__byte_perm(s[w], 0, 0x4342)));
     }
   }
-  // bf16 pairs of successive tokens
-  __device__ __forceinline__ void put(uint32_t* r) const {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t c[4] = {code[q].x, code[q].y, code[q].z, code[q].w};
-      const uint32_t s[4] = {scale[q].x, scale[q].y, scale[q].z, scale[q].w};
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        r[q * 8 + w * 2] = mul_bf16x2(codes_bf16x2(__byte_perm(c[w], 0, 0x1404)), scales_bf16x2(__byte_perm(s[w], 0, 0x4140)));
-        r[q * 8 + w * 2 + 1] =
-            mul_bf16x2(codes_bf16x2(__byte_perm(c[w], 0, 0x3424)), scales_bf16x2(__byte_perm(s[w], 0, 0x4342)));
-      }
-    }
-  }
-};
+}
 
 // B operand: 64-column boxes kBoxBytes apart (leading dimension), 8-token groups 1024 bytes apart.
 __device__ __forceinline__ uint32_t desc_lo_b(uint32_t addr) {
   return ((addr & 0x3FFFFu) >> 4) | ((uint32_t)(kBoxBytes >> 4) << 16);
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+// The stages of a pair in order, over all its segments.
+struct Walk {
+  Segment s;
+  int i = 0, kb = 0;
+  const Segment* last;   // of the last wave, in shared memory
+  int n, whole, KB, pairs;
+  __device__ __forceinline__ Walk(const WgradParams& p, int g, int pairs_, const Segment* last_, int n_last)
+      : last(last_), n(p.whole + n_last), whole(p.whole), KB(p.KB), pairs(pairs_) {
+    s.tile = g - pairs;
+    enter();
+  }
+  __device__ __forceinline__ void enter() {
+    if (i < whole) {
+      s = {s.tile + pairs, 0, KB, -1};
+    } else if (i < n) {
+      s = last[i - whole];
+    }
+    kb = s.kb0;
+  }
+  __device__ __forceinline__ bool on() const { return i < n; }
+  __device__ __forceinline__ void next() {
+    if (++kb == s.kb1) {
+      ++i;
+      enter();
+    }
+  }
+};
+
+// Four columns of a row of dW; `left` of them exist.
+__device__ __forceinline__ void put4(const WgradParams& p, float* at, float4 v, int left) {
+  if (p.vec && left >= 4) {
+    float4* to = reinterpret_cast<float4*>(at);
+    if (p.add) {
+      const float4 o = *to;
+      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+    }
+    *to = v;
+  } else {
+    const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < left) at[k] = x[k] + (p.add ? at[k] : 0.f);
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap ty, const WgradParams p) {
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  uint8_t* codes = smem + kOffCodes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + W_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = blockIdx.x, grid = gridDim.x;
+  Segment* last_wave = reinterpret_cast<Segment*>(tmem_slot + 4);
+  int* n_last_wave = reinterpret_cast<int*>(last_wave + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, block = blockIdx.x & 1, g = blockIdx.x >> 1,
+            pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < W_COUNT; ++b)
-      mbar_init(&bars[b], (b >= W_AF && b < W_AF + kStages) || b == W_DE ? 4 : 1);
+      mbar_init(&bars[b], b >= W_AF && b < W_AF + kStages ? 8 : b == W_DE ? 16 : 1);
     *abort_flag = 0;
+    *n_last_wave = last_segments(p, g, pairs, last_wave);
     fence_mbar_init();
   }
-  if (warp == 5) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   fence_before_sync();
-  __syncthreads();
+  cg::this_cluster().sync();
   fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int boxes = (p.W + 63) / 64;
-  Segment s;
+  const int n_last = *n_last_wave;
 
-  if (warp == 4) {
+  if (warp >= 8) {
+    regs_dec<kRegsRest>();
+    if (warp == 8) {
     if (lane == 0) {
+      // ------------------------------------------------------------ loads
       tma_prefetch_desc(&ty);
-      int it = 0, last_phase[kStages];
-      for (int st = 0; st < kStages; ++st) last_phase[st] = -1;
-      bool ok = true;
-      for (int i = 0; ok && segment(p, g, grid, i, s); ++i) {
-        const int m0 = s.tile / p.CT * p.W;
-        for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
-          const int st = it % kStages, n = it / kStages;
-          if (it >= kStages && !mbar_wait(&bars[W_E + st], (n - 1) & 1, abort_flag, p.err)) {
-            ok = false;
-            break;
-          }
-          mbar_expect_tx(&bars[W_BF + st], boxes * kBoxBytes);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(smem + st * kStageBytes + b * kBoxBytes, &ty, &bars[W_BF + st], m0 + b * 64, kb * 64);
-          last_phase[st] = n & 1;
+      const int boxes = (p.W / 2 + 63) / 64;
+      int it = 0, last[kStages], landed[kStages];   // phase of a stage's last load, and of its last codes
+      for (int st = 0; st < kStages; ++st) last[st] = landed[st] = -1;
+      for (Walk w(p, g, pairs, last_wave, n_last); w.on(); w.next(), ++it) {
+        const int st = it % kStages, n = it / kStages;
+        if (it >= kStages && !mbar_wait(&bars[W_E + st], (n - 1) & 1, abort_flag, p.err)) break;
+        const int m0 = w.s.tile / p.CT * p.W + block * (p.W / 2), cb = w.s.tile % p.CT * 8 + block * 4;
+        const uint32_t bar = in_block(smem_u32(&bars[W_BF + st]), 0);
+        if (block == 0) mbar_expect_tx(&bars[W_BF + st], 2 * boxes * kBoxBytes);
+        for (int b = 0; b < boxes; ++b)
+          tma_load_pair(smem + st * kYBytes + b * kBoxBytes, &ty, bar, m0 + b * 64, w.kb * 64);
+        last[st] = n & 1;
+        if (cb < p.CB) {
+          const uint32_t bytes = min(4, p.CB - cb) * kCkBlock;
+          mbar_expect_tx(&bars[W_CF + st], bytes);
+          bulk_load(codes + st * kCodeBytes, p.ck + ((int64_t)w.kb * p.CB + cb) * kCkBlock, bytes, &bars[W_CF + st]);
+          landed[st] = n & 1;
+        } else {
+          mbar_arrive(&bars[W_CF + st]);   // channels past the end: nothing comes
         }
       }
-      for (int st = 0; st < kStages; ++st)
-        if (last_phase[st] >= 0) mbar_wait_drain(&bars[W_BF + st], last_phase[st]);
+      for (int st = 0; st < kStages; ++st) {
+        if (landed[st] >= 0) mbar_wait_drain(&bars[W_CF + st], landed[st]);
+        if (block == 0 && last[st] >= 0) mbar_wait_drain(&bars[W_BF + st], last[st]);
+      }
     }
     __syncwarp();
-  } else if (warp == 5) {
-    if (lane == 0) {
+    } else if (warp == 9) {
+    if (lane == 0 && block == 0) {
+      // --------------------------------------------------------- products
       const uint32_t idesc = idesc_bf16(kTileC, p.W, 0, 1);
-      int it = 0;
-      bool ok = true;
-      for (int i = 0; ok && segment(p, g, grid, i, s); ++i) {
-        if (i > 0 && !mbar_wait(&bars[W_DE], (i - 1) & 1, abort_flag, p.err)) break;
-        fence_after_sync();
-        for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
-          const int st = it % kStages;
-          const uint32_t phase = (it / kStages) & 1;
-          if (!mbar_wait(&bars[W_BF + st], phase, abort_flag, p.err) ||
-              !mbar_wait(&bars[W_AF + st], phase, abort_flag, p.err)) {
-            ok = false;
-            break;
-          }
-          fence_after_sync();
-          const uint32_t b_lo = desc_lo_b(smem_u32(smem) + st * kStageBytes), a = tmem + kColA + st * 32;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ts_lo(tmem, a + kk * 8, b_lo + kk * (2048 >> 4), idesc, kb > s.kb0 || kk > 0);
-          mma_commit(&bars[W_E + st]);
-        }
-        if (ok) mma_commit(&bars[W_DF]);
-      }
-      mma_commit(&bars[W_DRAIN]);
-      mbar_wait_drain(&bars[W_DRAIN], 0);
-    }
-    __syncwarp();
-  } else {
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    int it = 0;
-    bool ok = true;
-    for (int i = 0; ok && segment(p, g, grid, i, s); ++i) {
-      const int ct = s.tile % p.CT, cb = ct * 4 + warp;
-      Codes next;
-      next.get(p, s.kb0, cb, lane);
-      for (int kb = s.kb0; kb < s.kb1; ++kb, ++it) {
+      int it = 0, chunk = 0, in = 0;
+      for (Walk w(p, g, pairs, last_wave, n_last); w.on(); ++it) {
+        if (in == 0 && chunk > 0 && !mbar_wait(&bars[W_DE], (chunk - 1) & 1, abort_flag, p.err)) break;
         const int st = it % kStages;
-        const Codes now = next;
-        if (kb + 1 < s.kb1) next.get(p, kb + 1, cb, lane);
-        uint32_t r[32];
-        now.put(r);
-        if (it >= kStages &&
-            !__all_sync(0xffffffffu, mbar_wait(&bars[W_E + st], (it / kStages - 1) & 1, abort_flag, p.err))) {
+        const uint32_t phase = (it / kStages) & 1;
+        if (!mbar_wait(&bars[W_BF + st], phase, abort_flag, p.err) ||
+            !mbar_wait(&bars[W_AF + st], phase, abort_flag, p.err))
+          break;
+        fence_after_sync();
+        const uint32_t b_lo = desc_lo_b(smem_u32(smem) + st * kYBytes), a = tmem + kColA + st * 32;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) mma_pair(tmem, a + kk * 8, b_lo + kk * (2048 >> 4), idesc, in > 0 || kk > 0);
+        commit_pair(&bars[W_E + st]);
+        const int tile = w.i;
+        w.next();
+        if (++in == kChunk || w.i != tile) {
+          commit_pair(&bars[W_DF]);
+          in = 0;
+          ++chunk;
+        }
+      }
+      commit_pair(&bars[W_DRAIN]);
+    }
+    // nothing of the pair is in flight behind this
+    if (lane == 0) mbar_wait_drain(&bars[W_DRAIN], 0);
+    __syncwarp();
+    }
+  } else {
+    regs_inc<kRegsSums>();
+    const int group = warp >> 2, w4 = warp & 3, half = p.W / 2;
+    const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
+    const uint32_t taken = in_block(smem_u32(&bars[W_DE]), 0);
+    float* stage = reinterpret_cast<float*>(smem + kOffStage) + warp * 32 * kStageRow;
+    float acc[kTileM / 2];
+#pragma unroll
+    for (int e = 0; e < kTileM / 2; ++e) acc[e] = 0.f;
+    int it = 0, end = 0, chunk = 0;   // stages converted, and at the end of the chunk
+    bool ok = true;
+    Walk c(p, g, pairs, last_wave, n_last);
+    for (Walk d(p, g, pairs, last_wave, n_last); d.on() && ok; ++chunk) {
+      // the chunk: up to kChunk stages of one segment
+      const int len = min(kChunk, d.s.kb1 - d.kb);
+      end += len;
+      for (; c.on() && it < end + kAhead; ++it, c.next()) {
+        if (it % kGroups != group) continue;
+        const int st = it % kStages, n = it / kStages;
+        const bool there = c.s.tile % p.CT * 8 + block * 4 + w4 < p.CB;
+        // the codes, and TMEM's stage
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars[W_CF + st], n & 1, abort_flag, p.err) &&
+                                         (it < kStages || mbar_wait(&bars[W_E + st], (n - 1) & 1, abort_flag, p.err)))) {
           ok = false;
           break;
         }
         fence_after_sync();
-        tmem_st32(tmem + lane_base + kColA + st * 32, r);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t r[16];
+          if (there) convert(codes + st * kCodeBytes + w4 * kCkBlock, lane, h, r);
+          else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = 0;
+          }
+          tmem_st16(tmem + lane_base + kColA + st * 32 + h * 16, r);
+        }
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[W_AF + st]);
+        if (lane == 0) arrive_in(in_block(smem_u32(&bars[W_AF + st]), 0));
       }
-      if (!ok || !__all_sync(0xffffffffu, mbar_wait(&bars[W_DF], i & 1, abort_flag, p.err))) break;
+      if (!ok || !__all_sync(0xffffffffu, mbar_wait(&bars[W_DF], chunk & 1, abort_flag, p.err))) break;
       fence_after_sync();
-      const int c = ct * kTileC + warp * 32 + lane, m0 = s.tile / p.CT * p.W, width = min(p.W, p.M - m0);
-      float* row = p.dw + (int64_t)c * p.M + m0;
-      float4* part = reinterpret_cast<float4*>(p.part) + (size_t)max(s.slot, 0) * (kPartBytes / 16) + warp * 32 + lane;
-      for (int j = 0; j < p.W; j += 32) {
-        uint32_t x[32];
-        tmem_ld32(tmem + lane_base + j, x);
-        tmem_ld_wait();
-        if (s.slot >= 0) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            if (j + e < p.W)
-              part[(j + e) / 4 * kTileC] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]),
-                                                       __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-        } else if (c < p.C) {
+      for (int j = 0; j < kTileM / 2; j += 16)
+        if (j < half) {
+          uint32_t x[16];
+          tmem_ld16(tmem + lane_base + group * half + j, x);
+          tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            if (p.vec && j + e + 3 < width) {
-              float4* at = reinterpret_cast<float4*>(row + j + e);
-              float4 v = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]), __uint_as_float(x[e + 2]),
-                                     __uint_as_float(x[e + 3]));
-              if (p.add) {
-                const float4 o = *at;
-                v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-              }
-              *at = v;
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (j + e + k < width) row[j + e + k] = __uint_as_float(x[e + k]) + (p.add ? row[j + e + k] : 0.f);
-            }
-          }
+          for (int e = 0; e < 16; ++e) acc[j + e] += __uint_as_float(x[e]);
         }
-      }
       fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[W_DE]);
+      if (lane == 0) arrive_in(taken);
+      const int tile = d.s.tile, slot = d.s.slot, segment = d.i;
+      d.kb += len - 1;
+      d.next();
+      if (d.i == segment) continue;
+      // the segment's results, 16 columns of 32 channels at a time through
+      // shared memory, so that they leave in rows
+      const int c0 = tile % p.CT * kTileC + block * kHalfC + w4 * 32, m0 = tile / p.CT * p.W + group * half;
+      float4* part = reinterpret_cast<float4*>(p.part) + (size_t)(max(slot, 0) * 2 + block) * (kPartBytes / 16) + w4 * 32 + lane +
+                     group * half / 4 * kHalfC;
+#pragma unroll
+      for (int j = 0; j < kTileM / 2; j += 16) {
+        if (j >= half) continue;
+        if (slot >= 0) {
+#pragma unroll
+          for (int e = j; e < j + 16; e += 4) part[e / 4 * kHalfC] = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+        } else {
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(stage + lane * kStageRow + e) = make_float4(acc[j + e], acc[j + e + 1], acc[j + e + 2], acc[j + e + 3]);
+          __syncwarp();
+          const int e = (lane & 3) * 4, left = min(half, p.M - m0) - j - e;
+          for (int r = lane >> 2; r < 32 && c0 + r < p.C; r += 8)
+            put4(p, p.dw + (int64_t)(c0 + r) * p.M + m0 + j + e, *reinterpret_cast<const float4*>(stage + r * kStageRow + e), left);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kTileM / 2; ++e) acc[e] = 0.f;
     }
   }
 
   __syncwarp();
   fence_before_sync();
-  __syncthreads();
+  cg::this_cluster().sync();
   fence_after_sync();
-  if (warp == 5) tmem_dealloc(tmem, 512);
+  if (warp == 9)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-// Adds up the parts of a tile of the last wave; a block does 8 columns x 128 channels.
+// Adds up the parts of a tile of the last wave; a block does 4 columns x 256 channels.
 __global__ void __launch_bounds__(256) wgrad_join_kernel(const WgradParams p) {
   const int tile = blockIdx.y;   // of the last wave
   const int64_t a = (int64_t)tile * p.KB, b = a + p.KB, all = (int64_t)p.rest * p.KB;
-  int g = (int)(a * p.parts / all);   // the first block whose share reaches past a
+  int g = (int)(a * p.parts / all);   // the first pair whose share reaches past a
   while (g > 0 && share(p, g) > a) --g;
   while (share(p, g + 1) <= a) ++g;
-  if (share(p, g) <= a && share(p, g + 1) >= b) return;   // one block did it all
-  const int cg4 = blockIdx.x * 2 + (threadIdx.x >> 7), r = threadIdx.x & 127;
-  if (cg4 * 4 >= p.W) return;
+  if (share(p, g) <= a && share(p, g + 1) >= b) return;   // one pair did it all
+  const int c4 = blockIdx.x, block = threadIdx.x >> 7, r = threadIdx.x & 127;
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   for (; g < p.parts && share(p, g) < b; ++g) {
     const int slot = 2 * g + (share(p, g) / p.KB != tile);
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(p.part) + (size_t)slot * (kPartBytes / 16) + cg4 * kTileC + r);
+    const float4 v =
+        __ldcs(reinterpret_cast<const float4*>(p.part) + (size_t)(slot * 2 + block) * (kPartBytes / 16) + c4 * kHalfC + r);
     sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
   }
-  const int all_tile = p.CT * p.MT - p.rest + tile, c = all_tile % p.CT * kTileC + r;
-  const int m0 = all_tile / p.CT * p.W, m = m0 + cg4 * 4, end = min(p.M, m0 + p.W);
-  if (c >= p.C) return;
-  float* at = p.dw + (int64_t)c * p.M + m;
-  const float v[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (m + k < end) at[k] = v[k] + (p.add ? at[k] : 0.f);
+  const int which = p.CT * p.MT - p.rest + tile, c = which % p.CT * kTileC + threadIdx.x;
+  const int m0 = which / p.CT * p.W, m = m0 + c4 * 4, end = min(p.M, m0 + p.W);
+  if (c < p.C && m < end) put4(p, p.dw + (int64_t)c * p.M + m, sum, end - m);
 }
 
 typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -347,7 +469,7 @@ stp_status check_wgrad(const stp_ckpt_desc* d, int cols) {
   return STP_OK;
 }
 
-// Tiles and the blocks' shares of them on a GPU of n_sm SMs; returns the launch's blocks.
+// Tiles and the pairs' shares of them on a GPU of n_sm SMs; returns the launch's pairs.
 int plan(WgradParams& p, const stp_ckpt_desc* d, int cols, int n_sm) {
   p.N = d->n_tokens;
   p.C = d->dim;
@@ -356,13 +478,14 @@ int plan(WgradParams& p, const stp_ckpt_desc* d, int cols, int n_sm) {
   p.KB = (int)ck_token_blocks(p.N);
   p.CT = (p.C + kTileC - 1) / kTileC;
   p.MT = (p.M + kTileM - 1) / kTileM;
-  p.W = ((p.M + p.MT - 1) / p.MT + 15) / 16 * 16;   // tiles of one width, not full ones and a narrow last
+  p.W = ((p.M + p.MT - 1) / p.MT + 31) / 32 * 32;   // tiles of one width, not full ones and a narrow last
   const int64_t tiles = (int64_t)p.CT * p.MT;
-  p.whole = (int)(tiles / n_sm);
-  p.rest = (int)(tiles % n_sm);
+  const int pairs = n_sm / 2;
+  p.whole = (int)(tiles / pairs);
+  p.rest = (int)(tiles % pairs);
   const int64_t most = (int64_t)p.rest * p.KB / kLeastBlocks;
-  p.parts = p.rest == 0 ? 0 : (int)(most < p.rest ? p.rest : most < n_sm ? most : n_sm);
-  return p.whole > 0 ? n_sm : p.parts;
+  p.parts = p.rest == 0 ? 0 : (int)(most < p.rest ? p.rest : most < pairs ? most : pairs);
+  return p.whole > 0 ? pairs : p.parts;
 }
 
 }  // namespace
@@ -381,7 +504,7 @@ extern "C" stp_status stp_ckpt_wgrad_workspace_size(const stp_ckpt_desc* desc, i
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_ckpt_wgrad_workspace_size: %s", cudaGetErrorString(e));
   WgradParams p{};
   plan(p, desc, cols, n_sm);
-  *ws_bytes = 256 + (p.parts > p.rest ? 2 * (size_t)p.parts * kPartBytes : 0);
+  *ws_bytes = 256 + (p.parts > p.rest ? 4 * (size_t)p.parts * kPartBytes : 0);
   return STP_OK;
 }
 
@@ -410,7 +533,7 @@ extern "C" stp_status stp_ckpt_wgrad(const stp_ckpt_desc* desc, int32_t cols, co
       e = limit([] { return cudaFuncSetAttribute(wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
     if (e != cudaSuccess) return fail(STP_ECUDA, "stp_ckpt_wgrad: %s", cudaGetErrorString(e));
     WgradParams p{};
-    const int grid = plan(p, desc, cols, n_sm);
+    const int pairs = plan(p, desc, cols, n_sm);
     p.add = accumulate != 0;
     p.vec = reinterpret_cast<uintptr_t>(d_w) % 16 == 0 && p.M % 4 == 0;
     p.ck = static_cast<const uint8_t*>(d_ckpt);
@@ -419,8 +542,8 @@ extern "C" stp_status stp_ckpt_wgrad(const stp_ckpt_desc* desc, int32_t cols, co
     p.err = static_cast<uint32_t*>(d_ws);
     CUtensorMap ty;
     if (!make_map(&ty, d_y, p.N, p.M, y_stride)) return fail(STP_ECUDA, "stp_ckpt_wgrad: tensor map encoding failed");
-    wgrad_kernel<<<grid, kThreads, kSmem, s>>>(ty, p);
-    if (p.parts > p.rest) wgrad_join_kernel<<<dim3((p.W / 4 + 1) / 2, p.rest), 256, 0, s>>>(p);
+    wgrad_kernel<<<2 * pairs, kThreads, kSmem, s>>>(ty, p);
+    if (p.parts > p.rest) wgrad_join_kernel<<<dim3(p.W / 4, p.rest), 256, 0, s>>>(p);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_ckpt_wgrad: %s", cudaGetErrorString(e));
