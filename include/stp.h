@@ -827,7 +827,7 @@ stp_status stp_embed_bwd(const stp_embed_desc* desc, const void* d_out, const in
 /*
  * Activations kept in 8 bits between the forward and the backward pass.  A
  * checkpoint holds x [N, C] as e4m3 codes with one power-of-two scale for 32
- * successive channels of a token (33/32 bytes an element): with a the largest
+ * successive channels of a token (34/32 bytes an element): with a the largest
  * magnitude of the 32 and s the smallest power of two, from 2^-117 on, with
  * a <= 448 s,
  *   x^ = s round_e4m3(x / s)   (to nearest, ties to even),
@@ -842,7 +842,7 @@ typedef struct {
   int64_t stride;   /* elements between tokens of x, >= C     */
 } stp_ckpt_desc;
 
-/* Bytes of a checkpoint: 2112 for every 64 tokens x 32 channels begun. */
+/* Bytes of a checkpoint: 2176 for every 64 tokens x 32 channels begun. */
 stp_status stp_ckpt_size(const stp_ckpt_desc* desc, size_t* ckpt_bytes);
 
 /*

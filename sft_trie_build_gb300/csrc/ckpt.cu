@@ -1,6 +1,6 @@
 // Activations kept in 8 bits (layout and rounding: ckpt.h), and their return.
 //
-// Bound by memory: storing reads x and writes 33/32 bytes an element, restoring the
+// Bound by memory: storing reads x and writes 34/32 bytes an element, restoring the
 // reverse.  A warp takes 16 tokens x 64 channels and a lane two channels of all
 // 16 tokens: rows of x are read 128 bytes (bf16) at a time, the lane's codes
 // are two whole 16-byte pieces of the checkpoint, and nothing passes through
@@ -40,7 +40,7 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   return d;
 }
 
-// Scale byte of a float's magnitude, given by its bits: monotone in it.
+// Exponent field of the scale of a float's magnitude, given by its bits: monotone in it.
 __device__ __forceinline__ uint32_t scale_of(uint32_t bits) {
   if (bits >= 0x7f800000u) return kCkNaN;
   return (uint32_t)max((int)((bits + 0x1fffffu) >> 23) - 8, kCkLeast);   // carries above 1.75
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const CkptParams p)
       }
     }
   }
-  uint32_t code[2][4], scale[4];
+  uint32_t code[2][4], scale[kTokens / 2];
 #pragma unroll
   for (int i = 0; i < kTokens; i += 2) {
     // the larger magnitude of each of two tokens, low and high half
@@ -124,15 +124,13 @@ __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const CkptParams p)
     const uint32_t keep = (s0 == kCkNaN ? 0u : 0xffu) | (s1 == kCkNaN ? 0u : 0xff00u);
     lo &= keep;
     hi &= keep;
-    const uint32_t ss = s0 | s1 << 8;
+    scale[i / 2] = s0 << 7 | s1 << 23;
     if (i & 2) {
-      code[0][i / 4] |= lo << 16;
-      code[1][i / 4] |= hi << 16;
-      scale[i / 4] |= ss << 16;
+      code[0][i / 4] = pack_codes(code[0][i / 4] | lo << 16);
+      code[1][i / 4] = pack_codes(code[1][i / 4] | hi << 16);
     } else {
       code[0][i / 4] = lo;
       code[1][i / 4] = hi;
-      scale[i / 4] = ss;
     }
   }
   const int cb = c / kCkChannels, in = c & (kCkChannels - 1), q = group & 3;
@@ -141,7 +139,11 @@ __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const CkptParams p)
   uint4* to = reinterpret_cast<uint4*>(block + q * 512 + in * 16);
   to[0] = make_uint4(code[0][0], code[0][1], code[0][2], code[0][3]);
   to[1] = make_uint4(code[1][0], code[1][1], code[1][2], code[1][3]);
-  if (in == 0) *reinterpret_cast<uint4*>(block + kCkCodes + q * 16) = make_uint4(scale[0], scale[1], scale[2], scale[3]);
+  if (in == 0) {
+    uint4* scales = reinterpret_cast<uint4*>(block + kCkCodes + q * 32);
+    scales[0] = make_uint4(scale[0], scale[1], scale[2], scale[3]);
+    scales[1] = make_uint4(scale[4], scale[5], scale[6], scale[7]);
+  }
 }
 
 template <typename T, bool WIDE>
@@ -153,22 +155,26 @@ __global__ void __launch_bounds__(kThreads) ckpt_load_kernel(const CkptParams p)
   const int cb = c / kCkChannels, in = c & (kCkChannels - 1), q = group & 3;
   const uint8_t* block = p.ck + ((int64_t)(group >> 2) * p.CB + cb) * kCkBlock;
   const uint4* from = reinterpret_cast<const uint4*>(block + q * 512 + in * 16);
-  const uint4 a4 = __ldcs(from), b4 = __ldcs(from + 1), s4 = *reinterpret_cast<const uint4*>(block + kCkCodes + q * 16);
-  const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+  const uint4* scales = reinterpret_cast<const uint4*>(block + kCkCodes + q * 32);
+  const uint4 a4 = __ldcs(from), b4 = __ldcs(from + 1), s4 = scales[0], t4 = scales[1];
+  const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
+  const uint32_t s[8] = {s4.x, s4.y, s4.z, s4.w, t4.x, t4.y, t4.z, t4.w};
   T* y = static_cast<T*>(p.y) + c;
 #pragma unroll
-  for (int i = 0; i < kTokens; ++i) {
-    if (n0 + i >= p.N) return;
-    const int w = i / 4, k = i & 3;
-    // both channels' codes in the upper bytes of the halves, the token's scale in both halves
-    const uint32_t x = __byte_perm(a[w], b[w], (4 + k) << 12 | k << 4) & 0xff00ff00u;
-    const uint32_t f = scales_bf16x2(__byte_perm(s[w], 0, 0x4040 | k << 8 | k));
-    const uint32_t v = mul_bf16x2(codes_bf16x2(x), f);
-    T* at = y + (int64_t)(n0 + i) * p.stride;
-    if (WIDE && c + 1 < p.C) Two<T>::put(at, v);
-    else {
-      Two<T>::put1(at, v);
-      if (c + 1 < p.C) Two<T>::put1(at + 1, v >> 16);
+  for (int i = 0; i < kTokens; i += 2) {
+    // two tokens of either channel, then two channels of either token
+    const uint32_t va = values_bf16x2(i & 2 ? late_codes(a[i / 4]) : early_codes(a[i / 4]), s[i / 2]);
+    const uint32_t vb = values_bf16x2(i & 2 ? late_codes(b[i / 4]) : early_codes(b[i / 4]), s[i / 2]);
+    const uint32_t v[2] = {__byte_perm(va, vb, 0x5410), __byte_perm(va, vb, 0x7632)};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (n0 + i + k >= p.N) return;
+      T* at = y + (int64_t)(n0 + i + k) * p.stride;
+      if (WIDE && c + 1 < p.C) Two<T>::put(at, v[k]);
+      else {
+        Two<T>::put1(at, v[k]);
+        if (c + 1 < p.C) Two<T>::put1(at + 1, v[k] >> 16);
+      }
     }
   }
 }

@@ -1,17 +1,25 @@
 // Layout of an activation checkpoint in 8 bits, and its exact return to bf16.
 //
 // A checkpoint of x [N, C] is an array of blocks of 64 tokens x 32 channels,
-// channel blocks of the same tokens side by side, 2112 bytes each:
-//   codes  uint8 [4][32][16]   e4m3 code of token 16 q + i and channel c at [q][c][i]
-//   scale  uint8 [64]          of each token: 2^(scale - 127) times a code is the value
+// channel blocks of the same tokens side by side, 2176 bytes each:
+//   codes  uint32 [4][32][4]   e4m3 codes of tokens 16 q + 4 i .. 16 q + 4 i + 3, channel c, at [q][c][i]
+//   scale  bf16 [64]           of each token: scale times a code is the value
 // Tokens lie next to one another, as the weight gradient contracts over them: a
 // thread that owns a channel reads 16 tokens at once.  Tokens and channels past
 // the end are zeros.  The scale is the smallest power of two, from 2^-117 on, at which the 32
 // channels' largest magnitude is at most 448 (e4m3's largest); a block that
-// holds an infinity or a NaN has scale 255 and codes 0, which return as NaN.
+// holds an infinity or a NaN has scale infinity and codes 0, which return as NaN.
 //
 // A code has four significant bits and a power of two leaves them as they are,
 // so the values are exact in bf16 (the smallest is 2^-9 2^-117, a normal number).
+// Its exponent and fraction, in the places of bf16's lowest exponent bits and
+// highest fraction bits, are the value times 2^-120 (below the smallest normal
+// number for e4m3's subnormals), and multiplying by 2^120 is exact.
+//
+// The four codes of a word are laid out so that they come back as two pairs with
+// five operations: the later two tokens' bits are in place (sign 15, exponent
+// and fraction 10..4 of a half), the earlier two's fill the gaps, four places away
+// from theirs (sign in 11, upper exponent bits in 14..12, the rest in 3..0).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -23,9 +31,9 @@ namespace stp {
 
 constexpr int kCkTokens = 64, kCkChannels = 32;
 constexpr int kCkCodes = kCkTokens * kCkChannels;
-constexpr int kCkBlock = kCkCodes + kCkTokens;   // bytes, a multiple of 16
-constexpr int kCkLeast = 10;                     // scale of 2^-117
-constexpr int kCkNaN = 255;
+constexpr int kCkBlock = kCkCodes + kCkTokens * 2;   // bytes, a multiple of 16
+constexpr int kCkLeast = 10;                         // exponent field of 2^-117
+constexpr int kCkNaN = 255;                          // and of infinity
 
 inline int64_t ck_token_blocks(int64_t n) { return (n + kCkTokens - 1) / kCkTokens; }
 inline int64_t ck_channel_blocks(int64_t c) { return (c + kCkChannels - 1) / kCkChannels; }
@@ -36,14 +44,21 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Two codes, in bits 8..15 and 24..31 of x, times 2^120 2^-127 each: the code's
-// exponent and fraction in bf16's places are the value times 2^-120, below the
-// smallest normal for e4m3's subnormals; the product with 2^120 is exact.
-__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t x) {
-  return mul_bf16x2((x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), 0x7b807b80u);
+// Four codes, in a word's bytes, to their places and back; `early` are the
+// first two tokens' values times 2^-120, `late` the other two's.
+__device__ __forceinline__ uint32_t pack_codes(uint32_t c) {
+  const uint32_t x = __byte_perm(c, 0, 0x1404), y = __byte_perm(c, 0, 0x3424);   // in the halves' upper bytes
+  return (x & 0x70007000u) | ((x >> 8) & 0x000f000fu) | ((x >> 4) & 0x08000800u) | (y & 0x80008000u) |
+         ((y >> 4) & 0x07f007f0u);
+}
+__device__ __forceinline__ uint32_t late_codes(uint32_t w) { return w & 0x87f087f0u; }
+__device__ __forceinline__ uint32_t early_codes(uint32_t w) {
+  return ((w << 4) & 0x80f080f0u) | ((w >> 4) & 0x07000700u);
 }
 
-// Factors 2^(scale - 127) as bf16 of two tokens whose scales lie in bytes 0 and 2.
-__device__ __forceinline__ uint32_t scales_bf16x2(uint32_t b) { return b << 7; }
+// Codes as above times their scales.
+__device__ __forceinline__ uint32_t values_bf16x2(uint32_t codes, uint32_t scales) {
+  return mul_bf16x2(mul_bf16x2(codes, 0x7b807b80u), scales);
+}
 
 }  // namespace stp

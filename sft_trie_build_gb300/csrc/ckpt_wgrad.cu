@@ -160,13 +160,15 @@ __device__ __forceinline__ void convert(const uint8_t* block, int lane, int part
   const uint4* from = reinterpret_cast<const uint4*>(block);
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const uint4 c4 = from[(part * 2 + q) * 32 + lane], s4 = from[kCkCodes / 16 + part * 2 + q];
-    const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+    const uint4 c4 = from[(part * 2 + q) * 32 + lane];
+    const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      r[q * 8 + w * 2] = mul_bf16x2(codes_bf16x2(__byte_perm(c[w], 0, 0x1404)), scales_bf16x2(__byte_perm(s[w], 0, 0x4140)));
-      r[q * 8 + w * 2 + 1] =
-          mul_bf16x2(codes_bf16x2(__byte_perm(c[w], 0, 0x3424)), scales_bf16x2(__byte_perm(s[w], 0, 0x4342)));
+    for (int w = 0; w < 4; w += 2) {
+      const uint4 s4 = from[kCkCodes / 16 + part * 4 + q * 2 + w / 2];   // the same for all lanes
+      r[q * 8 + w * 2] = values_bf16x2(early_codes(c[w]), s4.x);
+      r[q * 8 + w * 2 + 1] = values_bf16x2(late_codes(c[w]), s4.y);
+      r[q * 8 + w * 2 + 2] = values_bf16x2(early_codes(c[w + 1]), s4.z);
+      r[q * 8 + w * 2 + 3] = values_bf16x2(late_codes(c[w + 1]), s4.w);
     }
   }
 }
