@@ -842,7 +842,7 @@ typedef struct {
   int64_t stride;   /* elements between tokens of x, >= C     */
 } stp_ckpt_desc;
 
-/* Bytes of a checkpoint: 2176 for every 64 tokens x 32 channels begun. */
+/* Bytes of a checkpoint: 4352 for every 128 tokens x 32 channels begun. */
 stp_status stp_ckpt_size(const stp_ckpt_desc* desc, size_t* ckpt_bytes);
 
 /*

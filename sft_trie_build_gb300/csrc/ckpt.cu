@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTokens = 16;   // of a warp
+constexpr int kGroups = kCkTokens / kTokens;
 
 struct CkptParams {
   int N, C, CB, along;   // blocks that lie along the channels
@@ -133,9 +134,9 @@ __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const CkptParams p)
       code[1][i / 4] = hi;
     }
   }
-  const int cb = c / kCkChannels, in = c & (kCkChannels - 1), q = group & 3;
+  const int cb = c / kCkChannels, in = c & (kCkChannels - 1), q = group & (kGroups - 1);
   if (cb >= p.CB) return;
-  uint8_t* block = p.ck + ((int64_t)(group >> 2) * p.CB + cb) * kCkBlock;
+  uint8_t* block = p.ck + ((int64_t)(group / kGroups) * p.CB + cb) * kCkBlock;
   uint4* to = reinterpret_cast<uint4*>(block + q * 512 + in * 16);
   to[0] = make_uint4(code[0][0], code[0][1], code[0][2], code[0][3]);
   to[1] = make_uint4(code[1][0], code[1][1], code[1][2], code[1][3]);
@@ -152,8 +153,8 @@ __global__ void __launch_bounds__(kThreads) ckpt_load_kernel(const CkptParams p)
   const int group = blockIdx.x / p.along;   // of tokens
   const int c = ((blockIdx.x - group * p.along) * (kThreads / 32) + warp) * 64 + lane * 2, n0 = group * kTokens;
   if (c >= p.C) return;
-  const int cb = c / kCkChannels, in = c & (kCkChannels - 1), q = group & 3;
-  const uint8_t* block = p.ck + ((int64_t)(group >> 2) * p.CB + cb) * kCkBlock;
+  const int cb = c / kCkChannels, in = c & (kCkChannels - 1), q = group & (kGroups - 1);
+  const uint8_t* block = p.ck + ((int64_t)(group / kGroups) * p.CB + cb) * kCkBlock;
   const uint4* from = reinterpret_cast<const uint4*>(block + q * 512 + in * 16);
   const uint4* scales = reinterpret_cast<const uint4*>(block + kCkCodes + q * 32);
   const uint4 a4 = __ldcs(from), b4 = __ldcs(from + 1), s4 = scales[0], t4 = scales[1];
@@ -192,7 +193,7 @@ stp_status check_ckpt(const stp_ckpt_desc* d) {
 template <typename T>
 void launch(const CkptParams& p, bool save, bool wide, cudaStream_t s) {
   // every 16 tokens of the last block are written, so that it ends in zeros
-  const int groups = save ? (int)ck_token_blocks(p.N) * (kCkTokens / kTokens) : (p.N + kTokens - 1) / kTokens;
+  const int groups = save ? (int)ck_token_blocks(p.N) * kGroups : (p.N + kTokens - 1) / kTokens;
   const unsigned grid = (unsigned)groups * p.along;
   if (save && wide) ckpt_save_kernel<T, true><<<grid, kThreads, 0, s>>>(p);
   else if (save) ckpt_save_kernel<T, false><<<grid, kThreads, 0, s>>>(p);

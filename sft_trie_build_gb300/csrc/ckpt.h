@@ -1,9 +1,9 @@
 // Layout of an activation checkpoint in 8 bits, and its exact return to bf16.
 //
-// A checkpoint of x [N, C] is an array of blocks of 64 tokens x 32 channels,
-// channel blocks of the same tokens side by side, 2176 bytes each:
-//   codes  uint32 [4][32][4]   e4m3 codes of tokens 16 q + 4 i .. 16 q + 4 i + 3, channel c, at [q][c][i]
-//   scale  bf16 [64]           of each token: scale times a code is the value
+// A checkpoint of x [N, C] is an array of blocks of 128 tokens x 32 channels,
+// channel blocks of the same tokens side by side, 4352 bytes each:
+//   codes  uint32 [8][32][4]   e4m3 codes of tokens 16 q + 4 i .. 16 q + 4 i + 3, channel c, at [q][c][i]
+//   scale  bf16 [128]          of each token: scale times a code is the value
 // Tokens lie next to one another, as the weight gradient contracts over them: a
 // thread that owns a channel reads 16 tokens at once.  Tokens and channels past
 // the end are zeros.  The scale is the smallest power of two, from 2^-117 on, at which the 32
@@ -29,7 +29,7 @@
 
 namespace stp {
 
-constexpr int kCkTokens = 64, kCkChannels = 32;
+constexpr int kCkTokens = 128, kCkChannels = 32;
 constexpr int kCkCodes = kCkTokens * kCkChannels;
 constexpr int kCkBlock = kCkCodes + kCkTokens * 2;   // bytes, a multiple of 16
 constexpr int kCkLeast = 10;                         // exponent field of 2^-117

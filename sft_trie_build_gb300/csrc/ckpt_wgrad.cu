@@ -9,8 +9,8 @@
 // Two blocks of a cluster multiply a tile of 256 channels x up to 256 columns
 // together (cta_group::2): each holds the sums of its 128 channels in TMEM and half of
 // dY's columns in shared memory.  Operand A is in TMEM, too: a warp owns 32
-// channels, a lane one of them (a TMEM lane), reads the codes of 64 tokens from
-// shared memory, turns them to bf16 (ckpt.h) and stores them to TMEM, eight stages of 32
+// channels, a lane one of them (a TMEM lane), reads the codes of 128 tokens from
+// shared memory, turns them to bf16 (ckpt.h) and stores them to TMEM, four stages of 64
 // columns behind the 256 columns of sums.  So shared memory carries the codes and half a tile of dY, by
 // bulk and tensor copies, and is read for operand B only.  dY lies there as in memory, tokens x columns
 // (MN-major, 128-byte swizzle).
@@ -56,20 +56,23 @@ constexpr int kThreads = 384;       // warps 0-7 convert and add up, 8 loads, 9 
 // 2 x 232 + 40 = 3 x 168.
 constexpr int kRegsSums = 232, kRegsRest = 40;
 constexpr int kGroups = 2;          // warp groups among them
-constexpr int kStages = 8;
-constexpr int kAhead = 6;           // stages converted ahead when sums are taken: less than kStages
-constexpr int kChunk = 32;          // stages between two takings
+// A stage is 128 tokens.  With 64 (and twice as many) a stage's waits and arrivals, about 600
+// cycles of its converting group, took as long as its conversion: 745 us for the
+// 16384-token projection against 549.
+constexpr int kStages = 4;
+constexpr int kAhead = 3;           // stages converted ahead when sums are taken: less than kStages
+constexpr int kChunk = 16;          // stages between two takings
 constexpr int kTileC = 256, kHalfC = 128, kTileM = 256;
-constexpr int kBoxBytes = 64 * 64 * 2;              // 64 tokens x 64 columns
+constexpr int kBoxBytes = kCkTokens * 64 * 2;       // 64 columns of a stage's tokens
 constexpr int kYBytes = 2 * kBoxBytes;              // a block's half of the columns
-constexpr int kCodeBytes = 4 * kCkBlock;            // 64 tokens x 128 channels
+constexpr int kCodeBytes = 4 * kCkBlock;            // 128 channels of them
 constexpr int kStageRow = 20;       // floats of a row of results on their way: 16, and 4 so that rows lie in other banks
 constexpr int kOffCodes = kStages * kYBytes, kOffStage = kOffCodes + kStages * kCodeBytes,
               kOffBars = kOffStage + 8 * 32 * kStageRow * 4;
 constexpr int kSmem = kOffBars + 512 + 1024;
 constexpr int kColA = 256;          // first TMEM column of A's stages
 constexpr size_t kPartBytes = (size_t)kHalfC * kTileM * 4;   // of a block
-constexpr int kLeastBlocks = 12;    // token blocks of a part at least
+constexpr int kLeastBlocks = 6;     // stages of a part at least
 
 struct WgradParams {
   int N, C, M, CB, KB, W;       // W: columns of a tile, a multiple of 32
@@ -121,6 +124,25 @@ __device__ __forceinline__ uint32_t in_block(uint32_t addr, int block) {
   return r;
 }
 
+// mbar_wait with the SM's clock, which is near, in place of the global timer:
+// a stage's waits lie on the path from one product to the next.
+constexpr long long kWaitLimitCycles = 4000000000ll;   // about 2 s
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      *abort = 1;
+      atomicOr(err, kErrTimeout);
+      return false;
+    }
+  }
+}
+
 // Arrives on a barrier of either block.  What the barriers between the blocks
 // order lies in TMEM, which tcgen05's own waits and fences order, so no wider
 // scope is asked for: a release at cluster scope waits for all memory (1250 us
@@ -154,28 +176,26 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       : "memory");
 }
 
-// A channel's codes of 32 tokens (the first or the second of a block's) in
-// shared memory to bf16 pairs of successive tokens.
+// A channel's codes of 64 tokens (the first or the second half of a block's)
+// in shared memory to bf16 pairs of successive tokens.
 __device__ __forceinline__ void convert(const uint8_t* block, int lane, int part, uint32_t* r) {
-  const uint4* from = reinterpret_cast<const uint4*>(block);
+  const uint4* codes = reinterpret_cast<const uint4*>(block) + part * 4 * 32 + lane;
+  const uint4* scales = reinterpret_cast<const uint4*>(block + kCkCodes) + part * 8;   // the same for all lanes
+  uint4 c[4];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const uint4 c4 = from[(part * 2 + q) * 32 + lane];
-    const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w};
+  for (int q = 0; q < 4; ++q) c[q] = codes[q * 32];
 #pragma unroll
-    for (int w = 0; w < 4; w += 2) {
-      const uint4 s4 = from[kCkCodes / 16 + part * 4 + q * 2 + w / 2];   // the same for all lanes
-      r[q * 8 + w * 2] = values_bf16x2(early_codes(c[w]), s4.x);
-      r[q * 8 + w * 2 + 1] = values_bf16x2(late_codes(c[w]), s4.y);
-      r[q * 8 + w * 2 + 2] = values_bf16x2(early_codes(c[w + 1]), s4.z);
-      r[q * 8 + w * 2 + 3] = values_bf16x2(late_codes(c[w + 1]), s4.w);
-    }
+  for (int q = 0; q < 4; ++q) {
+    const uint4 s = scales[q * 2], t = scales[q * 2 + 1];
+    r[q * 8] = values_bf16x2(early_codes(c[q].x), s.x);
+    r[q * 8 + 1] = values_bf16x2(late_codes(c[q].x), s.y);
+    r[q * 8 + 2] = values_bf16x2(early_codes(c[q].y), s.z);
+    r[q * 8 + 3] = values_bf16x2(late_codes(c[q].y), s.w);
+    r[q * 8 + 4] = values_bf16x2(early_codes(c[q].z), t.x);
+    r[q * 8 + 5] = values_bf16x2(late_codes(c[q].z), t.y);
+    r[q * 8 + 6] = values_bf16x2(early_codes(c[q].w), t.z);
+    r[q * 8 + 7] = values_bf16x2(late_codes(c[q].w), t.w);
   }
-}
-
-// B operand: 64-column boxes kBoxBytes apart (leading dimension), 8-token groups 1024 bytes apart.
-__device__ __forceinline__ uint32_t desc_lo_b(uint32_t addr) {
-  return ((addr & 0x3FFFFu) >> 4) | ((uint32_t)(kBoxBytes >> 4) << 16);
 }
 
 // The stages of a pair in order, over all its segments.
@@ -265,12 +285,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int st = 0; st < kStages; ++st) last[st] = landed[st] = -1;
       for (Walk w(p, g, pairs, last_wave, n_last); w.on(); w.next(), ++it) {
         const int st = it % kStages, n = it / kStages;
-        if (it >= kStages && !mbar_wait(&bars[W_E + st], (n - 1) & 1, abort_flag, p.err)) break;
+        if (it >= kStages && !wait(&bars[W_E + st], (n - 1) & 1, abort_flag, p.err)) break;
         const int m0 = w.s.tile / p.CT * p.W + block * (p.W / 2), cb = w.s.tile % p.CT * 8 + block * 4;
         const uint32_t bar = in_block(smem_u32(&bars[W_BF + st]), 0);
         if (block == 0) mbar_expect_tx(&bars[W_BF + st], 2 * boxes * kBoxBytes);
         for (int b = 0; b < boxes; ++b)
-          tma_load_pair(smem + st * kYBytes + b * kBoxBytes, &ty, bar, m0 + b * 64, w.kb * 64);
+          tma_load_pair(smem + st * kYBytes + b * kBoxBytes, &ty, bar, m0 + b * 64, w.kb * kCkTokens);
         last[st] = n & 1;
         if (cb < p.CB) {
           const uint32_t bytes = min(4, p.CB - cb) * kCkBlock;
@@ -293,16 +313,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t idesc = idesc_bf16(kTileC, p.W, 0, 1);
       int it = 0, chunk = 0, in = 0;
       for (Walk w(p, g, pairs, last_wave, n_last); w.on(); ++it) {
-        if (in == 0 && chunk > 0 && !mbar_wait(&bars[W_DE], (chunk - 1) & 1, abort_flag, p.err)) break;
+        if (in == 0 && chunk > 0 && !wait(&bars[W_DE], (chunk - 1) & 1, abort_flag, p.err)) break;
         const int st = it % kStages;
         const uint32_t phase = (it / kStages) & 1;
-        if (!mbar_wait(&bars[W_BF + st], phase, abort_flag, p.err) ||
-            !mbar_wait(&bars[W_AF + st], phase, abort_flag, p.err))
+        if (!wait(&bars[W_BF + st], phase, abort_flag, p.err) ||
+            !wait(&bars[W_AF + st], phase, abort_flag, p.err))
           break;
         fence_after_sync();
-        const uint32_t b_lo = desc_lo_b(smem_u32(smem) + st * kYBytes), a = tmem + kColA + st * 32;
+        const uint32_t b_lo = desc_lo_mnmajor(smem_u32(smem) + st * kYBytes), a = tmem + kColA + st * 64;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_pair(tmem, a + kk * 8, b_lo + kk * (2048 >> 4), idesc, in > 0 || kk > 0);
+        for (int kk = 0; kk < kCkTokens / 16; ++kk) mma_pair(tmem, a + kk * 8, b_lo + kk * (2048 >> 4), idesc, in > 0 || kk > 0);
         commit_pair(&bars[W_E + st]);
         const int tile = w.i;
         w.next();
@@ -339,28 +359,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int st = it % kStages, n = it / kStages;
         const bool there = c.s.tile % p.CT * 8 + block * 4 + w4 < p.CB;
         // the codes, and TMEM's stage
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars[W_CF + st], n & 1, abort_flag, p.err) &&
-                                         (it < kStages || mbar_wait(&bars[W_E + st], (n - 1) & 1, abort_flag, p.err)))) {
+        if (!__all_sync(0xffffffffu, wait(&bars[W_CF + st], n & 1, abort_flag, p.err) &&
+                                         (it < kStages || wait(&bars[W_E + st], (n - 1) & 1, abort_flag, p.err)))) {
           ok = false;
           break;
         }
         fence_after_sync();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t r[16];
+          uint32_t r[32];
           if (there) convert(codes + st * kCodeBytes + w4 * kCkBlock, lane, h, r);
           else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) r[e] = 0;
+            for (int e = 0; e < 32; ++e) r[e] = 0;
           }
-          tmem_st16(tmem + lane_base + kColA + st * 32 + h * 16, r);
+          tmem_st32(tmem + lane_base + kColA + st * 64 + h * 32, r);
         }
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
         if (lane == 0) arrive_in(in_block(smem_u32(&bars[W_AF + st]), 0));
       }
-      if (!ok || !__all_sync(0xffffffffu, mbar_wait(&bars[W_DF], chunk & 1, abort_flag, p.err))) break;
+      if (!ok || !__all_sync(0xffffffffu, wait(&bars[W_DF], chunk & 1, abort_flag, p.err))) break;
       fence_after_sync();
 #pragma unroll
       for (int j = 0; j < kTileM / 2; j += 16)
@@ -451,13 +471,13 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// dY [N, M], rows `stride` elements apart: boxes of 64 columns x 64 tokens; zeros outside.
+// dY [N, M], rows `stride` elements apart: boxes of 64 columns x 128 tokens; zeros outside.
 bool make_map(CUtensorMap* m, const void* base, int N, int M, int64_t stride) {
   EncodeFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)M, (cuuint64_t)N};
   cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-  cuuint32_t box[2] = {64, 64};
+  cuuint32_t box[2] = {64, kCkTokens};
   cuuint32_t estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
