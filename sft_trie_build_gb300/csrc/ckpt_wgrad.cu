@@ -51,7 +51,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;       // warps 0-7 convert and add up, 8 loads, 9 multiplies
+constexpr int kThreads = 384;       // warps 0-7 convert and add up, 8 loads dY, 9 multiplies, 10 loads codes
 // Registers of a thread: 168 at launch (65536 / 384), of which the warps that keep no sums give theirs up:
 // 2 x 232 + 40 = 3 x 168.
 constexpr int kRegsSums = 232, kRegsRest = 40;
@@ -111,10 +111,12 @@ __device__ __forceinline__ int last_segments(const WgradParams& p, int g, int pa
   return n;
 }
 
-// Barriers: the codes of a stage have landed (both blocks'), dY of both blocks
-// has landed and A of both is in place (first block's), the stage is free
-// (both); the sums of a chunk are ready (both) and taken by both (first block's).
-enum { W_CF = 0, W_BF = kStages, W_AF = 2 * kStages, W_E = 3 * kStages, W_DF = 4 * kStages, W_DE, W_DRAIN, W_COUNT };
+// Barriers: the codes of a stage have landed and are read (each block's own),
+// dY of both blocks has landed and A of both is in place (first block's), the
+// stage is multiplied (both); the sums of a chunk are ready (both) and taken by both (first
+// block's).  Codes are fetched again as soon as they are read, so that their way from memory
+// does not lie between a product and the next conversion for its stage.
+enum { W_CF = 0, W_CE = kStages, W_BF = 2 * kStages, W_AF = 3 * kStages, W_E = 4 * kStages, W_DF = 5 * kStages, W_DE, W_DRAIN, W_COUNT };
 
 // ---- a pair's instructions
 
@@ -141,6 +143,18 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
       return false;
     }
   }
+}
+
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // Arrives on a barrier of either block.  What the barriers between the blocks
@@ -258,7 +272,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < W_COUNT; ++b)
-      mbar_init(&bars[b], b >= W_AF && b < W_AF + kStages ? 8 : b == W_DE ? 16 : 1);
+      mbar_init(&bars[b], b >= W_AF && b < W_AF + kStages ? 8 : b >= W_CE && b < W_CE + kStages ? 4 : b == W_DE ? 16 : 1);
     *abort_flag = 0;
     *n_last_wave = last_segments(p, g, pairs, last_wave);
     fence_mbar_init();
@@ -278,33 +292,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     regs_dec<kRegsRest>();
     if (warp == 8) {
     if (lane == 0) {
-      // ------------------------------------------------------------ loads
+      // -------------------------------------------------------------- dY
       tma_prefetch_desc(&ty);
       const int boxes = (p.W / 2 + 63) / 64;
-      int it = 0, last[kStages], landed[kStages];   // phase of a stage's last load, and of its last codes
-      for (int st = 0; st < kStages; ++st) last[st] = landed[st] = -1;
+      int it = 0, last[kStages];   // phase of a stage's last load
+      for (int st = 0; st < kStages; ++st) last[st] = -1;
       for (Walk w(p, g, pairs, last_wave, n_last); w.on(); w.next(), ++it) {
         const int st = it % kStages, n = it / kStages;
         if (it >= kStages && !wait(&bars[W_E + st], (n - 1) & 1, abort_flag, p.err)) break;
-        const int m0 = w.s.tile / p.CT * p.W + block * (p.W / 2), cb = w.s.tile % p.CT * 8 + block * 4;
+        const int m0 = w.s.tile / p.CT * p.W + block * (p.W / 2);
         const uint32_t bar = in_block(smem_u32(&bars[W_BF + st]), 0);
         if (block == 0) mbar_expect_tx(&bars[W_BF + st], 2 * boxes * kBoxBytes);
         for (int b = 0; b < boxes; ++b)
           tma_load_pair(smem + st * kYBytes + b * kBoxBytes, &ty, bar, m0 + b * 64, w.kb * kCkTokens);
         last[st] = n & 1;
+      }
+      for (int st = 0; st < kStages; ++st)
+        if (block == 0 && last[st] >= 0) mbar_wait_drain(&bars[W_BF + st], last[st]);
+    }
+    __syncwarp();
+    } else if (warp == 10) {
+    if (lane == 0) {
+      // ----------------------------------------------------------- codes
+      int it = 0, last[kStages];
+      for (int st = 0; st < kStages; ++st) last[st] = -1;
+      for (Walk w(p, g, pairs, last_wave, n_last); w.on(); w.next(), ++it) {
+        const int st = it % kStages, n = it / kStages, cb = w.s.tile % p.CT * 8 + block * 4;
+        if (it >= kStages && !wait(&bars[W_CE + st], (n - 1) & 1, abort_flag, p.err)) break;
         if (cb < p.CB) {
           const uint32_t bytes = min(4, p.CB - cb) * kCkBlock;
           mbar_expect_tx(&bars[W_CF + st], bytes);
           bulk_load(codes + st * kCodeBytes, p.ck + ((int64_t)w.kb * p.CB + cb) * kCkBlock, bytes, &bars[W_CF + st]);
-          landed[st] = n & 1;
+          last[st] = n & 1;
         } else {
           mbar_arrive(&bars[W_CF + st]);   // channels past the end: nothing comes
         }
       }
-      for (int st = 0; st < kStages; ++st) {
-        if (landed[st] >= 0) mbar_wait_drain(&bars[W_CF + st], landed[st]);
-        if (block == 0 && last[st] >= 0) mbar_wait_drain(&bars[W_BF + st], last[st]);
-      }
+      for (int st = 0; st < kStages; ++st)
+        if (last[st] >= 0) mbar_wait_drain(&bars[W_CF + st], last[st]);
     }
     __syncwarp();
     } else if (warp == 9) {
@@ -355,6 +380,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int len = min(kChunk, d.s.kb1 - d.kb);
       end += len;
       for (; c.on() && it < end + kAhead; ++it, c.next()) {
+        // the tensor core waits: first the sums
+        if (it >= end && __any_sync(0xffffffffu, test(&bars[W_DF], chunk & 1))) break;
         if (it % kGroups != group) continue;
         const int st = it % kStages, n = it / kStages;
         const bool there = c.s.tile % p.CT * 8 + block * 4 + w4 < p.CB;
@@ -375,6 +402,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           tmem_st32(tmem + lane_base + kColA + st * 64 + h * 32, r);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[W_CE + st]);   // the codes are read
         tmem_st_wait();
         fence_before_sync();
         __syncwarp();
