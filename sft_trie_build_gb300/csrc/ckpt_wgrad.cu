@@ -129,6 +129,7 @@ __device__ __forceinline__ uint32_t in_block(uint32_t addr, int block) {
 // mbar_wait with the SM's clock, which is near, in place of the global timer:
 // a stage's waits lie on the path from one product to the next.
 constexpr long long kWaitLimitCycles = 4000000000ll;   // about 2 s
+constexpr uint64_t kDrainLimitNs = 20000000000ull;     // of a whole launch
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
@@ -190,17 +191,23 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
       : "memory");
 }
 
+// 16 bytes of shared memory (through a generic address they take longer).
+__device__ __forceinline__ uint4 load_shared(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+
 // A channel's codes of 64 tokens (the first or the second half of a block's)
 // in shared memory to bf16 pairs of successive tokens.
-__device__ __forceinline__ void convert(const uint8_t* block, int lane, int part, uint32_t* r) {
-  const uint4* codes = reinterpret_cast<const uint4*>(block) + part * 4 * 32 + lane;
-  const uint4* scales = reinterpret_cast<const uint4*>(block + kCkCodes) + part * 8;   // the same for all lanes
+__device__ __forceinline__ void convert(uint32_t block, int lane, int part, uint32_t* r) {
+  const uint32_t codes = block + part * 2048 + lane * 16, scales = block + kCkCodes + part * 128;
   uint4 c[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) c[q] = codes[q * 32];
+  for (int q = 0; q < 4; ++q) c[q] = load_shared(codes + q * 512);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const uint4 s = scales[q * 2], t = scales[q * 2 + 1];
+    const uint4 s = load_shared(scales + q * 32), t = load_shared(scales + q * 32 + 16);   // the same for all lanes
     r[q * 8] = values_bf16x2(early_codes(c[q].x), s.x);
     r[q * 8 + 1] = values_bf16x2(late_codes(c[q].x), s.y);
     r[q * 8 + 2] = values_bf16x2(early_codes(c[q].y), s.z);
@@ -217,9 +224,9 @@ struct Walk {
   Segment s;
   int i = 0, kb = 0;
   const Segment* last;   // of the last wave, in shared memory
-  int n, whole, KB, pairs;
+  int n, whole, KB, CT, pairs, ct, mt;   // the tile's place along channels and columns
   __device__ __forceinline__ Walk(const WgradParams& p, int g, int pairs_, const Segment* last_, int n_last)
-      : last(last_), n(p.whole + n_last), whole(p.whole), KB(p.KB), pairs(pairs_) {
+      : last(last_), n(p.whole + n_last), whole(p.whole), KB(p.KB), CT(p.CT), pairs(pairs_) {
     s.tile = g - pairs;
     enter();
   }
@@ -230,6 +237,8 @@ struct Walk {
       s = last[i - whole];
     }
     kb = s.kb0;
+    mt = s.tile / CT;
+    ct = s.tile - mt * CT;
   }
   __device__ __forceinline__ bool on() const { return i < n; }
   __device__ __forceinline__ void next() {
@@ -300,7 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (Walk w(p, g, pairs, last_wave, n_last); w.on(); w.next(), ++it) {
         const int st = it % kStages, n = it / kStages;
         if (it >= kStages && !wait(&bars[W_E + st], (n - 1) & 1, abort_flag, p.err)) break;
-        const int m0 = w.s.tile / p.CT * p.W + block * (p.W / 2);
+        const int m0 = w.mt * p.W + block * (p.W / 2);
         const uint32_t bar = in_block(smem_u32(&bars[W_BF + st]), 0);
         if (block == 0) mbar_expect_tx(&bars[W_BF + st], 2 * boxes * kBoxBytes);
         for (int b = 0; b < boxes; ++b)
@@ -317,7 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int it = 0, last[kStages];
       for (int st = 0; st < kStages; ++st) last[st] = -1;
       for (Walk w(p, g, pairs, last_wave, n_last); w.on(); w.next(), ++it) {
-        const int st = it % kStages, n = it / kStages, cb = w.s.tile % p.CT * 8 + block * 4;
+        const int st = it % kStages, n = it / kStages, cb = w.ct * 8 + block * 4;
         if (it >= kStages && !wait(&bars[W_CE + st], (n - 1) & 1, abort_flag, p.err)) break;
         if (cb < p.CB) {
           const uint32_t bytes = min(4, p.CB - cb) * kCkBlock;
@@ -359,14 +368,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       commit_pair(&bars[W_DRAIN]);
     }
-    // nothing of the pair is in flight behind this
-    if (lane == 0) mbar_wait_drain(&bars[W_DRAIN], 0);
+    // nothing of the pair is in flight behind this; the second block's wait is all it does, so it looks rarely
+    if (lane == 0)
+      for (const uint64_t t0 = globaltimer(); !mbar_try_wait(&bars[W_DRAIN], 0) && globaltimer() - t0 < kDrainLimitNs;) __nanosleep(500);
     __syncwarp();
     }
   } else {
     regs_inc<kRegsSums>();
     const int group = warp >> 2, w4 = warp & 3, half = p.W / 2;
     const uint32_t lane_base = (uint32_t)(w4 * 32) << 16;
+    const uint32_t codes_at = smem_u32(codes) + w4 * kCkBlock;
     const uint32_t taken = in_block(smem_u32(&bars[W_DE]), 0);
     float* stage = reinterpret_cast<float*>(smem + kOffStage) + warp * 32 * kStageRow;
     float acc[kTileM / 2];
@@ -384,7 +395,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (it >= end && __any_sync(0xffffffffu, test(&bars[W_DF], chunk & 1))) break;
         if (it % kGroups != group) continue;
         const int st = it % kStages, n = it / kStages;
-        const bool there = c.s.tile % p.CT * 8 + block * 4 + w4 < p.CB;
         // the codes, and TMEM's stage
         if (!__all_sync(0xffffffffu, wait(&bars[W_CF + st], n & 1, abort_flag, p.err) &&
                                          (it < kStages || wait(&bars[W_E + st], (n - 1) & 1, abort_flag, p.err)))) {
@@ -392,15 +402,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         fence_after_sync();
+        if (c.ct * 8 + block * 4 + w4 < p.CB) {   // channels past the end: sums that nothing reads
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t r[32];
-          if (there) convert(codes + st * kCodeBytes + w4 * kCkBlock, lane, h, r);
-          else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = 0;
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            convert(codes_at + st * kCodeBytes, lane, h, r);
+            tmem_st32(tmem + lane_base + kColA + st * 64 + h * 32, r);
           }
-          tmem_st32(tmem + lane_base + kColA + st * 64 + h * 32, r);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[W_CE + st]);   // the codes are read
@@ -423,13 +431,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       fence_before_sync();
       __syncwarp();
       if (lane == 0) arrive_in(taken);
-      const int tile = d.s.tile, slot = d.s.slot, segment = d.i;
+      const int ct = d.ct, mt = d.mt, slot = d.s.slot, segment = d.i;
       d.kb += len - 1;
       d.next();
       if (d.i == segment) continue;
       // the segment's results, 16 columns of 32 channels at a time through
       // shared memory, so that they leave in rows
-      const int c0 = tile % p.CT * kTileC + block * kHalfC + w4 * 32, m0 = tile / p.CT * p.W + group * half;
+      const int c0 = ct * kTileC + block * kHalfC + w4 * 32, m0 = mt * p.W + group * half;
       float4* part = reinterpret_cast<float4*>(p.part) + (size_t)(max(slot, 0) * 2 + block) * (kPartBytes / 16) + w4 * 32 + lane +
                      group * half / 4 * kHalfC;
 #pragma unroll
