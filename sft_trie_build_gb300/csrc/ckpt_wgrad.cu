@@ -75,7 +75,7 @@ constexpr size_t kPartBytes = (size_t)kHalfC * kTileM * 4;   // of a block
 constexpr int kLeastBlocks = 6;     // stages of a part at least
 
 struct WgradParams {
-  int N, C, M, CB, KB, W;       // W: columns of a tile, a multiple of 32
+  int N, C, M, CB, KB, W;       // W: columns of a tile, a multiple of 16
   int CT, MT;                   // tiles along channels and columns
   int whole, rest, parts;       // waves of whole tiles; tiles of the last wave, and pairs that share them
   bool add, vec;                // vec: rows of dW start at whole 16 bytes
@@ -86,8 +86,9 @@ struct WgradParams {
 };
 
 // The share of pair g in the last wave: token blocks [at, end) of `rest` tiles of KB each.
-__host__ __device__ __forceinline__ int64_t share(const WgradParams& p, int g) {
-  return (int64_t)p.rest * p.KB * g / p.parts;
+// The products stay below 2^31: fewer tiles than pairs (76), at most 2^17 stages each, times a pair's number.
+__device__ __forceinline__ int share(const WgradParams& p, int g) {
+  return (int)((uint32_t)(p.rest * p.KB) * (uint32_t)g / (uint32_t)p.parts);
 }
 
 struct Segment {
@@ -97,15 +98,14 @@ struct Segment {
 // The one or two segments of pair g in the last wave; returns how many.
 __device__ __forceinline__ int last_segments(const WgradParams& p, int g, int pairs, Segment* to) {
   if (g >= p.parts) return 0;
-  const int64_t at = share(p, g), end = share(p, g + 1);
-  const int first = (int)(at / p.KB);
+  const int at = share(p, g), end = share(p, g + 1), first = at / p.KB;
   int n = 0;
-  for (int tile = first; n < 2 && (int64_t)tile * p.KB < end; ++tile, ++n) {
-    const int64_t t0 = (int64_t)tile * p.KB;
+  for (int tile = first; n < 2 && tile * p.KB < end; ++tile, ++n) {
+    const int t0 = tile * p.KB;
     Segment& s = to[n];
     s.tile = p.whole * pairs + tile;
-    s.kb0 = (int)(max(t0, at) - t0);
-    s.kb1 = (int)(min(t0 + p.KB, end) - t0);
+    s.kb0 = max(t0, at) - t0;
+    s.kb1 = min(t0 + p.KB, end) - t0;
     s.slot = s.kb0 == 0 && s.kb1 == p.KB ? -1 : 2 * g + n;
   }
   return n;
@@ -283,6 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int b = 0; b < W_COUNT; ++b)
       mbar_init(&bars[b], b >= W_AF && b < W_AF + kStages ? 8 : b >= W_CE && b < W_CE + kStages ? 4 : b == W_DE ? 16 : 1);
     *abort_flag = 0;
+    if (blockIdx.x == 0) *p.err = 0;   // a lost wait sets it seconds later
     *n_last_wave = last_segments(p, g, pairs, last_wave);
     fence_mbar_init();
   }
@@ -445,7 +446,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (j >= half) continue;
         if (slot >= 0) {
 #pragma unroll
-          for (int e = j; e < j + 16; e += 4) part[e / 4 * kHalfC] = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+          for (int e = j; e < j + 16; e += 4)
+            if (e < half) part[e / 4 * kHalfC] = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
         } else {
           __syncwarp();
 #pragma unroll
@@ -473,18 +475,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // Adds up the parts of a tile of the last wave; a block does 4 columns x 256 channels.
 __global__ void __launch_bounds__(256) wgrad_join_kernel(const WgradParams p) {
   const int tile = blockIdx.y;   // of the last wave
-  const int64_t a = (int64_t)tile * p.KB, b = a + p.KB, all = (int64_t)p.rest * p.KB;
-  int g = (int)(a * p.parts / all);   // the first pair whose share reaches past a
-  while (g > 0 && share(p, g) > a) --g;
-  while (share(p, g + 1) <= a) ++g;
-  if (share(p, g) <= a && share(p, g + 1) >= b) return;   // one pair did it all
+  const int a = tile * p.KB, b = a + p.KB;
+  int g0 = (int)((uint32_t)a * (uint32_t)p.parts / (uint32_t)(p.rest * p.KB));   // the first pair whose share reaches past a
+  while (g0 > 0 && share(p, g0) > a) --g0;
+  while (share(p, g0 + 1) <= a) ++g0;
+  int g1 = g0 + 1;   // one past the last pair with a share of the tile
+  while (g1 < p.parts && share(p, g1) < b) ++g1;
+  if (g1 == g0 + 1) return;   // one pair did it all
   const int c4 = blockIdx.x, block = threadIdx.x >> 7, r = threadIdx.x & 127;
+  // only the first share may begin in another tile, whose part comes first
+  const bool second = share(p, g0) < a;
+  const float4* from = reinterpret_cast<const float4*>(p.part) + (size_t)block * (kPartBytes / 16) + c4 * kHalfC + r;
+  constexpr size_t kSlot = 2 * kPartBytes / 16;   // of a pair's part
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (; g < p.parts && share(p, g) < b; ++g) {
-    const int slot = 2 * g + (share(p, g) / p.KB != tile);
-    const float4 v =
-        __ldcs(reinterpret_cast<const float4*>(p.part) + (size_t)(slot * 2 + block) * (kPartBytes / 16) + c4 * kHalfC + r);
-    sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+  for (int g = g0; g < g1; g += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      v[k] = g + k < g1 ? __ldcs(from + (size_t)(2 * (g + k) + (second && g + k == g0)) * kSlot) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum = make_float4(sum.x + v[k].x, sum.y + v[k].y, sum.z + v[k].z, sum.w + v[k].w);
   }
   const int which = p.CT * p.MT - p.rest + tile, c = which % p.CT * kTileC + threadIdx.x;
   const int m0 = which / p.CT * p.W, m = m0 + c4 * 4, end = min(p.M, m0 + p.W);
@@ -537,7 +547,7 @@ int plan(WgradParams& p, const stp_ckpt_desc* d, int cols, int n_sm) {
   p.KB = (int)ck_token_blocks(p.N);
   p.CT = (p.C + kTileC - 1) / kTileC;
   p.MT = (p.M + kTileM - 1) / kTileM;
-  p.W = ((p.M + p.MT - 1) / p.MT + 31) / 32 * 32;   // tiles of one width, not full ones and a narrow last
+  p.W = ((p.M + p.MT - 1) / p.MT + 15) / 16 * 16;   // tiles of one width, not full ones and a narrow last
   const int64_t tiles = (int64_t)p.CT * p.MT;
   const int pairs = n_sm / 2;
   p.whole = (int)(tiles / pairs);
@@ -580,10 +590,11 @@ extern "C" stp_status stp_ckpt_wgrad(const stp_ckpt_desc* desc, int32_t cols, co
   if (y_stride < cols || y_stride % 8)
     return fail(STP_EINVAL, "stp_ckpt_wgrad: y_stride must be at least cols and a multiple of 8");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemsetAsync(d_ws, 0, 4, s);
-  if (e == cudaSuccess && desc->n_tokens == 0) {
-    if (!accumulate) e = cudaMemsetAsync(d_w, 0, (size_t)desc->dim * cols * 4, s);
-  } else if (e == cudaSuccess) {
+  cudaError_t e = cudaSuccess;
+  if (desc->n_tokens == 0) {
+    e = cudaMemsetAsync(d_ws, 0, 4, s);
+    if (e == cudaSuccess && !accumulate) e = cudaMemsetAsync(d_w, 0, (size_t)desc->dim * cols * 4, s);
+  } else {
     int dev = 0, n_sm = 0;
     e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
