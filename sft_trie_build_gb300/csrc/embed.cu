@@ -6,16 +6,16 @@
 //
 // The gradient adds up rows of d_out that lie anywhere, some tokens once, some
 // thousands of times, in an order that does not depend on timing:
-//   embed_sort_kernel   one cluster of eight blocks sorts (token, position) by token,
-//                 stable, in two or three passes over 9 bits or less; the other
-//                 blocks meanwhile write zeros over the rows of tokens that do not occur
+//   embed_sort_kernel   every block takes a range of tokens out of all positions, in
+//                 order, and sorts (token, position) by token, stable, in one or two
+//                 passes over 9 bits or less; no block waits for another one.  It also
+//                 writes zeros over the rows of its tokens that do not occur
 //   embed_sum_kernel    pieces of 32 sorted entries each: a thread adds its 16 bytes of
 //                 channels entry by entry.  A token that occurs 64 times at most is added up
 //                 where it begins, also beyond the piece; what a piece holds of
 //                 another one goes to the workspace
 //   embed_join_kernel   those tokens: the sums of their pieces, in order
 // Every row of d_out is read once and every row of dE written once.  Sums are float32.
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,19 +24,18 @@
 #include "logit_rows.cuh"
 #include "per_device.h"
 
-namespace cg = cooperative_groups;
-
 namespace stp {
 namespace {
 
 using rows::Piece;
 
 constexpr int kThreads = 256;
-constexpr int kSortBlocks = 8;      // the portable cluster size
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 512;
-constexpr int kHeld = 8;            // entries of a lane in registers: all of them up to 65536 tokens
+constexpr int kHeld = 8;            // entries of a lane in registers
+constexpr int kMaxWords = 4128;     // of 32 tokens in a block's range: 2^24 tokens over 128 blocks or more
+constexpr int kScan = 64;           // positions of a lane in a walk over them
 constexpr int kPiece = 32;          // sorted entries of a piece
 constexpr int kShort = 64;          // entries of a token that one block adds up, at most
 constexpr int kJoinAlong = 32, kJoinRows = kThreads / kJoinAlong;
@@ -51,6 +50,7 @@ struct EmbedParams {
   void* out;
   uint32_t* err;
   // backward
+  int blocks;              // of the sort; each takes whole groups of 32 tokens
   int bits, passes;        // of a sort pass; the last pass writes to `sorted`
   const void* d_out;
   uint64_t* sorted;        // token << 32 | position, ascending; token V: none
@@ -107,139 +107,205 @@ __global__ void __launch_bounds__(kThreads) embed_fwd_kernel(const EmbedParams p
 
 struct SortShared {
   uint32_t hist[kSortWarps][kMaxBins];       // entries of a warp before it, then where the next goes
-  uint32_t total[kSortBlocks][kMaxBins];     // of each block of the cluster
   uint32_t base[kMaxBins];
+  uint32_t seen[kMaxWords];
   uint32_t warp_sum[kSortWarps];
-  uint32_t bad[kSortBlocks];
+  uint32_t below;
 };
 
-__device__ __forceinline__ uint64_t entry_of(const EmbedParams& p, int i) {
-  const int tok = p.tok[i];
-  return ((uint64_t)(uint32_t)(tok < 0 || tok >= p.V ? p.V : tok) << 32) | (uint32_t)i;
+// The sum of the warps' numbers before this one, and of all; every thread of the block calls it.
+__device__ __forceinline__ uint32_t before_warp(SortShared& sh, uint32_t mine, uint32_t& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  if (lane == 0) sh.warp_sum[warp] = mine;
+  __syncthreads();
+  const uint32_t x = sh.warp_sum[lane];
+  all = __reduce_add_sync(0xffffffffu, x);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? x : 0);
 }
 
-// Writes zeros over the rows of tokens that do not occur, block `at` of `of`.
-__device__ void fill_absent(const EmbedParams& p, uint32_t* seen, int at, int of) {
-  const int v0 = (int)((int64_t)p.V * at / of), v1 = (int)((int64_t)p.V * (at + 1) / of);
-  const int t = threadIdx.x;
-  for (int i = t; i < (v1 - v0 + 31) / 32; i += kSortThreads) seen[i] = 0;
-  __syncthreads();
-  for (int i0 = t; i0 < p.N; i0 += 16 * kSortThreads) {
-    int x[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] = i0 + k * kSortThreads < p.N ? p.tok[i0 + k * kSortThreads] - v0 : -1;
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (x[k] >= 0 && x[k] < v1 - v0) atomicOr(seen + (x[k] >> 5), 1u << (x[k] & 31));
-  }
-  __syncthreads();
-  for (int v = v0 + (t >> 5); v < v1; v += kSortWarps) {
-    if (seen[(v - v0) >> 5] >> ((v - v0) & 31) & 1) continue;
-    float4* row = reinterpret_cast<float4*>(p.d_table + (int64_t)v * p.C);
-    for (int i = t & 31; i < p.C / 4; i += 32) __stcs(row + i, make_float4(0.f, 0.f, 0.f, 0.f));
-  }
-}
-
-__global__ void __cluster_dims__(kSortBlocks, 1, 1) __launch_bounds__(kSortThreads, 1)
-    embed_sort_kernel(const EmbedParams p) {
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const EmbedParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   SortShared& sh = *reinterpret_cast<SortShared*>(smem);
-  if (blockIdx.x >= kSortBlocks) {
-    fill_absent(p, reinterpret_cast<uint32_t*>(smem), blockIdx.x - kSortBlocks, gridDim.x - kSortBlocks);
-    return;
+  const int k = blockIdx.x, t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const unsigned below_me = (1u << lane) - 1;
+  // the block's tokens, in groups of 32; V stands for no token
+  const int words = (p.V >> 5) + 1;
+  const int w0 = (int)((int64_t)words * k / p.blocks), w1 = (int)((int64_t)words * (k + 1) / p.blocks);
+  if (w0 == w1) return;   // never the last block
+  const uint32_t v0 = (uint32_t)w0 * 32, v1 = (uint32_t)w1 * 32;
+  for (int i = t; i < w1 - w0; i += kSortThreads) sh.seen[i] = 0;
+  if (t == 0) sh.below = 0;
+
+  // ---- the block's entries, in order of position: kScan positions of a lane
+  // at a time, a warp's next to one another.  As unsigned numbers, tokens that
+  // are none lie behind all others, in the last block's range.
+  constexpr int kRound = kSortThreads * kScan;
+  const uint32_t span = k == p.blocks - 1 ? ~v0 : v1 - 1 - v0;
+  uint32_t below = 0, first = 0;   // entries of smaller tokens: the block's place among the sorted ones
+  if (p.N > kRound) {
+    for (int i0 = t; i0 < p.N; i0 += 16 * kSortThreads) {
+      uint32_t x[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = i0 + j * kSortThreads < p.N ? (uint32_t)p.tok[i0 + j * kSortThreads] : ~0u;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) below += x[j] < v0;
+    }
+    before_warp(sh, __reduce_add_sync(0xffffffffu, below), first);
   }
-  cg::cluster_group cl = cg::this_cluster();
-  const int rank = blockIdx.x, t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int bins = 1 << p.bits;
-  // a warp's entries, in order of position over warps and blocks
-  const int groups = (p.N + 31) / 32, all = kSortBlocks * kSortWarps, me = rank * kSortWarps + warp;
-  const int lo = (int)((int64_t)groups * me / all) * 32, hi = min(p.N, (int)((int64_t)groups * (me + 1) / all) * 32);
+  uint64_t *even = p.sorted, *odd = p.other;
+  uint32_t n = 0;   // the block's entries so far
+  for (int r0 = 0; r0 < p.N; r0 += kRound) {
+    // a lane's positions: at + 32 j, those below the end
+    const int each = min(kScan, ((p.N - r0 + kSortThreads - 1) / kSortThreads + 15) / 16 * 16);
+    const int at = r0 + warp * each * 32 + lane;
+    const int there = max(0, min(each, (p.N - at + 31) / 32));
+    uint64_t in = 0, less = 0;   // bit j: position at + 32 j is the block's, or one of a smaller token
+#pragma unroll 1
+    for (int j0 = 0; j0 < each; j0 += 16) {
+      uint32_t x[16], a = 0, b = 0;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) x[j] = (uint32_t)p.tok[min(at + (j0 + j) * 32, p.N - 1)];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        a |= x[j] - v0 <= span ? 1u << j : 0;
+        b |= x[j] < v0 ? 1u << j : 0;
+      }
+      in |= (uint64_t)a << j0;
+      less |= (uint64_t)b << j0;
+    }
+    const uint64_t keep = there == 64 ? ~0ull : (1ull << there) - 1;
+    in &= keep;
+    below = __popcll(less & keep);
+    const uint32_t mine = __reduce_add_sync(0xffffffffu, (uint32_t)__popcll(in));
+    uint32_t all, place = before_warp(sh, mine, all);
+    if (p.N <= kRound) before_warp(sh, __reduce_add_sync(0xffffffffu, below), first);
+    if (r0 == 0) {
+      even += first;
+      odd += first;
+    }
+    place += n;
+    n += all;
+    uint64_t* to = p.passes & 1 ? odd : even;
+    // words of the warp's bits: positions that any lane has
+    const uint32_t any[2] = {__reduce_or_sync(0xffffffffu, (uint32_t)in), __reduce_or_sync(0xffffffffu, (uint32_t)(in >> 32))};
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      for (uint32_t left = any[h]; left; left &= left - 1) {
+        const int j = h * 32 + __ffs(left) - 1;
+        const bool on = in >> j & 1;
+        const unsigned who = __ballot_sync(0xffffffffu, on);
+        if (on) to[place + __popc(who & below_me)] = (uint32_t)(at + j * 32);
+        place += __popc(who);
+      }
+  }
+  __syncthreads();   // the positions are in place
+  // their tokens, which a walk position by position would wait for one by one
   bool bad = false;
-  cl.sync();   // every block runs: others may write to it
+  for (uint32_t i0 = t; i0 < n; i0 += 4 * kSortThreads) {
+    uint64_t* e = (p.passes & 1 ? odd : even) + i0;
+    uint32_t at[4];
+    int x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) at[j] = i0 + j * kSortThreads < n ? (uint32_t)e[j * kSortThreads] : ~0u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = at[j] != ~0u ? p.tok[at[j]] : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (at[j] != ~0u) {
+        bad |= x[j] >= p.V;
+        const uint32_t token = x[j] < 0 || x[j] >= p.V ? (uint32_t)p.V : (uint32_t)x[j];
+        e[j * kSortThreads] = (uint64_t)token << 32 | at[j];
+        // a word that holds the bit already is not written: many atomics on one word would come one by one
+        uint32_t* word = &sh.seen[(token - v0) >> 5];
+        if (!(*reinterpret_cast<volatile uint32_t*>(word) >> (token & 31) & 1)) atomicOr(word, 1u << (token & 31));
+      }
+  }
+  bad = __syncthreads_or(bad);   // all of them are the last block's
+  if (k == p.blocks - 1 && t == 0) {
+    *p.err = bad ? kErrBadList : 0;
+    *p.n_long = 0;
+  }
+  // zeros over the rows of the block's tokens that do not occur, a warp a row:
+  // on their way while the entries are sorted
+  if (!p.add)
+    for (uint32_t v = v0 + warp; v < min(v1, (uint32_t)p.V); v += kSortWarps) {
+      if (sh.seen[(v - v0) >> 5] >> (v & 31) & 1) continue;
+      float4* row = reinterpret_cast<float4*>(p.d_table + (int64_t)v * p.C);
+      for (int i = lane; i < p.C / 4; i += 32) __stcs(row + i, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+
+  // ---- their order by token
+  const int bins = 1 << p.bits, groups = (n + 31) / 32;
+  const int lo = groups * warp / kSortWarps * 32, hi = min((int)n, groups * (warp + 1) / kSortWarps * 32);
   for (int pass = 0; pass < p.passes; ++pass) {
-    const uint64_t* from = (p.passes - pass) & 1 ? p.other : p.sorted;
-    uint64_t* to = (p.passes - pass) & 1 ? p.sorted : p.other;
-    const int shift = 32 + pass * p.bits;
-    auto get = [&](int i) { return pass == 0 ? entry_of(p, i) : from[i]; };
-    auto bin = [&](uint64_t x) { return (uint32_t)(x >> shift) & (bins - 1); };
+    const uint64_t* from = (p.passes - pass) & 1 ? odd : even;
+    uint64_t* to = (p.passes - pass) & 1 ? even : odd;
+    auto bin = [&](uint64_t x) { return ((uint32_t)(x >> 32) - v0) >> (pass * p.bits) & (bins - 1); };
     for (int i = t; i < kSortWarps * bins; i += kSortThreads) sh.hist[i >> p.bits][i & (bins - 1)] = 0;
-    // the first entries of the warp stay in registers for both walks
-    uint64_t held[kHeld];
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      const int i = lo + k * 32 + lane;
-      held[k] = i < hi ? get(i) : 0;
-      if (pass == 0) bad = bad || (i < hi && p.tok[i] >= p.V);
-    }
     __syncthreads();
+    // one group of 32 entries: how many of the warp's are before a lane's in its
+    // bin, and the counter behind them; the bin's first lane returns its lanes in `group`
+    auto rank = [&](int i, uint64_t x, uint32_t& group) {
+      const bool on = i < hi;
+      const uint32_t b = on ? bin(x) : bins;
+      unsigned same = 0xffffffffu;   // the lanes with the same bin
+      for (int j = 0; j <= p.bits; ++j) {
+        const unsigned ones = __ballot_sync(0xffffffffu, b >> j & 1);
+        same &= b >> j & 1 ? ones : ~ones;
+      }
+      const int mine = __popc(same & below_me);
+      const uint32_t before = on ? sh.hist[warp][b] + mine : 0;
+      __syncwarp();
+      group = on && mine == 0 ? __popc(same) : 0;
+      if (group) sh.hist[warp][b] += group;
+      __syncwarp();
+      return before;
+    };
+    // the first entries stay in registers, and so do their ranks
+    uint64_t held[kHeld];
+    uint32_t ranks[kHeld], group[kHeld], other;
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k)
-      if (lo + k * 32 + lane < hi) atomicAdd(&sh.hist[warp][bin(held[k])], 1u);
-    for (int i = lo + kHeld * 32 + lane; i < hi; i += 32) {
-      if (pass == 0) bad = bad || p.tok[i] >= p.V;
-      atomicAdd(&sh.hist[warp][bin(get(i))], 1u);
-    }
-    bad = __syncthreads_or(bad);
-    if (t < bins) {
-      uint32_t sum = 0;
+    for (int h = 0; h < kHeld; ++h) held[h] = lo + h * 32 + lane < hi ? from[lo + h * 32 + lane] : 0;
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+      if (lo + h * 32 < hi) ranks[h] = rank(lo + h * 32 + lane, held[h], group[h]);
+    for (int i0 = lo + kHeld * 32; i0 < hi; i0 += 32) rank(i0 + lane, i0 + lane < hi ? from[i0 + lane] : 0, other);
+    __syncthreads();
+    uint32_t sum = 0;
+    if (t < bins)
 #pragma unroll 8
       for (int w = 0; w < kSortWarps; ++w) {
         const uint32_t c = sh.hist[w][t];
         sh.hist[w][t] = sum;
         sum += c;
       }
-      for (int r = 0; r < kSortBlocks; ++r) *cl.map_shared_rank(&sh.total[rank][t], r) = sum;
-    }
-    if (pass == 0 && t == 0) *cl.map_shared_rank(&sh.bad[rank], 0) = bad;
-    cl.sync();
-    if (pass == 0 && rank == 0 && t == 0) {
-      *p.n_long = 0;
-      uint32_t any = 0;
-      for (int r = 0; r < kSortBlocks; ++r) any |= sh.bad[r];
-      *p.err = any ? kErrBadList : 0;
-    }
-    // where a bin begins, and this block's entries in it
-    uint32_t sum = 0, before = 0;
-    if (t < bins)
-      for (int r = 0; r < kSortBlocks; ++r) {
-        const uint32_t c = sh.total[r][t];
-        sum += c;
-        before += r < rank ? c : 0;
-      }
-    uint32_t up = sum;
+    // where a bin begins
+    uint32_t up = sum, all;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, up, o);
       if (lane >= o) up += x;
     }
-    if (lane == 31) sh.warp_sum[warp] = up;
-    __syncthreads();
-    before += __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[lane] : 0);
+    const uint32_t before = before_warp(sh, __shfl_sync(0xffffffffu, up, 31), all);
     if (t < bins) sh.base[t] = before + up - sum;
     __syncthreads();
-    auto place = [&](int i, uint64_t x) {
-      const bool on = i < hi;
-      const uint32_t b = on ? bin(x) : bins;
-      // the lanes with the same bin (a match instruction takes the bins one by one, 240 cycles for a warp)
-      unsigned same = 0xffffffffu;
-      for (int k = 0; k <= p.bits; ++k) {
-        const unsigned ones = __ballot_sync(0xffffffffu, b >> k & 1);
-        same &= b >> k & 1 ? ones : ~ones;
-      }
-      const int mine = __popc(same & ((1u << lane) - 1));
-      if (on) to[sh.base[b] + sh.hist[warp][b] + mine] = x;
-      __syncwarp();
-      if (on && mine == 0) sh.hist[warp][b] += __popc(same);
-      __syncwarp();
-    };
+    const bool more = lo + kHeld * 32 < hi;   // then the counters go on behind the first entries
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k)
-      if (lo + k * 32 < hi) place(lo + k * 32 + lane, held[k]);
+    for (int h = 0; h < kHeld; ++h)
+      if (lo + h * 32 + lane < hi) to[sh.base[bin(held[h])] + sh.hist[warp][bin(held[h])] + ranks[h]] = held[h];
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+      if (more && group[h]) atomicAdd(&sh.hist[warp][bin(held[h])], group[h]);
+    __syncwarp();
     for (int i0 = lo + kHeld * 32; i0 < hi; i0 += 32) {
       const int i = i0 + lane;
-      place(i, i < hi ? get(i) : 0);
+      const uint64_t x = i < hi ? from[i] : 0;
+      const uint32_t before = rank(i, x, other);
+      if (i < hi) to[sh.base[bin(x)] + before] = x;
     }
-    cl.sync();   // the pass's entries are in place, and every block is done with the totals
+    __syncthreads();
   }
 }
 
@@ -449,7 +515,7 @@ EmbedParams embed_params(const stp_embed_desc* d, const int32_t* tok, void* ws) 
 }
 
 template <typename T>
-cudaError_t run_bwd(const EmbedParams& p, int n_sm, cudaStream_t s) {
+cudaError_t run_bwd(EmbedParams p, cudaStream_t s) {
   constexpr int E = Piece<T>::E;
   static PerDevice limit;
   constexpr int smem = sizeof(SortShared);
@@ -457,19 +523,15 @@ cudaError_t run_bwd(const EmbedParams& p, int n_sm, cudaStream_t s) {
     return cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (e != cudaSuccess) return e;
-  // Clusters that write zeros, all of them resident: of 152 SMs, 16 clusters of eight find a place at a time
-  const int fill = p.add ? 0 : n_sm / 10 > 1 ? n_sm / 10 : 1;
-  embed_sort_kernel<<<kSortBlocks * (1 + fill), kSortThreads, smem, s>>>(p);
-  if (p.N > 0) {
-    const int pieces = (p.N + kPiece - 1) / kPiece, along = (p.C / E + 31) / 32 * 32;
-    const dim3 block(along < kThreads ? along : kThreads, along < kThreads ? kThreads / along : 1);
-    embed_sum_kernel<T>
-        <<<dim3((pieces + block.y - 1) / block.y, (p.C / E + block.x - 1) / block.x), block, 0, s>>>(p);
-    const int most = p.N / (kShort + 1);   // tokens that occur more often
-    if (most > 0)
-      embed_join_kernel<T><<<dim3(most < 64 ? most : 64, (p.C / E + kJoinAlong - 1) / kJoinAlong),
-                             dim3(kJoinAlong, kJoinRows), 0, s>>>(p);
-  }
+  embed_sort_kernel<<<p.blocks, kSortThreads, smem, s>>>(p);
+  const int pieces = (p.N + kPiece - 1) / kPiece, along = (p.C / E + 31) / 32 * 32;
+  const dim3 block(along < kThreads ? along : kThreads, along < kThreads ? kThreads / along : 1);
+  if (pieces > 0)
+    embed_sum_kernel<T><<<dim3((pieces + block.y - 1) / block.y, (p.C / E + block.x - 1) / block.x), block, 0, s>>>(p);
+  const int often = p.N / (kShort + 1);   // tokens that occur more than kShort times, at most
+  if (often > 0)
+    embed_join_kernel<T><<<dim3(often < 128 ? often : 128, (p.C / E + kJoinAlong - 1) / kJoinAlong),
+                           dim3(kJoinAlong, kJoinRows), 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -543,16 +605,18 @@ extern "C" stp_status stp_embed_bwd(const stp_embed_desc* desc, const void* d_ou
   p.part = reinterpret_cast<float*>(ws + w.part);
   p.n_long = reinterpret_cast<uint32_t*>(ws + 16);   // in the error word's 256 bytes
   p.long_at = reinterpret_cast<uint32_t*>(ws + w.long_at);
-  int width = 1;   // bits of a token, V among them
-  while ((p.V >> width) != 0) ++width;
-  p.passes = (width + 8) / 9;
-  p.bits = (width + p.passes - 1) / p.passes;
   int dev = 0, n_sm = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
+  p.blocks = n_sm > 128 ? n_sm : 128;
+  const int most = ((p.V >> 5) / p.blocks + 1) * 32;   // tokens of a block
+  int width = 1;
+  while (((most - 1) >> width) != 0) ++width;
+  p.passes = (width + 8) / 9;
+  p.bits = (width + p.passes - 1) / p.passes;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (e == cudaSuccess)
-    e = desc->dtype == STP_BF16 ? run_bwd<__nv_bfloat16>(p, n_sm, s) : run_bwd<float>(p, n_sm, s);
+    e = desc->dtype == STP_BF16 ? run_bwd<__nv_bfloat16>(p, s) : run_bwd<float>(p, s);
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_embed_bwd: %s", cudaGetErrorString(e));
   return STP_OK;
 }
