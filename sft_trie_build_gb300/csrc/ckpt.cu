@@ -4,8 +4,10 @@
 // reverse.  A warp takes 16 tokens x 64 channels and a lane two channels of all
 // 16 tokens: rows of x are read 128 bytes (bf16) at a time, the lane's codes
 // are two whole 16-byte pieces of the checkpoint, and nothing passes through
-// shared memory.  The largest magnitude of 32 channels is found by exchange among 16
-// lanes, for two tokens in one register.
+// shared memory.  The largest magnitudes of 16 lanes' 32 channels are found by
+// halving: a lane gives away the tokens of which it is not to know the maximum, two tokens
+// in a register, so that a lane works out the scales of two tokens instead of
+// all sixteen (16384 x 4096 bf16: 40 us against 50 with every lane working out all).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -41,10 +43,19 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   return d;
 }
 
-// Exponent field of the scale of a float's magnitude, given by its bits: monotone in it.
-__device__ __forceinline__ uint32_t scale_of(uint32_t bits) {
-  if (bits >= 0x7f800000u) return kCkNaN;
-  return (uint32_t)max((int)((bits + 0x1fffffu) >> 23) - 8, kCkLeast);   // carries above 1.75
+// A float's magnitude as 16 bits, monotone in it and exact at the borders
+// between scales: its upper half, and a last bit for what lies below.
+__device__ __forceinline__ uint32_t key_of(uint32_t bits) {
+  bits &= 0x7fffffffu;
+  return bits >> 16 | ((bits & 0xffffu) != 0);
+}
+
+// The scale of a largest magnitude (its key) as bf16, and one over it: above 1.75 the exponent carries.
+__device__ __forceinline__ void scale_of(uint32_t key, uint32_t& scale, uint32_t& inverse) {
+  const uint32_t field = max((int)((key + 0x1fu) >> 7) - 8, (int)kCkLeast);
+  const bool finite = key < 0x7f80u;
+  scale = finite ? field << 7 : kCkNaN;
+  inverse = finite ? (254 - field) << 7 : 0;
 }
 
 // Two channels of one token as they lie in memory.
@@ -100,39 +111,46 @@ __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const CkptParams p)
       }
     }
   }
-  uint32_t code[2][4], scale[kTokens / 2];
+  // the larger magnitude of the lane's two channels, two tokens in a register
+  uint32_t m[kTokens / 2];
 #pragma unroll
   for (int i = 0; i < kTokens; i += 2) {
-    // the larger magnitude of each of two tokens, low and high half
-    uint32_t m;
     if constexpr (sizeof(T) == 2) {
       const uint32_t a = v[i].w & 0x7fff7fffu, b = v[i + 1].w & 0x7fff7fffu;
-      m = max_u16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+      m[i / 2] = max_u16x2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
     } else {
-      const uint32_t a = max(__float_as_uint(v[i].lo()) & 0x7fffffffu, __float_as_uint(v[i].hi()) & 0x7fffffffu);
-      const uint32_t b = max(__float_as_uint(v[i + 1].lo()) & 0x7fffffffu, __float_as_uint(v[i + 1].hi()) & 0x7fffffffu);
-      m = scale_of(a) | scale_of(b) << 16;
+      m[i / 2] = max_u16x2(key_of(__float_as_uint(v[i].lo())) | key_of(__float_as_uint(v[i + 1].lo())) << 16,
+                           key_of(__float_as_uint(v[i].hi())) | key_of(__float_as_uint(v[i + 1].hi())) << 16);
     }
+  }
+  // among 16 lanes: lane 2 j and 2 j + 1 come to hold tokens 2 j and 2 j + 1
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const uint32_t s0 = sizeof(T) == 2 ? scale_of(m << 16) : m & 0xffff;
-    const uint32_t s1 = sizeof(T) == 2 ? scale_of(m & 0xffff0000u) : m >> 16;
-    const float f0 = s0 == kCkNaN ? 0.f : __uint_as_float((254 - s0) << 23);
-    const float f1 = s1 == kCkNaN ? 0.f : __uint_as_float((254 - s1) << 23);
-    uint32_t lo = to_e4m3x2(v[i].lo() * f0, v[i + 1].lo() * f1);
-    uint32_t hi = to_e4m3x2(v[i].hi() * f0, v[i + 1].hi() * f1);
-    // infinities and NaN times 0 are no codes
-    const uint32_t keep = (s0 == kCkNaN ? 0u : 0xffu) | (s1 == kCkNaN ? 0u : 0xff00u);
-    lo &= keep;
-    hi &= keep;
-    scale[i / 2] = s0 << 7 | s1 << 23;
-    if (i & 2) {
-      code[0][i / 4] = pack_codes(code[0][i / 4] | lo << 16);
-      code[1][i / 4] = pack_codes(code[1][i / 4] | hi << 16);
-    } else {
-      code[0][i / 4] = lo;
-      code[1][i / 4] = hi;
+  for (int o = 8, left = 4; o > 1; o >>= 1, left >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < left; ++i) {
+      const uint32_t keep = up ? m[i + left] : m[i], give = up ? m[i] : m[i + left];
+      m[i] = max_u16x2(keep, __shfl_xor_sync(0xffffffffu, give, o));
     }
+  }
+  m[0] = max_u16x2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+  uint32_t s0, s1, r0, r1;
+  scale_of(m[0] & 0xffffu, s0, r0);
+  scale_of(m[0] >> 16, s1, r1);
+  const uint32_t scales = s0 | s1 << 16, inverse = r0 | r1 << 16;
+  uint32_t code[2][kTokens / 4];
+#pragma unroll
+  for (int i = 0; i < kTokens; i += 4) {
+    uint32_t lo[2], hi[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t f = __shfl_sync(0xffffffffu, inverse, (lane & 16) | (i + 2 * k));
+      const float f0 = __uint_as_float(f << 16), f1 = __uint_as_float(f & 0xffff0000u);
+      lo[k] = to_e4m3x2(v[i + 2 * k].lo() * f0, v[i + 2 * k + 1].lo() * f1);
+      hi[k] = to_e4m3x2(v[i + 2 * k].hi() * f0, v[i + 2 * k + 1].hi() * f1);
+    }
+    code[0][i / 4] = pack_codes(lo[0], lo[1]);
+    code[1][i / 4] = pack_codes(hi[0], hi[1]);
   }
   const int cb = c / kCkChannels, in = c & (kCkChannels - 1), q = group & (kGroups - 1);
   if (cb >= p.CB) return;
@@ -140,11 +158,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const CkptParams p)
   uint4* to = reinterpret_cast<uint4*>(block + q * 512 + in * 16);
   to[0] = make_uint4(code[0][0], code[0][1], code[0][2], code[0][3]);
   to[1] = make_uint4(code[1][0], code[1][1], code[1][2], code[1][3]);
-  if (in == 0) {
-    uint4* scales = reinterpret_cast<uint4*>(block + kCkCodes + q * 32);
-    scales[0] = make_uint4(scale[0], scale[1], scale[2], scale[3]);
-    scales[1] = make_uint4(scale[4], scale[5], scale[6], scale[7]);
-  }
+  if (!(lane & 1)) reinterpret_cast<uint32_t*>(block + kCkCodes + q * 32)[(lane & 15) / 2] = scales;
 }
 
 template <typename T, bool WIDE>

@@ -8,7 +8,7 @@
 // thread that owns a channel reads 16 tokens at once.  Tokens and channels past
 // the end are zeros.  The scale is the smallest power of two, from 2^-117 on, at which the 32
 // channels' largest magnitude is at most 448 (e4m3's largest); a block that
-// holds an infinity or a NaN has scale infinity and codes 0, which return as NaN.
+// holds an infinity or a NaN has scale NaN and any codes, and returns as NaN.
 //
 // A code has four significant bits and a power of two leaves them as they are,
 // so the values are exact in bf16 (the smallest is 2^-9 2^-117, a normal number).
@@ -32,8 +32,8 @@ namespace stp {
 constexpr int kCkTokens = 128, kCkChannels = 32;
 constexpr int kCkCodes = kCkTokens * kCkChannels;
 constexpr int kCkBlock = kCkCodes + kCkTokens * 2;   // bytes, a multiple of 16
-constexpr int kCkLeast = 10;                         // exponent field of 2^-117
-constexpr int kCkNaN = 255;                          // and of infinity
+constexpr uint32_t kCkLeast = 10;                    // exponent field of 2^-117
+constexpr uint32_t kCkNaN = 0x7fc0;                  // a bf16 NaN
 
 inline int64_t ck_token_blocks(int64_t n) { return (n + kCkTokens - 1) / kCkTokens; }
 inline int64_t ck_channel_blocks(int64_t c) { return (c + kCkChannels - 1) / kCkChannels; }
@@ -44,10 +44,11 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Four codes, in a word's bytes, to their places and back; `early` are the
-// first two tokens' values times 2^-120, `late` the other two's.
-__device__ __forceinline__ uint32_t pack_codes(uint32_t c) {
-  const uint32_t x = __byte_perm(c, 0, 0x1404), y = __byte_perm(c, 0, 0x3424);   // in the halves' upper bytes
+// Two and two codes of successive tokens, each pair in a number's lower bytes,
+// to their places in a word, and back; `early` are the first two tokens' values times 2^-120,
+// `late` the other two's.
+__device__ __forceinline__ uint32_t pack_codes(uint32_t early, uint32_t late) {
+  const uint32_t x = __byte_perm(early, 0, 0x1404), y = __byte_perm(late, 0, 0x1404);   // in the halves' upper bytes
   return (x & 0x70007000u) | ((x >> 8) & 0x000f000fu) | ((x >> 4) & 0x08000800u) | (y & 0x80008000u) |
          ((y >> 4) & 0x07f007f0u);
 }

@@ -6,8 +6,8 @@
 //
 // The gradient adds up rows of d_out that lie anywhere, some tokens once, some
 // thousands of times, in an order that does not depend on timing:
-//   embed_sort_kernel   every block takes a range of tokens out of all positions, in
-//                 order, and sorts (token, position) by token, stable, in one or two
+//   embed_sort_kernel   every block takes a range of tokens out of all positions, in a
+//                 fixed order, and sorts (token, position) by token, stable, in one or two
 //                 passes over 9 bits or less; no block waits for another one.  It also
 //                 writes zeros over the rows of its tokens that do not occur
 //   embed_sum_kernel    pieces of 32 sorted entries each: a thread adds its 16 bytes of
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const Embed
   for (int i = t; i < w1 - w0; i += kSortThreads) sh.seen[i] = 0;
   if (t == 0) sh.below = 0;
 
-  // ---- the block's entries, in order of position: kScan positions of a lane
+  // ---- the block's entries, in a fixed order: kScan positions of a lane
   // at a time, a warp's next to one another.  As unsigned numbers, tokens that
   // are none lie behind all others, in the last block's range.
   constexpr int kRound = kSortThreads * kScan;
@@ -177,8 +177,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const Embed
     const uint64_t keep = there == 64 ? ~0ull : (1ull << there) - 1;
     in &= keep;
     below = __popcll(less & keep);
-    const uint32_t mine = __reduce_add_sync(0xffffffffu, (uint32_t)__popcll(in));
-    uint32_t all, place = before_warp(sh, mine, all);
+    uint32_t all, place = before_warp(sh, __reduce_add_sync(0xffffffffu, (uint32_t)__popcll(in)), all);
     if (p.N <= kRound) before_warp(sh, __reduce_add_sync(0xffffffffu, below), first);
     if (r0 == 0) {
       even += first;
@@ -187,31 +186,30 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const Embed
     place += n;
     n += all;
     uint64_t* to = p.passes & 1 ? odd : even;
-    // words of the warp's bits: positions that any lane has
-    const uint32_t any[2] = {__reduce_or_sync(0xffffffffu, (uint32_t)in), __reduce_or_sync(0xffffffffu, (uint32_t)(in >> 32))};
+    // lane by lane, so that a lane walks its own positions only
+    const uint32_t each_in = (uint32_t)__popcll(in);
+    uint32_t up = each_in;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      for (uint32_t left = any[h]; left; left &= left - 1) {
-        const int j = h * 32 + __ffs(left) - 1;
-        const bool on = in >> j & 1;
-        const unsigned who = __ballot_sync(0xffffffffu, on);
-        if (on) to[place + __popc(who & below_me)] = (uint32_t)(at + j * 32);
-        place += __popc(who);
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += x;
+    }
+    to += place + up - each_in;
+    for (; in; in &= in - 1) *to++ = (uint32_t)(at + (__ffsll(in) - 1) * 32);
   }
   __syncthreads();   // the positions are in place
   // their tokens, which a walk position by position would wait for one by one
   bool bad = false;
-  for (uint32_t i0 = t; i0 < n; i0 += 4 * kSortThreads) {
+  for (uint32_t i0 = t; i0 < n; i0 += 8 * kSortThreads) {
     uint64_t* e = (p.passes & 1 ? odd : even) + i0;
-    uint32_t at[4];
-    int x[4];
+    uint32_t at[8];
+    int x[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) at[j] = i0 + j * kSortThreads < n ? (uint32_t)e[j * kSortThreads] : ~0u;
+    for (int j = 0; j < 8; ++j) at[j] = i0 + j * kSortThreads < n ? (uint32_t)e[j * kSortThreads] : ~0u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = at[j] != ~0u ? p.tok[at[j]] : 0;
+    for (int j = 0; j < 8; ++j) x[j] = at[j] != ~0u ? p.tok[at[j]] : 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 8; ++j)
       if (at[j] != ~0u) {
         bad |= x[j] >= p.V;
         const uint32_t token = x[j] < 0 || x[j] >= p.V ? (uint32_t)p.V : (uint32_t)x[j];
