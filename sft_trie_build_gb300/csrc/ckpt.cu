@@ -95,19 +95,24 @@ __global__ void __launch_bounds__(kThreads) ckpt_save_kernel(const CkptParams p)
   if ((c & ~63) >= p.CB * kCkChannels) return;   // the warp lies past the last block
   const T* x = static_cast<const T*>(p.x) + c;
   Two<T> v[kTokens];
+  if (WIDE && n0 + kTokens <= p.N && (c | 63) < p.C) {   // all of it is there
 #pragma unroll
-  for (int i = 0; i < kTokens; ++i) {
-    const bool on = n0 + i < p.N;
-    const T* at = x + (int64_t)(n0 + i) * p.stride;
-    v[i] = {};
-    if (on && WIDE && c + 1 < p.C) v[i].get(at);
-    else if (on && c < p.C) {
-      v[i].get1(at);
-      if (!WIDE && c + 1 < p.C) {
-        Two<T> b = {};
-        b.get1(at + 1);
-        if constexpr (sizeof(T) == 2) v[i].w |= b.w << 16;
-        else v[i].w.y = b.w.x;
+    for (int i = 0; i < kTokens; ++i) v[i].get(x + (n0 + i) * p.stride);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      const bool on = n0 + i < p.N;
+      const T* at = x + (n0 + i) * p.stride;
+      v[i] = {};
+      if (on && WIDE && c + 1 < p.C) v[i].get(at);
+      else if (on && c < p.C) {
+        v[i].get1(at);
+        if (!WIDE && c + 1 < p.C) {
+          Two<T> b = {};
+          b.get1(at + 1);
+          if constexpr (sizeof(T) == 2) v[i].w |= b.w << 16;
+          else v[i].w.y = b.w.x;
+        }
       }
     }
   }
@@ -175,6 +180,7 @@ __global__ void __launch_bounds__(kThreads) ckpt_load_kernel(const CkptParams p)
   const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
   const uint32_t s[8] = {s4.x, s4.y, s4.z, s4.w, t4.x, t4.y, t4.z, t4.w};
   T* y = static_cast<T*>(p.y) + c;
+  const bool full = n0 + kTokens <= p.N;
 #pragma unroll
   for (int i = 0; i < kTokens; i += 2) {
     // two tokens of either channel, then two channels of either token
@@ -183,8 +189,8 @@ __global__ void __launch_bounds__(kThreads) ckpt_load_kernel(const CkptParams p)
     const uint32_t v[2] = {__byte_perm(va, vb, 0x5410), __byte_perm(va, vb, 0x7632)};
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      if (n0 + i + k >= p.N) return;
-      T* at = y + (int64_t)(n0 + i + k) * p.stride;
+      if (!full && n0 + i + k >= p.N) return;
+      T* at = y + (n0 + i + k) * p.stride;
       if (WIDE && c + 1 < p.C) Two<T>::put(at, v[k]);
       else {
         Two<T>::put1(at, v[k]);
