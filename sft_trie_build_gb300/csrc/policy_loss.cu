@@ -175,14 +175,37 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
     // dz = p (h ln p + c), and g more for the token itself
     const float h = w * p.gamma, c = p.gamma != 0.f ? fmaf(h, ent, -g) : -g;
     const float shift = -ref * kLog2eT, scale = p.scale, sl2 = p.sl2, h2 = h * kLn2T;
+    // ln p in units of ln 2; with both passes l2 = (x - m) sl2 + shift
+    const float up = LSE ? 0.f : 0.f - ref, sub = LSE ? -m : 0.f;
+    const auto log2p = [=](float x) { return LSE ? fmaf(x + sub, sl2, shift) : fmaf(x, scale, up) * kLog2eT; };
     const auto grad = [=](float x) {
-      const float l2 = LSE ? fmaf(x - m, sl2, shift) : fmaf(x, scale, -ref) * kLog2eT;
+      const float l2 = log2p(x);
       return ex2(l2) * fmaf(h2, fmaxf(l2, -1e30f), c);
     };
-    map_row(row, out, part, ring, [=](float* z, int, auto N) {
+    // two by two, as the pass issues more than it may; without an entropy term p times one number
+    const auto pairs = [=](float* z, auto N, auto term) {
+      if constexpr (decltype(N)::value % 2 == 0) {
 #pragma unroll
-      for (int e = 0; e < N(); ++e) z[e] = grad(z[e]);
-    });
+        for (int e = 0; e < N(); e += 2) {
+          float2 l = make_float2(z[e], z[e + 1]);
+          l = LSE ? __ffma2_rn(__fadd2_rn(l, make_float2(sub, sub)), make_float2(sl2, sl2), make_float2(shift, shift))
+                  : __fmul2_rn(__ffma2_rn(l, make_float2(scale, scale), make_float2(up, up)), make_float2(kLog2eT, kLog2eT));
+          const float2 p2 = __fmul2_rn(make_float2(ex2(l.x), ex2(l.y)), term(l));
+          z[e] = p2.x;
+          z[e + 1] = p2.y;
+        }
+      } else {
+        z[0] = grad(z[0]);
+      }
+    };
+    if (h2 == 0.f)
+      map_row(row, out, part, ring, [=](float* z, int, auto N) { pairs(z, N, [=](float2) { return make_float2(c, c); }); });
+    else
+      map_row(row, out, part, ring, [=](float* z, int, auto N) {
+        pairs(z, N, [=](float2 l) {
+          return __ffma2_rn(make_float2(h2, h2), make_float2(fmaxf(l.x, -1e30f), fmaxf(l.y, -1e30f)), make_float2(c, c));
+        });
+      });
     __syncthreads();   // the block's stores before that of the token
     if (mine && t == 0) put(out + target, grad(zt) + g);
   }
