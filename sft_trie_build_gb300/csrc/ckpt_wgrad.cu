@@ -61,6 +61,8 @@ constexpr int kGroups = 2;          // warp groups among them
 // 16384-token projection against 549.
 constexpr int kStages = 4;
 constexpr int kAhead = 3;           // stages converted ahead when sums are taken: less than kStages
+// A group meets each of its stages in every round of the ring: a wait by parity would take the phase two rounds before for the one it wants.
+static_assert(kStages % kGroups == 0 && kAhead < kStages, "ring of stages");
 constexpr int kChunk = 16;          // stages between two takings
 constexpr int kTileC = 256, kHalfC = 128, kTileM = 256;
 constexpr int kBoxBytes = kCkTokens * 64 * 2;       // 64 columns of a stage's tokens
@@ -317,8 +319,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tma_load_pair(smem + st * kYBytes + b * kBoxBytes, &ty, bar, m0 + b * 64, w.kb * kCkTokens);
         last[st] = n & 1;
       }
-      for (int st = 0; st < kStages; ++st)
+      // nothing is on its way to this block's memory or barriers when it ends
+      for (int st = 0; st < kStages; ++st) {
         if (block == 0 && last[st] >= 0) mbar_wait_drain(&bars[W_BF + st], last[st]);
+        if (last[st] >= 0) wait(&bars[W_E + st], last[st], abort_flag, p.err);
+      }
     }
     __syncwarp();
     } else if (warp == 10) {
@@ -368,6 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       commit_pair(&bars[W_DRAIN]);
+      if (chunk > 0) wait(&bars[W_DE], (chunk - 1) & 1, abort_flag, p.err);   // the other block's last arrivals, too
     }
     // nothing of the pair is in flight behind this; the second block's wait is all it does, so it looks rarely
     if (lane == 0)
@@ -402,6 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
+        __syncwarp();
         fence_after_sync();
         if (c.ct * 8 + block * 4 + w4 < p.CB) {   // channels past the end: sums that nothing reads
 #pragma unroll
