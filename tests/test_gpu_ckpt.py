@@ -202,3 +202,26 @@ def test_same_each_time_captured_and_on_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(dw, want)
     assert stp.stp_device_status(ws) == stp.STP_OK
+
+
+def test_calls_one_behind_another():
+    # sizes with and without parts, one after another without waiting, in one workspace
+    sizes = [(512, 256, 1024), (20001, 130, 300), (65, 127, 255), (4096, 1300, 5000)]
+    data = [_whole(*z) for z in sizes]
+    descs = [stp.ckpt_desc(n, c) for n, c, _ in sizes]
+    ws = _space(max(stp.stp_ckpt_wgrad_workspace_size(d, z[2]) for d, z in zip(descs, sizes)))
+    kept, ys, dws = [], [], []
+    for (x, dy), d, (n, c, m) in zip(data, descs, sizes):
+        ck = _space(stp.stp_ckpt_size(d))
+        stp.stp_ckpt_save(d, x.cuda(), ck)
+        y = torch.zeros(n, (m + 7) // 8 * 8, dtype=torch.bfloat16, device="cuda")
+        y[:, :m] = dy.cuda()
+        kept.append(ck), ys.append(y), dws.append(torch.zeros(c, m, device="cuda"))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for d, (n, c, m), ck, y, dw in zip(descs, sizes, kept, ys, dws):
+            stp.stp_ckpt_wgrad(d, m, ck, y, y.stride(0), True, dw, ws)
+    torch.cuda.synchronize()
+    assert stp.stp_device_status(ws) == stp.STP_OK
+    for (x, dy), dw in zip(data, dws):
+        assert torch.equal(dw.double(), 5 * (x.cuda().double().T @ dy.cuda().double()))
