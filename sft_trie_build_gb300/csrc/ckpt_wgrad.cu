@@ -37,6 +37,7 @@
 #include <mutex>
 
 #include "ckpt.h"
+#include "follow.cuh"
 #include "internal.h"
 #include "layout.h"
 #include "per_device.h"
@@ -496,6 +497,7 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const WgradParams p) {
   const bool second = share(p, g0) < a;
   const float4* from = reinterpret_cast<const float4*>(p.part) + (size_t)block * (kPartBytes / 16) + c4 * kHalfC + r;
   constexpr size_t kSlot = 2 * kPartBytes / 16;   // of a pair's part
+  wait_for_previous();
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int g = g0; g < g1; g += 8) {
     float4 v[8];
@@ -638,8 +640,8 @@ extern "C" stp_status stp_ckpt_wgrad(const stp_ckpt_desc* desc, int32_t cols, co
     CUtensorMap ty;
     if (!make_map(&ty, d_y, p.N, p.M, y_stride)) return fail(STP_ECUDA, "stp_ckpt_wgrad: tensor map encoding failed");
     wgrad_kernel<<<2 * pairs, kThreads, kSmem, s>>>(ty, p);
-    if (p.parts > p.rest) wgrad_join_kernel<<<dim3(p.W / 4, p.rest), 256, 0, s>>>(p);
     e = cudaGetLastError();
+    if (e == cudaSuccess && p.parts > p.rest) e = launch_after(wgrad_join_kernel, dim3(p.W / 4, p.rest), dim3(256), s, p);
   }
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_ckpt_wgrad: %s", cudaGetErrorString(e));
   return STP_OK;

@@ -19,6 +19,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "follow.cuh"
 #include "internal.h"
 #include "layout.h"
 #include "logit_rows.cuh"
@@ -341,6 +342,7 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(const EmbedParams p
   const int lane = threadIdx.x & 31, c = (blockIdx.y * blockDim.x + threadIdx.x) * E;
   const bool on = c < p.C;
   const uint32_t none = (uint32_t)p.V;
+  wait_for_previous();
   // entries from kShort before the piece to kShort behind it; what is outside is no token
   uint64_t near[kPiece / 32 + 2 * kShort / 32];
 #pragma unroll
@@ -419,6 +421,7 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(const EmbedParams 
   __shared__ float sums[kJoinRows][kJoinAlong][E];
   const int pieces = (p.N + kPiece - 1) / kPiece, lane = threadIdx.x, y = threadIdx.y;
   const int c = (blockIdx.y * kJoinAlong + lane) * E;
+  wait_for_previous();
   const uint32_t n = *p.n_long;
   for (uint32_t at = blockIdx.x; at < n; at += gridDim.x) {
     const int piece = p.long_at[at];
@@ -524,13 +527,14 @@ cudaError_t run_bwd(EmbedParams p, cudaStream_t s) {
   embed_sort_kernel<<<p.blocks, kSortThreads, smem, s>>>(p);
   const int pieces = (p.N + kPiece - 1) / kPiece, along = (p.C / E + 31) / 32 * 32;
   const dim3 block(along < kThreads ? along : kThreads, along < kThreads ? kThreads / along : 1);
-  if (pieces > 0)
-    embed_sum_kernel<T><<<dim3((pieces + block.y - 1) / block.y, (p.C / E + block.x - 1) / block.x), block, 0, s>>>(p);
+  e = cudaGetLastError();
+  if (e == cudaSuccess && pieces > 0)
+    e = launch_after(embed_sum_kernel<T>, dim3((pieces + block.y - 1) / block.y, (p.C / E + block.x - 1) / block.x), block, s, p);
   const int often = p.N / (kShort + 1);   // tokens that occur more than kShort times, at most
-  if (often > 0)
-    embed_join_kernel<T><<<dim3(often < 128 ? often : 128, (p.C / E + kJoinAlong - 1) / kJoinAlong),
-                           dim3(kJoinAlong, kJoinRows), 0, s>>>(p);
-  return cudaGetLastError();
+  if (e == cudaSuccess && often > 0)
+    e = launch_after(embed_join_kernel<T>, dim3(often < 128 ? often : 128, (p.C / E + kJoinAlong - 1) / kJoinAlong),
+                     dim3(kJoinAlong, kJoinRows), s, p);
+  return e;
 }
 
 }  // namespace
