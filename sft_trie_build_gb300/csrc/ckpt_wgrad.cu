@@ -26,7 +26,9 @@
 //
 // Work: whole tiles first, one per pair of blocks and wave, all pairs at the
 // same tokens, so that what they read together stays in L2; the tiles of the
-// last, partial wave are cut along the tokens into equal parts for all pairs.
+// last, partial wave are cut along the tokens into as many equal parts as there are pairs for
+// each, so that the pairs of one part read the same tokens too (with shares of equal size
+// across tiles, 65531 tokens of 1000 channels x 523 columns were read three times: 72 us against JOINT_US).
 // Parts of a tile go to the workspace and wgrad_join_kernel adds them in order.
 #include <cooperative_groups.h>
 #include <cuda.h>
@@ -82,39 +84,17 @@ constexpr int kLeastM = 32;         // columns of a tile made narrower, at least
 struct WgradParams {
   int N, C, M, CB, KB, W;       // W: columns of a tile, a multiple of 16
   int CT, MT;                   // tiles along channels and columns
-  int whole, rest, parts;       // waves of whole tiles; tiles of the last wave, and pairs that share them
+  int whole, rest, parts;       // waves of whole tiles; tiles of the last wave, and parts that each is cut into
   bool add, vec;                // vec: rows of dW start at whole 16 bytes
   const uint8_t* ck;
   float* dw;
-  float* part;                  // [parts][2][2][64][128][4]: pair, its first or second part, block, column / 4, channel, column % 4
+  float* part;                  // [parts][rest][2][64][128][4]: part, tile, block, column / 4, channel, column % 4
   uint32_t* err;
 };
-
-// The share of pair g in the last wave: token blocks [at, end) of `rest` tiles of KB each.
-// The products stay below 2^31: fewer tiles than pairs (76), at most 2^17 stages each, times a pair's number.
-__device__ __forceinline__ int share(const WgradParams& p, int g) {
-  return (int)((uint32_t)(p.rest * p.KB) * (uint32_t)g / (uint32_t)p.parts);
-}
 
 struct Segment {
   int tile, kb0, kb1, slot;   // slot: of the workspace, -1 when the tile is whole
 };
-
-// The one or two segments of pair g in the last wave; returns how many.
-__device__ __forceinline__ int last_segments(const WgradParams& p, int g, int pairs, Segment* to) {
-  if (g >= p.parts) return 0;
-  const int at = share(p, g), end = share(p, g + 1), first = at / p.KB;
-  int n = 0;
-  for (int tile = first; n < 2 && tile * p.KB < end; ++tile, ++n) {
-    const int t0 = tile * p.KB;
-    Segment& s = to[n];
-    s.tile = p.whole * pairs + tile;
-    s.kb0 = max(t0, at) - t0;
-    s.kb1 = min(t0 + p.KB, end) - t0;
-    s.slot = s.kb0 == 0 && s.kb1 == p.KB ? -1 : 2 * g + n;
-  }
-  return n;
-}
 
 // Barriers: the codes of a stage have landed and are read (each block's own),
 // dY of both blocks has landed and A of both is in place (first block's), the
@@ -224,23 +204,26 @@ __device__ __forceinline__ void convert(uint32_t block, int lane, int part, uint
   }
 }
 
-// The stages of a pair in order, over all its segments.
+// The stages of a pair in order: whole tiles, then its part of one.
 struct Walk {
   Segment s;
-  int i = 0, kb = 0;
-  const Segment* last;   // of the last wave, in shared memory
-  int n, whole, KB, CT, pairs, ct, mt;   // the tile's place along channels and columns
-  __device__ __forceinline__ Walk(const WgradParams& p, int g, int pairs_, const Segment* last_, int n_last)
-      : last(last_), n(p.whole + n_last), whole(p.whole), KB(p.KB), CT(p.CT), pairs(pairs_) {
+  int i = 0, kb = 0, n, whole, KB, CT, pairs, ct, mt;   // the tile's place along channels and columns
+  Segment last;
+  __device__ __forceinline__ Walk(const WgradParams& p, int g, int pairs_)
+      : whole(p.whole), KB(p.KB), CT(p.CT), pairs(pairs_) {
+    n = whole;
     s.tile = g - pairs;
+    if (g < p.rest * p.parts) {
+      const int part = g / p.rest;
+      last = {whole * pairs + g - part * p.rest, (int)((int64_t)KB * part / p.parts),
+              (int)((int64_t)KB * (part + 1) / p.parts), p.parts > 1 ? g : -1};
+      ++n;
+    }
     enter();
   }
   __device__ __forceinline__ void enter() {
-    if (i < whole) {
-      s = {s.tile + pairs, 0, KB, -1};
-    } else if (i < n) {
-      s = last[i - whole];
-    }
+    if (i < whole) s = {s.tile + pairs, 0, KB, -1};
+    else if (i < n) s = last;
     kb = s.kb0;
     mt = s.tile / CT;
     ct = s.tile - mt * CT;
@@ -279,8 +262,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + W_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  Segment* last_wave = reinterpret_cast<Segment*>(tmem_slot + 4);
-  int* n_last_wave = reinterpret_cast<int*>(last_wave + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, block = blockIdx.x & 1, g = blockIdx.x >> 1,
             pairs = gridDim.x >> 1;
 
@@ -289,7 +270,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&bars[b], b >= W_AF && b < W_AF + kStages ? 8 : b >= W_CE && b < W_CE + kStages ? 4 : b == W_DE ? 16 : 1);
     *abort_flag = 0;
     if (blockIdx.x == 0) *p.err = 0;   // a lost wait sets it seconds later
-    *n_last_wave = last_segments(p, g, pairs, last_wave);
     fence_mbar_init();
   }
   if (warp == 9) {
@@ -301,7 +281,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cg::this_cluster().sync();
   fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const int n_last = *n_last_wave;
 
   if (warp >= 8) {
     regs_dec<kRegsRest>();
@@ -312,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int boxes = (p.W / 2 + 63) / 64;
       int it = 0, last[kStages];   // phase of a stage's last load
       for (int st = 0; st < kStages; ++st) last[st] = -1;
-      for (Walk w(p, g, pairs, last_wave, n_last); w.on(); w.next(), ++it) {
+      for (Walk w(p, g, pairs); w.on(); w.next(), ++it) {
         const int st = it % kStages, n = it / kStages;
         if (it >= kStages && !wait(&bars[W_E + st], (n - 1) & 1, abort_flag, p.err)) break;
         const int m0 = w.mt * p.W + block * (p.W / 2);
@@ -334,7 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------------- codes
       int it = 0, last[kStages];
       for (int st = 0; st < kStages; ++st) last[st] = -1;
-      for (Walk w(p, g, pairs, last_wave, n_last); w.on(); w.next(), ++it) {
+      for (Walk w(p, g, pairs); w.on(); w.next(), ++it) {
         const int st = it % kStages, n = it / kStages, cb = w.ct * 8 + block * 4;
         if (it >= kStages && !wait(&bars[W_CE + st], (n - 1) & 1, abort_flag, p.err)) break;
         if (cb < p.CB) {
@@ -355,7 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // --------------------------------------------------------- products
       const uint32_t idesc = idesc_bf16(kTileC, p.W, 0, 1);
       int it = 0, chunk = 0, in = 0;
-      for (Walk w(p, g, pairs, last_wave, n_last); w.on(); ++it) {
+      for (Walk w(p, g, pairs); w.on(); ++it) {
         if (in == 0 && chunk > 0 && !wait(&bars[W_DE], (chunk - 1) & 1, abort_flag, p.err)) break;
         const int st = it % kStages;
         const uint32_t phase = (it / kStages) & 1;
@@ -395,8 +374,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int e = 0; e < kTileM / 2; ++e) acc[e] = 0.f;
     int it = 0, end = 0, chunk = 0;   // stages converted, and at the end of the chunk
     bool ok = true;
-    Walk c(p, g, pairs, last_wave, n_last);
-    for (Walk d(p, g, pairs, last_wave, n_last); d.on() && ok; ++chunk) {
+    Walk c(p, g, pairs);
+    for (Walk d(p, g, pairs); d.on() && ok; ++chunk) {
       // the chunk: up to kChunk stages of one segment
       const int len = min(kChunk, d.s.kb1 - d.kb);
       end += len;
@@ -484,26 +463,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // Adds up the parts of a tile of the last wave; a block does 4 columns x 256 channels.
 __global__ void __launch_bounds__(256) wgrad_join_kernel(const WgradParams p) {
-  const int tile = blockIdx.y;   // of the last wave
-  const int a = tile * p.KB, b = a + p.KB;
-  int g0 = (int)((uint32_t)a * (uint32_t)p.parts / (uint32_t)(p.rest * p.KB));   // the first pair whose share reaches past a
-  while (g0 > 0 && share(p, g0) > a) --g0;
-  while (share(p, g0 + 1) <= a) ++g0;
-  int g1 = g0 + 1;   // one past the last pair with a share of the tile
-  while (g1 < p.parts && share(p, g1) < b) ++g1;
-  if (g1 == g0 + 1) return;   // one pair did it all
-  const int c4 = blockIdx.x, block = threadIdx.x >> 7, r = threadIdx.x & 127;
-  // only the first share may begin in another tile, whose part comes first
-  const bool second = share(p, g0) < a;
-  const float4* from = reinterpret_cast<const float4*>(p.part) + (size_t)block * (kPartBytes / 16) + c4 * kHalfC + r;
-  constexpr size_t kSlot = 2 * kPartBytes / 16;   // of a pair's part
+  const int tile = blockIdx.y, c4 = blockIdx.x, block = threadIdx.x >> 7, r = threadIdx.x & 127;
+  const size_t slot = 2 * kPartBytes / 16;
+  const float4* from = reinterpret_cast<const float4*>(p.part) + tile * slot + (size_t)block * (kPartBytes / 16) + c4 * kHalfC + r;
   wait_for_previous();
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int g = g0; g < g1; g += 8) {
+  for (int g = 0; g < p.parts; g += 8) {
     float4 v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      v[k] = g + k < g1 ? __ldcs(from + (size_t)(2 * (g + k) + (second && g + k == g0)) * kSlot) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[k] = g + k < p.parts ? __ldcs(from + (size_t)(g + k) * p.rest * slot) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum = make_float4(sum.x + v[k].x, sum.y + v[k].y, sum.z + v[k].z, sum.w + v[k].w);
   }
@@ -549,13 +518,12 @@ stp_status check_wgrad(const stp_ckpt_desc* d, int cols) {
   return STP_OK;
 }
 
-// Tiles and the pairs' shares of them on a GPU of n_sm SMs; returns the launch's
-// pairs.  The last wave's tiles are cut where that saves more stages (0.57 us each) than
+// Tiles and their parts on a GPU of n_sm SMs; returns the launch's pairs.  The
+// last wave's tiles are cut where that saves more stages (0.57 us each) than
 // joining costs, about 6 and one for every 1500 columns of all parts.  Measured in us, cut
-// and whole: 12 tiles of 32 stages 16.5 / 26, of 16 stages 14.4 / 16.1, of 8 13.5 / 11.3;
-// 64 tiles (of 76 pairs) of 12 stages 30 / 18, of 47 stages 50 / 42.  Where few tiles stay
-// whole they are made narrower instead, as many as there are pairs: 4 tiles of
-// 4 stages 14.3 us, 16 tiles 8.1.
+// and whole: 12 tiles of 32 stages 16.5 / 26, of 16 stages 14.4 / 16.1, of 8 13.5 / 11.3.
+// Where few tiles stay whole they are made narrower instead, as many as there
+// are pairs: 4 tiles of 4 stages 14.3 us, 16 tiles 8.1.
 int plan(WgradParams& p, const stp_ckpt_desc* d, int cols, int n_sm) {
   p.N = d->n_tokens;
   p.C = d->dim;
@@ -570,18 +538,17 @@ int plan(WgradParams& p, const stp_ckpt_desc* d, int cols, int n_sm) {
     p.MT = (p.M + p.W - 1) / p.W;
     p.whole = (int)((int64_t)p.CT * p.MT / pairs);
     p.rest = (int)((int64_t)p.CT * p.MT % pairs);
-    p.parts = p.rest;
+    p.parts = 1;
   };
   tiles();
-  const int64_t all = (int64_t)p.rest * p.KB;
-  const int parts = (int)std::min<int64_t>(pairs, all / kLeastBlocks);
-  if (parts > p.rest && p.KB - all / parts > 6 + (int64_t)parts * p.W / 1500) {
+  const int parts = p.rest ? std::min(pairs / p.rest, p.KB / kLeastBlocks) : 1;
+  if (parts > 1 && p.KB - (p.KB + parts - 1) / parts > 6 + (int64_t)p.rest * parts * p.W / 1500) {
     p.parts = parts;
   } else if (p.whole == 0 && p.CT <= pairs / 2) {
     p.MT = std::max(p.MT, std::min((p.M + kLeastM - 1) / kLeastM, pairs / p.CT));
     tiles();
   }
-  return p.whole > 0 ? pairs : p.parts;
+  return p.whole > 0 ? pairs : p.rest * p.parts;
 }
 
 }  // namespace
@@ -600,7 +567,7 @@ extern "C" stp_status stp_ckpt_wgrad_workspace_size(const stp_ckpt_desc* desc, i
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_ckpt_wgrad_workspace_size: %s", cudaGetErrorString(e));
   WgradParams p{};
   plan(p, desc, cols, n_sm);
-  *ws_bytes = 256 + (p.parts > p.rest ? 4 * (size_t)p.parts * kPartBytes : 0);
+  *ws_bytes = 256 + (p.parts > 1 ? 2 * (size_t)p.parts * p.rest * kPartBytes : 0);
   return STP_OK;
 }
 
@@ -641,7 +608,7 @@ extern "C" stp_status stp_ckpt_wgrad(const stp_ckpt_desc* desc, int32_t cols, co
     if (!make_map(&ty, d_y, p.N, p.M, y_stride)) return fail(STP_ECUDA, "stp_ckpt_wgrad: tensor map encoding failed");
     wgrad_kernel<<<2 * pairs, kThreads, kSmem, s>>>(ty, p);
     e = cudaGetLastError();
-    if (e == cudaSuccess && p.parts > p.rest) e = launch_after(wgrad_join_kernel, dim3(p.W / 4, p.rest), dim3(256), s, p);
+    if (e == cudaSuccess && p.parts > 1) e = launch_after(wgrad_join_kernel, dim3(p.W / 4, p.rest), dim3(256), s, p);
   }
   if (e != cudaSuccess) return fail(STP_ECUDA, "stp_ckpt_wgrad: %s", cudaGetErrorString(e));
   return STP_OK;
