@@ -330,32 +330,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     } else if (warp == 9) {
-    if (lane == 0 && block == 0) {
+    // the whole warp walks, so that addresses stay in uniform registers; one lane issues
+    const bool one = elect_one();
+    if (block == 0) {
       // --------------------------------------------------------- products
-      const uint32_t idesc = idesc_bf16(kTileC, p.W, 0, 1);
+      const uint32_t idesc = idesc_bf16(kTileC, p.W, 0, 1), b0 = desc_lo_mnmajor(smem_u32(smem));
       int it = 0, chunk = 0, in = 0;
       for (Walk w(p, g, pairs); w.on(); ++it) {
-        if (in == 0 && chunk > 0 && !wait(&bars[W_DE], (chunk - 1) & 1, abort_flag, p.err)) break;
+        if (in == 0 && chunk > 0 && !__all_sync(0xffffffffu, wait(&bars[W_DE], (chunk - 1) & 1, abort_flag, p.err))) break;
         const int st = it % kStages;
         const uint32_t phase = (it / kStages) & 1;
-        if (!wait(&bars[W_BF + st], phase, abort_flag, p.err) ||
-            !wait(&bars[W_AF + st], phase, abort_flag, p.err))
+        if (!__all_sync(0xffffffffu, wait(&bars[W_BF + st], phase, abort_flag, p.err) &&
+                                         wait(&bars[W_AF + st], phase, abort_flag, p.err)))
           break;
         fence_after_sync();
-        const uint32_t b_lo = desc_lo_mnmajor(smem_u32(smem) + st * kYBytes), a = tmem + kColA + st * 64;
+        if (one) {
+          const uint32_t b_lo = b0 + st * (kYBytes >> 4), a = tmem + kColA + st * 64;
 #pragma unroll
-        for (int kk = 0; kk < kCkTokens / 16; ++kk) mma_pair(tmem, a + kk * 8, b_lo + kk * (2048 >> 4), idesc, in > 0 || kk > 0);
-        commit_pair(&bars[W_E + st]);
+          for (int kk = 0; kk < kCkTokens / 16; ++kk) mma_pair(tmem, a + kk * 8, b_lo + kk * (2048 >> 4), idesc, in > 0 || kk > 0);
+          commit_pair(&bars[W_E + st]);
+        }
+        __syncwarp();
         const int tile = w.i;
         w.next();
         if (++in == kChunk || w.i != tile) {
-          commit_pair(&bars[W_DF]);
+          if (one) commit_pair(&bars[W_DF]);
           in = 0;
           ++chunk;
         }
       }
-      commit_pair(&bars[W_DRAIN]);
-      if (chunk > 0) wait(&bars[W_DE], (chunk - 1) & 1, abort_flag, p.err);   // the other block's last arrivals, too
+      if (one) {
+        commit_pair(&bars[W_DRAIN]);
+        if (chunk > 0) wait(&bars[W_DE], (chunk - 1) & 1, abort_flag, p.err);   // the other block's last arrivals, too
+      }
+      __syncwarp();
     }
     // nothing of the pair is in flight behind this; the second block's wait is all it does, so it looks rarely
     if (lane == 0)
