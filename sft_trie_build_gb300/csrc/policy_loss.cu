@@ -12,7 +12,8 @@
 // Bound by memory, as token_loss.cu: forward one read, backward one read and
 // one write, the step one read and one write, its second pass out of L2.  The
 // token's own logit is put right by one store after the pass, so that the pass
-// compares no ids.
+// compares no ids.  Short rows are a warp's, whose sums take no meeting of a
+// block.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -96,9 +97,154 @@ __device__ __forceinline__ Terms terms_of(const PolicyParams& p, int n, float lp
   return t;
 }
 
-// Forward (LSE), backward (GRAD) or both.  MANY: several blocks per row.
-template <typename T, bool LSE, bool GRAD, bool MANY>
-__global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPassBlocks)
+// What a row has besides its gradient, from its sums.
+// ln p = scale (x - m) - ref: with both passes at hand m is the row's maximum
+// and ref = ln sum exp(z - scale m), which hold for logits of any size.
+struct Row {
+  float m, ref, ent, lp;
+};
+__device__ __forceinline__ Row row_of(const PolicyParams& p, const Acc& s, float zt) {
+  const bool none = s.m == -INFINITY && s.s == 0.f;   // nothing but -inf
+  Row r;
+  r.m = s.m;
+  r.ref = log_sum(s);
+  r.lp = none && !isnan(zt) ? -INFINITY : fmaf(zt - r.m, p.scale, -r.ref);
+  r.ent = none ? 0.f : kLn2T * (log2f(s.s) - s.t / s.s);
+  return r;
+}
+__device__ __forceinline__ void put_outputs(const PolicyParams& p, int n, const Row& r, const Terms& term) {
+  p.lse[n] = r.m == -INFINITY && r.lp == -INFINITY ? -INFINITY : fmaf(r.m, p.scale, r.ref);
+  p.logprob[n] = r.lp;
+  p.entropy[n] = r.ent;
+  p.loss[n] = p.gamma != 0.f ? fmaf(-p.gamma, r.ent, term.loss) : term.loss;
+  if (p.kl) p.kl[n] = term.kl;
+}
+__device__ __forceinline__ void put_unread(const PolicyParams& p, int n, int target) {
+  const float x = target < 0 ? 0.f : NAN;
+  p.loss[n] = p.logprob[n] = p.entropy[n] = p.lse[n] = x;
+  if (p.kl) p.kl[n] = x;
+  if (!p.check && target >= p.V) atomicOr(p.err, kErrBadList);
+}
+
+// dz = p (h ln p + c), and g more for the token itself.  LSE: from the row's
+// maximum, else from lse alone.
+template <bool LSE>
+struct RowGrad {
+  float scale, sl2, sub, up, shift, h2, c, g;
+  __device__ __forceinline__ RowGrad(const PolicyParams& p, int n, const Row& r, const Terms& term) {
+    const float w = p.w[n] * p.scale, h = w * p.gamma;
+    g = w * term.g;
+    c = p.gamma != 0.f ? fmaf(h, r.ent, -g) : -g;
+    h2 = h * kLn2T;
+    scale = p.scale;
+    sl2 = p.sl2;
+    shift = -r.ref * kLog2eT;
+    up = -r.ref;
+    sub = -r.m;
+  }
+  __device__ __forceinline__ float operator()(float x) const {
+    const float l2 = LSE ? fmaf(x + sub, sl2, shift) : fmaf(x, scale, up) * kLog2eT;   // ln p in units of ln 2
+    return ex2(l2) * fmaf(h2, fmaxf(l2, -1e30f), c);
+  }
+  // Two by two, as the pass issues more than it may; without an entropy term p times one number.
+  template <bool ENT, int N>
+  __device__ __forceinline__ void apply(float* z) const {
+    if constexpr (N % 2) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) z[e] = (*this)(z[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        float2 l = make_float2(z[e], z[e + 1]);
+        l = LSE ? __ffma2_rn(__fadd2_rn(l, make_float2(sub, sub)), make_float2(sl2, sl2), make_float2(shift, shift))
+                : __fmul2_rn(__ffma2_rn(l, make_float2(scale, scale), make_float2(up, up)), make_float2(kLog2eT, kLog2eT));
+        const float2 term = ENT ? __ffma2_rn(make_float2(h2, h2), make_float2(fmaxf(l.x, -1e30f), fmaxf(l.y, -1e30f)),
+                                             make_float2(c, c))
+                                : make_float2(c, c);
+        const float2 p2 = __fmul2_rn(make_float2(ex2(l.x), ex2(l.y)), term);
+        z[e] = p2.x;
+        z[e + 1] = p2.y;
+      }
+    }
+  }
+};
+
+constexpr int kShortFlight = 8;   // logits of a lane at a time, in a warp's row
+
+// Whether rows are a warp's: short ones, and many of them or very short ones.
+// Measured in us, a block's and a warp's, of 20000 bf16 rows: step of 1000 logits 157 / 41,
+// of 4096 193 / 120, of 8000 206 / 243; forward of 1000 108 / 22, of 8000 141 / 98;
+// step of 200 rows of 2048 8.6 / 13.5.
+bool short_rows(int n, int vocab, bool grad) {
+  return vocab <= (grad ? 4096 : 8192) && (n >= 1216 || vocab <= 512);
+}
+
+template <typename T, bool LSE, bool GRAD>
+__global__ void __launch_bounds__(kRowThreads) policy_short_kernel(const PolicyParams p) {
+  if (LSE && p.check && blockIdx.x == gridDim.x - 1) {
+    check_below(p.N, p.V, p.err, [&](int64_t i) { return p.target[i]; });
+    return;
+  }
+  const int n = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (n >= p.N) return;
+  const T* row = static_cast<const T*>(p.z) + (int64_t)n * p.stride;
+  T* out = GRAD ? static_cast<T*>(p.dz) + (int64_t)n * p.stride : nullptr;
+  const int target = p.target[n];
+  if (target < 0 || target >= p.V) {
+    if (LSE && lane == 0) put_unread(p, n, target);
+    if (GRAD)
+      for (int i = lane; i < p.V; i += 32) put(out + i, 0.f);
+    return;
+  }
+  const auto load = [&](int i0, float* z) {
+#pragma unroll
+    for (int k = 0; k < kShortFlight; ++k) z[k] = i0 + k * 32 < p.V ? to_f(row[i0 + k * 32]) : -INFINITY;
+  };
+  const float zt = to_f(row[target]);
+  Row r{0.f, 0.f, 0.f, 0.f};
+  if (LSE) {
+    Acc a = {-INFINITY, 0.f, 0.f};
+    for (int i0 = lane; i0 - lane < p.V; i0 += 32 * kShortFlight) {
+      float z[kShortFlight], most, least;
+      load(i0, z);
+      extremes<kShortFlight>(z, most, least);
+      add<kShortFlight, true>(a, z, most, least, p.sl2);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Acc b;
+      b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
+      b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+      b.t = __shfl_xor_sync(0xffffffffu, a.t, o);
+      a = merge(a, b, p.sl2);
+    }
+    r = row_of(p, a, zt);
+  } else {
+    r = {0.f, p.lse_in[n], p.ent_in[n], p.lp_in[n]};
+  }
+  const Terms term = terms_of(p, n, r.lp);
+  if (LSE && lane == 0) put_outputs(p, n, r, term);
+  if (GRAD) {
+    __syncwarp();   // every lane has zt before a logit may be overwritten
+    const RowGrad<LSE> grad(p, n, r, term);
+    const bool zero = r.lp == -INFINITY;   // no step can raise it
+    for (int i0 = lane; i0 - lane < p.V; i0 += 32 * kShortFlight) {
+      float z[kShortFlight];
+      load(i0, z);
+      grad.template apply<true, kShortFlight>(z);
+#pragma unroll
+      for (int k = 0; k < kShortFlight; ++k) {
+        const int i = i0 + k * 32;
+        if (i < p.V) put(out + i, zero ? 0.f : i == target ? grad(zt) + grad.g : z[k]);
+      }
+    }
+  }
+}
+
+// Forward (LSE), backward (GRAD) or both.  MANY: several blocks per row.  FOUR: a step's rows are small enough
+// for as many blocks on an SM as a pass has.
+template <typename T, bool LSE, bool GRAD, bool MANY, bool FOUR = false>
+__global__ void __launch_bounds__(kRowThreads, LSE && GRAD && !FOUR ? kStepBlocks : kPassBlocks)
     policy_kernel(const PolicyParams p) {
   __shared__ Acc red[kRowWarps];
   __shared__ Acc sums[kMaxSplit];   // of the row's blocks
@@ -112,25 +258,18 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
   T* out = GRAD ? static_cast<T*>(p.dz) + (int64_t)n * p.stride : nullptr;
   const int target = p.target[n];
   if (target < 0 || target >= p.V) {   // the same for every block of the row
-    if (LSE && rank == 0 && t == 0) {
-      const float x = target < 0 ? 0.f : NAN;
-      p.loss[n] = p.logprob[n] = p.entropy[n] = p.lse[n] = x;
-      if (p.kl) p.kl[n] = x;
-      if (!p.check && target >= p.V) atomicOr(p.err, kErrBadList);
-    }
+    if (LSE && rank == 0 && t == 0) put_unread(p, n, target);
     if (GRAD) zero_row(out, p.V, rank, C);
     return;
   }
   const Part part = part_of(row, p.V, rank, C);
-  const auto ring = ring_of<LSE && GRAD ? kStepRounds : kPassRounds>(buffer, row, part);
+  const auto ring = ring_of<LSE && GRAD && !FOUR ? kStepRounds : kPassRounds>(buffer, row, part);
   ring.start(part.b0 + t);
   if (LSE && MANY) cg::this_cluster().barrier_arrive();   // this block runs: others may write to it
   const bool mine = target >= part.lo && target < part.hi;
   // backward alone: other blocks may write over what is not their part already
   const float zt = LSE || mine ? to_f(row[target]) : 0.f;
-  // ln p = scale (x - m) - ref: with both passes at hand m is the row's maximum
-  // and ref = ln sum exp(z - scale m), which hold for logits of any size
-  float m = 0.f, ref, ent, lp;
+  Row r;
   if (LSE) {
     float best;
     int round;
@@ -144,70 +283,26 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD ? kStepBlocks : kPass
       cl.sync();
       s = merge_all(sums, C, p.sl2);
     }
-    const bool none = s.m == -INFINITY && s.s == 0.f;   // nothing but -inf
-    m = s.m;
-    ref = log_sum(s);
-    lp = none && !isnan(zt) ? -INFINITY : fmaf(zt - m, p.scale, -ref);
-    ent = none ? 0.f : kLn2T * (log2f(s.s) - s.t / s.s);
-    if (rank == 0 && t == 0) {
-      p.lse[n] = none ? -INFINITY : fmaf(m, p.scale, ref);
-      p.logprob[n] = lp;
-      p.entropy[n] = ent;
-    }
+    r = row_of(p, s, zt);
   } else {
-    ref = p.lse_in[n];
-    lp = p.lp_in[n];
-    ent = p.ent_in[n];
+    r = {0.f, p.lse_in[n], p.ent_in[n], p.lp_in[n]};
   }
-  const Terms term = terms_of(p, n, lp);
-  if (LSE && rank == 0 && t == 0) {
-    p.loss[n] = p.gamma != 0.f ? fmaf(-p.gamma, ent, term.loss) : term.loss;
-    if (p.kl) p.kl[n] = term.kl;
-  }
+  const Terms term = terms_of(p, n, r.lp);
+  if (LSE && rank == 0 && t == 0) put_outputs(p, n, r, term);
   if (GRAD) {
     __syncthreads();   // every zt is read before a logit may be overwritten
-    if (lp == -INFINITY) {   // no step can raise it
+    if (r.lp == -INFINITY) {   // no step can raise it
       asm volatile("cp.async.wait_all;" ::: "memory");
       zero_row(out, p.V, rank, C);
       return;
     }
-    const float w = p.w[n] * p.scale, g = w * term.g;
-    // dz = p (h ln p + c), and g more for the token itself
-    const float h = w * p.gamma, c = p.gamma != 0.f ? fmaf(h, ent, -g) : -g;
-    const float shift = -ref * kLog2eT, scale = p.scale, sl2 = p.sl2, h2 = h * kLn2T;
-    // ln p in units of ln 2; with both passes l2 = (x - m) sl2 + shift
-    const float up = LSE ? 0.f : 0.f - ref, sub = LSE ? -m : 0.f;
-    const auto log2p = [=](float x) { return LSE ? fmaf(x + sub, sl2, shift) : fmaf(x, scale, up) * kLog2eT; };
-    const auto grad = [=](float x) {
-      const float l2 = log2p(x);
-      return ex2(l2) * fmaf(h2, fmaxf(l2, -1e30f), c);
-    };
-    // two by two, as the pass issues more than it may; without an entropy term p times one number
-    const auto pairs = [=](float* z, auto N, auto term) {
-      if constexpr (decltype(N)::value % 2 == 0) {
-#pragma unroll
-        for (int e = 0; e < N(); e += 2) {
-          float2 l = make_float2(z[e], z[e + 1]);
-          l = LSE ? __ffma2_rn(__fadd2_rn(l, make_float2(sub, sub)), make_float2(sl2, sl2), make_float2(shift, shift))
-                  : __fmul2_rn(__ffma2_rn(l, make_float2(scale, scale), make_float2(up, up)), make_float2(kLog2eT, kLog2eT));
-          const float2 p2 = __fmul2_rn(make_float2(ex2(l.x), ex2(l.y)), term(l));
-          z[e] = p2.x;
-          z[e + 1] = p2.y;
-        }
-      } else {
-        z[0] = grad(z[0]);
-      }
-    };
-    if (h2 == 0.f)
-      map_row(row, out, part, ring, [=](float* z, int, auto N) { pairs(z, N, [=](float2) { return make_float2(c, c); }); });
+    const RowGrad<LSE> grad(p, n, r, term);
+    if (grad.h2 == 0.f)
+      map_row(row, out, part, ring, [=](float* z, int, auto N) { grad.template apply<false, decltype(N)::value>(z); });
     else
-      map_row(row, out, part, ring, [=](float* z, int, auto N) {
-        pairs(z, N, [=](float2 l) {
-          return __ffma2_rn(make_float2(h2, h2), make_float2(fmaxf(l.x, -1e30f), fmaxf(l.y, -1e30f)), make_float2(c, c));
-        });
-      });
+      map_row(row, out, part, ring, [=](float* z, int, auto N) { grad.template apply<true, decltype(N)::value>(z); });
     __syncthreads();   // the block's stores before that of the token
-    if (mine && t == 0) put(out + target, grad(zt) + g);
+    if (mine && t == 0) put(out + target, grad(zt) + grad.g);
   }
 }
 
@@ -222,12 +317,27 @@ stp_status check_policy(const stp_policy_desc* d) {
   return check_rows(d->n_rows, d->vocab, d->stride, d->dtype, d->scale);
 }
 
-template <typename T>
-const void* policy_of(bool lse, bool grad, bool many) {
-  if (!lse) return (const void*)policy_kernel<T, false, true, true>;
-  if (!grad) return many ? (const void*)policy_kernel<T, true, false, true> : (const void*)policy_kernel<T, true, false, false>;
-  return many ? (const void*)policy_kernel<T, true, true, true> : (const void*)policy_kernel<T, true, true, false>;
+// How the rows of a call are taken.
+enum Form { kWarp, kBlock, kFour, kMany };
+
+// A step's rows of up to 100 KB: four blocks on an SM.  Measured in us, three and four: rows of 64 KB
+// (16000) 380 / 341, of 100 KB (8000) 270 / 258, of 120 KB (8000) 317 / 348.
+constexpr int64_t kFourBytes = 100 << 10;
+
+template <typename T, bool LSE, bool GRAD>
+const void* policy_as(Form f) {
+  if (f == kWarp) return (const void*)policy_short_kernel<T, LSE, GRAD>;
+  if constexpr (!LSE) return (const void*)policy_kernel<T, false, true, true>;
+  if constexpr (LSE && GRAD)
+    if (f == kFour) return (const void*)policy_kernel<T, true, true, false, true>;
+  return f == kMany ? (const void*)policy_kernel<T, LSE, GRAD, true> : (const void*)policy_kernel<T, LSE, GRAD, false>;
 }
+template <typename T>
+const void* policy_of(bool lse, bool grad, Form f) {
+  if (!lse) return policy_as<T, false, true>(f);
+  return grad ? policy_as<T, true, true>(f) : policy_as<T, true, false>(f);
+}
+int rounds_of(bool lse, bool grad, Form f) { return lse && grad && f != kFour ? kStepRounds : kPassRounds; }
 
 // The kernels' dynamic shared memory, above the default limit.
 cudaError_t allow_policy() {
@@ -236,11 +346,10 @@ cudaError_t allow_policy() {
     cudaError_t e = cudaSuccess;
     for (const bool lse : {false, true})
       for (const bool grad : {false, true})
-        for (const bool many : {false, true})
-          for (const void* k : {policy_of<__nv_bfloat16>(lse, grad, many), policy_of<float>(lse, grad, many)})
+        for (const Form f : {kBlock, kFour, kMany})
+          for (const void* k : {policy_of<__nv_bfloat16>(lse, grad, f), policy_of<float>(lse, grad, f)})
             if (e == cudaSuccess)
-              e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       ring_bytes(lse && grad ? kStepRounds : kPassRounds));
+              e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_bytes(rounds_of(lse, grad, f)));
     return e;
   });
 }
@@ -278,10 +387,19 @@ stp_status policy(const char* name, const stp_policy_desc* d, PolicyParams p, vo
     const int64_t bytes = row_bytes(p.V, d->dtype);
     const bool both = fwd && grad;
     p.C = both ? step_split_of(p.N, bytes) : split_of(p.N, bytes);
-    const void* k = d->dtype == STP_BF16 ? policy_of<__nv_bfloat16>(fwd, grad, p.C > 1)
-                                         : policy_of<float>(fwd, grad, p.C > 1);
-    e = allow_policy();
-    if (e == cudaSuccess) e = launch_rows(k, both ? kStepRounds : kPassRounds, p.N + p.check, p.C, &p, fwd, s);
+    const Form f = short_rows(p.N, p.V, grad) ? kWarp : p.C > 1 ? kMany : both && bytes <= kFourBytes ? kFour : kBlock;
+    const void* k = d->dtype == STP_BF16 ? policy_of<__nv_bfloat16>(fwd, grad, f) : policy_of<float>(fwd, grad, f);
+    if (f == kWarp) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)(((int64_t)p.N + kRowWarps - 1) / kRowWarps + p.check));
+      cfg.blockDim = dim3(kRowThreads);
+      cfg.stream = s;
+      void* args[] = {&p};
+      e = cudaLaunchKernelExC(&cfg, k, args);
+    } else {
+      e = allow_policy();
+      if (e == cudaSuccess) e = launch_rows(k, rounds_of(fwd, grad, f), p.N + p.check, p.C, &p, fwd, s);
+    }
   }
   if (e != cudaSuccess) return fail(STP_ECUDA, "%s: %s", name, cudaGetErrorString(e));
   return STP_OK;

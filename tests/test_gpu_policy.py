@@ -232,3 +232,36 @@ def test_captured_and_on_another_stream():
         graph.replay()
     torch.cuda.synchronize()
     assert np.array_equal(dz.double().cpu().numpy(), want["dz"]) and np.array_equal(out[0].double().cpu().numpy(), want["loss"])
+
+
+@pytest.mark.parametrize("how", ["fwd", "both", "step"])
+@pytest.mark.parametrize("n,v,dtype", [(1300, 513, stp.STP_BF16), (1300, 4096, stp.STP_FP32), (1217, 700, stp.STP_FP32), (9, 512, stp.STP_BF16),
+                                       (40, 31, stp.STP_FP32), (700, 9000, stp.STP_BF16), (1216, 8192, stp.STP_BF16)])
+def test_rows_of_a_warp_and_of_a_block(n, v, dtype, how):
+    # both sides of the rules on sizes: short rows, many and few of them
+    c = Case(n, v, dtype, scale=0.8)
+    a = c.call(how)
+    c.check(a)
+    if how != "fwd":
+        b = c.call(how, into=c.z)
+        assert all(np.array_equal(a[k], b[k]) for k in a)
+
+
+@pytest.mark.parametrize("n", [6, 1300])
+@pytest.mark.parametrize("how", ["both", "step"])
+def test_short_rows_strided_with_special_values(how, n):
+    v = 300
+    c = Case(n, v, stp.STP_BF16, stride=v + 3, offset=1)
+    c.z[0, v // 2:] = -INF
+    c.z[3] = -INF
+    c.z[4, 7] = NAN
+    c.z[5] = torch.finfo(torch.bfloat16).min
+    c.t[:6] = [3, -1, 5, 6, 7, 8]
+    between = c.z.as_strided((n - 1, 3), (v + 3, 1), c.z.storage_offset() + v).clone()
+    want = {k: x.copy() for k, x in c.call(how).items()}
+    assert want["logprob"][3] == -INF and (want["dz"][3] == 0).all() and want["entropy"][3] == 0
+    assert np.isnan(want["loss"][4]) and np.isnan(want["dz"][4]).any() and (want["dz"][0, v // 2:] == 0).all()
+    assert abs(want["logprob"][5] + np.log(v)) <= 1e-4 or how == "both"
+    got = c.call(how, into=c.z)
+    assert all(np.array_equal(want[k], got[k], equal_nan=True) for k in want)
+    assert torch.equal(c.z.as_strided((n - 1, 3), (v + 3, 1), c.z.storage_offset() + v), between)
