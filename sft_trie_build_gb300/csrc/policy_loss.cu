@@ -97,19 +97,33 @@ __device__ __forceinline__ Terms terms_of(const PolicyParams& p, int n, float lp
   return t;
 }
 
+// ln s in two numbers, of which the first is exact: s = 2^e f with f near 1, and
+// ln 2 is split so that e times its first part has no rounding (Cody and Waite's
+// reduction).  The log-probability of a likely token is the difference of two
+// numbers near 10, whose own roundings would be all its error.
+__device__ __forceinline__ float2 log_parts(float s) {
+  if (!(s > 0.f && s < INFINITY)) return make_float2(logf(s), 0.f);
+  const int bits = __float_as_int(s), up = (bits & 0x7fffff) > 0x3504f3;   // f above the root of 2 is halved
+  const float e = (float)((bits >> 23) - 127 + up);
+  const float f = __int_as_float((bits & 0x7fffff) | ((127 - up) << 23));
+  return make_float2(e * 0.693359375f, fmaf(e, -2.12194440e-4f, logf(f)));
+}
+
 // What a row has besides its gradient, from its sums.
-// ln p = scale (x - m) - ref: with both passes at hand m is the row's maximum
-// and ref = ln sum exp(z - scale m), which hold for logits of any size.
+// p = exp(scale (x - m)) / s and ln p = scale (x - m) - ref, which hold for
+// logits of any size; from lse alone ref = lse, m = 0.
 struct Row {
-  float m, ref, ent, lp;
+  float m, ref, ent, lp, inv;   // inv = 1 / s
 };
 __device__ __forceinline__ Row row_of(const PolicyParams& p, const Acc& s, float zt) {
   const bool none = s.m == -INFINITY && s.s == 0.f;   // nothing but -inf
+  const float2 ln = log_parts(s.s);
   Row r;
   r.m = s.m;
-  r.ref = log_sum(s);
-  r.lp = none && !isnan(zt) ? -INFINITY : fmaf(zt - r.m, p.scale, -r.ref);
-  r.ent = none ? 0.f : kLn2T * (log2f(s.s) - s.t / s.s);
+  r.ref = ln.x + ln.y;
+  r.lp = none && !isnan(zt) ? -INFINITY : fmaf(zt - r.m, p.scale, -ln.x) - ln.y;
+  r.inv = 1.f / s.s;
+  r.ent = none ? 0.f : fmaf(-kLn2T, s.t * r.inv, ln.x) + ln.y;
   return r;
 }
 __device__ __forceinline__ void put_outputs(const PolicyParams& p, int n, const Row& r, const Terms& term) {
@@ -127,15 +141,15 @@ __device__ __forceinline__ void put_unread(const PolicyParams& p, int n, int tar
 }
 
 // dz = p (h ln p + c), and g more for the token itself.  LSE: from the row's
-// maximum, else from lse alone.
+// maximum and sum (whose inverse is in h2 and c), else from lse alone.
 template <bool LSE>
 struct RowGrad {
   float scale, sl2, sub, up, shift, h2, c, g;
   __device__ __forceinline__ RowGrad(const PolicyParams& p, int n, const Row& r, const Terms& term) {
-    const float w = p.w[n] * p.scale, h = w * p.gamma;
+    const float w = p.w[n] * p.scale, h = w * p.gamma, inv = LSE ? r.inv : 1.f;
     g = w * term.g;
-    c = p.gamma != 0.f ? fmaf(h, r.ent, -g) : -g;
-    h2 = h * kLn2T;
+    c = (p.gamma != 0.f ? fmaf(h, r.ent, -g) : -g) * inv;
+    h2 = h * kLn2T * inv;
     scale = p.scale;
     sl2 = p.sl2;
     shift = -r.ref * kLog2eT;
@@ -143,8 +157,9 @@ struct RowGrad {
     sub = -r.m;
   }
   __device__ __forceinline__ float operator()(float x) const {
-    const float l2 = LSE ? fmaf(x + sub, sl2, shift) : fmaf(x, scale, up) * kLog2eT;   // ln p in units of ln 2
-    return ex2(l2) * fmaf(h2, fmaxf(l2, -1e30f), c);
+    const float d = LSE ? (x + sub) * sl2 : fmaf(x, scale, up) * kLog2eT;
+    const float l2 = LSE ? d + shift : d;   // ln p in units of ln 2
+    return ex2(d) * fmaf(h2, fmaxf(l2, -1e30f), c);
   }
   // Two by two, as the pass issues more than it may; without an entropy term p times one number.
   template <bool ENT, int N>
@@ -155,13 +170,16 @@ struct RowGrad {
     } else {
 #pragma unroll
       for (int e = 0; e < N; e += 2) {
-        float2 l = make_float2(z[e], z[e + 1]);
-        l = LSE ? __ffma2_rn(__fadd2_rn(l, make_float2(sub, sub)), make_float2(sl2, sl2), make_float2(shift, shift))
-                : __fmul2_rn(__ffma2_rn(l, make_float2(scale, scale), make_float2(up, up)), make_float2(kLog2eT, kLog2eT));
-        const float2 term = ENT ? __ffma2_rn(make_float2(h2, h2), make_float2(fmaxf(l.x, -1e30f), fmaxf(l.y, -1e30f)),
-                                             make_float2(c, c))
-                                : make_float2(c, c);
-        const float2 p2 = __fmul2_rn(make_float2(ex2(l.x), ex2(l.y)), term);
+        const float2 x = make_float2(z[e], z[e + 1]);
+        const float2 d =
+            LSE ? __fmul2_rn(__fadd2_rn(x, make_float2(sub, sub)), make_float2(sl2, sl2))
+                : __fmul2_rn(__ffma2_rn(x, make_float2(scale, scale), make_float2(up, up)), make_float2(kLog2eT, kLog2eT));
+        float2 term = make_float2(c, c);
+        if constexpr (ENT) {
+          const float2 l = LSE ? __fadd2_rn(d, make_float2(shift, shift)) : d;
+          term = __ffma2_rn(make_float2(h2, h2), make_float2(fmaxf(l.x, -1e30f), fmaxf(l.y, -1e30f)), term);
+        }
+        const float2 p2 = __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), term);
         z[e] = p2.x;
         z[e + 1] = p2.y;
       }
@@ -201,7 +219,7 @@ __global__ void __launch_bounds__(kRowThreads) policy_short_kernel(const PolicyP
     for (int k = 0; k < kShortFlight; ++k) z[k] = i0 + k * 32 < p.V ? to_f(row[i0 + k * 32]) : -INFINITY;
   };
   const float zt = to_f(row[target]);
-  Row r{0.f, 0.f, 0.f, 0.f};
+  Row r{};
   if (LSE) {
     Acc a = {-INFINITY, 0.f, 0.f};
     for (int i0 = lane; i0 - lane < p.V; i0 += 32 * kShortFlight) {
@@ -220,7 +238,7 @@ __global__ void __launch_bounds__(kRowThreads) policy_short_kernel(const PolicyP
     }
     r = row_of(p, a, zt);
   } else {
-    r = {0.f, p.lse_in[n], p.ent_in[n], p.lp_in[n]};
+    r = {0.f, p.lse_in[n], p.ent_in[n], p.lp_in[n], 1.f};
   }
   const Terms term = terms_of(p, n, r.lp);
   if (LSE && lane == 0) put_outputs(p, n, r, term);
@@ -285,7 +303,7 @@ __global__ void __launch_bounds__(kRowThreads, LSE && GRAD && !FOUR ? kStepBlock
     }
     r = row_of(p, s, zt);
   } else {
-    r = {0.f, p.lse_in[n], p.ent_in[n], p.lp_in[n]};
+    r = {0.f, p.lse_in[n], p.ent_in[n], p.lp_in[n], 1.f};
   }
   const Terms term = terms_of(p, n, r.lp);
   if (LSE && rank == 0 && t == 0) put_outputs(p, n, r, term);
