@@ -230,7 +230,8 @@ stp_status ckpt(const char* name, const stp_ckpt_desc* d, const void* x, void* y
   if (!t || !ck) return fail(STP_EINVAL, "%s: NULL device pointer", name);
   if (reinterpret_cast<uintptr_t>(ck) & 255) return fail(STP_EINVAL, "%s: the checkpoint must be 256-byte aligned", name);
   const int size = d->dtype == STP_BF16 ? 2 : 4;
-  if (reinterpret_cast<uintptr_t>(t) & (size - 1)) return fail(STP_EINVAL, "%s: the tensor is misaligned for its type", name);
+  if (reinterpret_cast<uintptr_t>(t) & (size - 1))
+    return fail(STP_EINVAL, "%s: the tensor is misaligned for its type", name);
   CkptParams p{};
   p.N = d->n_tokens;
   p.C = d->dim;

@@ -73,7 +73,8 @@ constexpr int kGroups = 2;          // warp groups among them
 // 16384-token projection against 549 at the time.
 constexpr int kStages = 4;
 constexpr int kAhead = 3;           // stages converted ahead when sums are taken: less than kStages
-// A group meets each of its stages in every round of the ring: a wait by parity would take the phase two rounds before for the one it wants.
+// A group meets each of its stages in every round of the ring: else a wait by
+// parity would take the phase two rounds before for the one it wants.
 static_assert(kStages % kGroups == 0 && kAhead < kStages, "ring of stages");
 constexpr int kChunk = 16;          // stages between two takings
 constexpr int kTileC = 256, kHalfC = 128, kTileM = 256;
@@ -109,7 +110,17 @@ struct Segment {
 // stage is multiplied (both); the sums of a chunk are ready (both) and taken by both (first
 // block's).  Codes are fetched again as soon as they are read, so that their way from memory
 // does not lie between a product and the next conversion for its stage.
-enum { W_CF = 0, W_CE = kStages, W_BF = 2 * kStages, W_AF = 3 * kStages, W_E = 4 * kStages, W_DF = 5 * kStages, W_DE, W_DRAIN, W_COUNT };
+enum {
+  W_CF = 0,
+  W_CE = kStages,
+  W_BF = 2 * kStages,
+  W_AF = 3 * kStages,
+  W_E = 4 * kStages,
+  W_DF = 5 * kStages,
+  W_DE,
+  W_DRAIN,
+  W_COUNT
+};
 
 // ---- a pair's instructions
 
@@ -293,90 +304,96 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp >= 8) {
     regs_dec<kRegsRest>();
     if (warp == 8) {
-    if (lane == 0) {
-      // -------------------------------------------------------------- dY
-      tma_prefetch_desc(&ty);
-      const int boxes = (p.W / 2 + 63) / 64;
-      int it = 0, last[kStages];   // phase of a stage's last load
-      for (int st = 0; st < kStages; ++st) last[st] = -1;
-      for (Walk w(p, g, pairs); w.on(); w.next(), ++it) {
-        const int st = it % kStages, n = it / kStages;
-        if (it >= kStages && !wait(&bars[W_E + st], (n - 1) & 1, abort_flag, p.err)) break;
-        const int m0 = w.mt * p.W + block * (p.W / 2);
-        const uint32_t bar = in_block(smem_u32(&bars[W_BF + st]), 0);
-        if (block == 0) mbar_expect_tx(&bars[W_BF + st], 2 * boxes * kBoxBytes);
-        for (int b = 0; b < boxes; ++b)
-          tma_load_pair(smem + st * kYBytes + b * kBoxBytes, &ty, bar, m0 + b * 64, w.kb * kCkTokens);
-        last[st] = n & 1;
-      }
-      // nothing is on its way to this block's memory or barriers when it ends
-      for (int st = 0; st < kStages; ++st) {
-        if (block == 0 && last[st] >= 0) mbar_wait_drain(&bars[W_BF + st], last[st]);
-        if (last[st] >= 0) wait(&bars[W_E + st], last[st], abort_flag, p.err);
-      }
-    }
-    __syncwarp();
-    } else if (warp == 10) {
-    if (lane == 0) {
-      // ----------------------------------------------------------- codes
-      int it = 0, last[kStages];
-      for (int st = 0; st < kStages; ++st) last[st] = -1;
-      for (Walk w(p, g, pairs); w.on(); w.next(), ++it) {
-        const int st = it % kStages, n = it / kStages, cb = w.ct * 8 + block * 4;
-        if (it >= kStages && !wait(&bars[W_CE + st], (n - 1) & 1, abort_flag, p.err)) break;
-        if (cb < p.CB) {
-          const uint32_t bytes = min(4, p.CB - cb) * kCkBlock;
-          mbar_expect_tx(&bars[W_CF + st], bytes);
-          bulk_load(codes + st * kCodeBytes, p.ck + ((int64_t)w.kb * p.CB + cb) * kCkBlock, bytes, &bars[W_CF + st]);
+      if (lane == 0) {
+        // -------------------------------------------------------------- dY
+        tma_prefetch_desc(&ty);
+        const int boxes = (p.W / 2 + 63) / 64;
+        int it = 0, last[kStages];   // phase of a stage's last load
+        for (int st = 0; st < kStages; ++st) last[st] = -1;
+        for (Walk w(p, g, pairs); w.on(); w.next(), ++it) {
+          const int st = it % kStages, n = it / kStages;
+          if (it >= kStages && !wait(&bars[W_E + st], (n - 1) & 1, abort_flag, p.err)) break;
+          const int m0 = w.mt * p.W + block * (p.W / 2);
+          const uint32_t bar = in_block(smem_u32(&bars[W_BF + st]), 0);
+          if (block == 0) mbar_expect_tx(&bars[W_BF + st], 2 * boxes * kBoxBytes);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_pair(smem + st * kYBytes + b * kBoxBytes, &ty, bar, m0 + b * 64, w.kb * kCkTokens);
           last[st] = n & 1;
-        } else {
-          mbar_arrive(&bars[W_CF + st]);   // channels past the end: nothing comes
         }
-      }
-      for (int st = 0; st < kStages; ++st)
-        if (last[st] >= 0) mbar_wait_drain(&bars[W_CF + st], last[st]);
-    }
-    __syncwarp();
-    } else if (warp == 9) {
-    // the whole warp walks, so that addresses stay in uniform registers; one lane issues
-    const bool one = elect_one();
-    if (block == 0) {
-      // --------------------------------------------------------- products
-      const uint32_t idesc = idesc_bf16(kTileC, p.W, 0, 1), b0 = desc_lo_mnmajor(smem_u32(smem));
-      int it = 0, chunk = 0, in = 0;
-      for (Walk w(p, g, pairs); w.on(); ++it) {
-        if (in == 0 && chunk > 0 && !__all_sync(0xffffffffu, wait(&bars[W_DE], (chunk - 1) & 1, abort_flag, p.err))) break;
-        const int st = it % kStages;
-        const uint32_t phase = (it / kStages) & 1;
-        if (!__all_sync(0xffffffffu, wait(&bars[W_BF + st], phase, abort_flag, p.err) &&
-                                         wait(&bars[W_AF + st], phase, abort_flag, p.err)))
-          break;
-        fence_after_sync();
-        if (one) {
-          const uint32_t b_lo = b0 + st * (kYBytes >> 4), a = tmem + kColA + st * 64;
-#pragma unroll
-          for (int kk = 0; kk < kCkTokens / 16; ++kk) mma_pair(tmem, a + kk * 8, b_lo + kk * (2048 >> 4), idesc, in > 0 || kk > 0);
-          commit_pair(&bars[W_E + st]);
+        // nothing is on its way to this block's memory or barriers when it ends
+        for (int st = 0; st < kStages; ++st) {
+          if (block == 0 && last[st] >= 0) mbar_wait_drain(&bars[W_BF + st], last[st]);
+          if (last[st] >= 0) wait(&bars[W_E + st], last[st], abort_flag, p.err);
         }
-        __syncwarp();
-        const int tile = w.i;
-        w.next();
-        if (++in == kChunk || w.i != tile) {
-          if (one) commit_pair(&bars[W_DF]);
-          in = 0;
-          ++chunk;
-        }
-      }
-      if (one) {
-        commit_pair(&bars[W_DRAIN]);
-        if (chunk > 0) wait(&bars[W_DE], (chunk - 1) & 1, abort_flag, p.err);   // the other block's last arrivals, too
       }
       __syncwarp();
-    }
-    // nothing of the pair is in flight behind this; the second block's wait is all it does, so it looks rarely
-    if (lane == 0)
-      for (const uint64_t t0 = globaltimer(); !mbar_try_wait(&bars[W_DRAIN], 0) && globaltimer() - t0 < kDrainLimitNs;) __nanosleep(500);
-    __syncwarp();
+    } else if (warp == 10) {
+      if (lane == 0) {
+        // ----------------------------------------------------------- codes
+        int it = 0, last[kStages];
+        for (int st = 0; st < kStages; ++st) last[st] = -1;
+        for (Walk w(p, g, pairs); w.on(); w.next(), ++it) {
+          const int st = it % kStages, n = it / kStages, cb = w.ct * 8 + block * 4;
+          if (it >= kStages && !wait(&bars[W_CE + st], (n - 1) & 1, abort_flag, p.err)) break;
+          if (cb < p.CB) {
+            const uint32_t bytes = min(4, p.CB - cb) * kCkBlock;
+            mbar_expect_tx(&bars[W_CF + st], bytes);
+            bulk_load(codes + st * kCodeBytes, p.ck + ((int64_t)w.kb * p.CB + cb) * kCkBlock, bytes, &bars[W_CF + st]);
+            last[st] = n & 1;
+          } else {
+            mbar_arrive(&bars[W_CF + st]);   // channels past the end: nothing comes
+          }
+        }
+        for (int st = 0; st < kStages; ++st)
+          if (last[st] >= 0) mbar_wait_drain(&bars[W_CF + st], last[st]);
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      // the whole warp walks, so that addresses stay in uniform registers; one lane issues
+      const bool one = elect_one();
+      if (block == 0) {
+        // --------------------------------------------------------- products
+        const uint32_t idesc = idesc_bf16(kTileC, p.W, 0, 1), b0 = desc_lo_mnmajor(smem_u32(smem));
+        int it = 0, chunk = 0, in = 0;
+        for (Walk w(p, g, pairs); w.on(); ++it) {
+          if (in == 0 && chunk > 0 &&
+              !__all_sync(0xffffffffu, wait(&bars[W_DE], (chunk - 1) & 1, abort_flag, p.err)))
+            break;
+          const int st = it % kStages;
+          const uint32_t phase = (it / kStages) & 1;
+          if (!__all_sync(0xffffffffu, wait(&bars[W_BF + st], phase, abort_flag, p.err) &&
+                                           wait(&bars[W_AF + st], phase, abort_flag, p.err)))
+            break;
+          fence_after_sync();
+          if (one) {
+            const uint32_t b_lo = b0 + st * (kYBytes >> 4), a = tmem + kColA + st * 64;
+#pragma unroll
+            for (int kk = 0; kk < kCkTokens / 16; ++kk)
+              mma_pair(tmem, a + kk * 8, b_lo + kk * (2048 >> 4), idesc, in > 0 || kk > 0);
+            commit_pair(&bars[W_E + st]);
+          }
+          __syncwarp();
+          const int tile = w.i;
+          w.next();
+          if (++in == kChunk || w.i != tile) {
+            if (one) commit_pair(&bars[W_DF]);
+            in = 0;
+            ++chunk;
+          }
+        }
+        if (one) {
+          commit_pair(&bars[W_DRAIN]);
+          if (chunk > 0) wait(&bars[W_DE], (chunk - 1) & 1, abort_flag, p.err);   // the other block's last arrivals, too
+        }
+        __syncwarp();
+      }
+      // nothing of the pair is in flight behind this; the second block's wait is
+      // all it does, so it looks rarely
+      if (lane == 0) {
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(&bars[W_DRAIN], 0) && globaltimer() - t0 < kDrainLimitNs) __nanosleep(500);
+      }
+      __syncwarp();
     }
   } else {
     regs_inc<kRegsSums>();
@@ -444,8 +461,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // the segment's results, 16 columns of 32 channels at a time through
       // shared memory, so that they leave in rows
       const int c0 = ct * kTileC + block * kHalfC + w4 * 32, m0 = mt * p.W + group * half;
-      float4* part = reinterpret_cast<float4*>(p.part) + (size_t)(max(slot, 0) * 2 + block) * (kPartBytes / 16) + w4 * 32 + lane +
-                     group * half / 4 * kHalfC;
+      float4* part = reinterpret_cast<float4*>(p.part) + (size_t)(max(slot, 0) * 2 + block) * (kPartBytes / 16) +
+                     w4 * 32 + lane + group * half / 4 * kHalfC;
 #pragma unroll
       for (int j = 0; j < kTileM / 2; j += 16) {
         if (j >= half) continue;
@@ -457,11 +474,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(stage + lane * kStageRow + e) = make_float4(acc[j + e], acc[j + e + 1], acc[j + e + 2], acc[j + e + 3]);
+            *reinterpret_cast<float4*>(stage + lane * kStageRow + e) =
+                make_float4(acc[j + e], acc[j + e + 1], acc[j + e + 2], acc[j + e + 3]);
           __syncwarp();
           const int e = (lane & 3) * 4, left = min(half, p.M - m0) - j - e;
           for (int r = lane >> 2; r < 32 && c0 + r < p.C; r += 8)
-            put4(p, p.dw + (int64_t)(c0 + r) * p.M + m0 + j + e, *reinterpret_cast<const float4*>(stage + r * kStageRow + e), left);
+            put4(p, p.dw + (int64_t)(c0 + r) * p.M + m0 + j + e,
+                 *reinterpret_cast<const float4*>(stage + r * kStageRow + e), left);
         }
       }
 #pragma unroll
@@ -481,7 +500,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(256) wgrad_join_kernel(const WgradParams p) {
   const int tile = blockIdx.y, c4 = blockIdx.x, block = threadIdx.x >> 7, r = threadIdx.x & 127;
   const size_t slot = 2 * kPartBytes / 16;
-  const float4* from = reinterpret_cast<const float4*>(p.part) + tile * slot + (size_t)block * (kPartBytes / 16) + c4 * kHalfC + r;
+  const float4* from = reinterpret_cast<const float4*>(p.part) + tile * slot + (size_t)block * (kPartBytes / 16) +
+                       c4 * kHalfC + r;
   wait_for_previous();
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int g = 0; g < p.parts; g += 8) {

@@ -111,7 +111,6 @@ struct SortShared {
   uint32_t base[kMaxBins];
   uint32_t seen[kMaxWords];
   uint32_t warp_sum[kSortWarps];
-  uint32_t below;
 };
 
 // The sum of the warps' numbers before this one, and of all; every thread of the block calls it.
@@ -136,7 +135,6 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const Embed
   if (w0 == w1) return;   // never the last block
   const uint32_t v0 = (uint32_t)w0 * 32, v1 = (uint32_t)w1 * 32;
   for (int i = t; i < w1 - w0; i += kSortThreads) sh.seen[i] = 0;
-  if (t == 0) sh.below = 0;
 
   // ---- the block's entries, in a fixed order: kScan positions of a lane
   // at a time, a warp's next to one another.  As unsigned numbers, tokens that
@@ -529,7 +527,8 @@ cudaError_t run_bwd(EmbedParams p, cudaStream_t s) {
   const dim3 block(along < kThreads ? along : kThreads, along < kThreads ? kThreads / along : 1);
   e = cudaGetLastError();
   if (e == cudaSuccess && pieces > 0)
-    e = launch_after(embed_sum_kernel<T>, dim3((pieces + block.y - 1) / block.y, (p.C / E + block.x - 1) / block.x), block, s, p);
+    e = launch_after(embed_sum_kernel<T>,
+                     dim3((pieces + block.y - 1) / block.y, (p.C / E + block.x - 1) / block.x), block, s, p);
   const int often = p.N / (kShort + 1);   // tokens that occur more than kShort times, at most
   if (e == cudaSuccess && often > 0)
     e = launch_after(embed_join_kernel<T>, dim3(often < 128 ? often : 128, (p.C / E + kJoinAlong - 1) / kJoinAlong),

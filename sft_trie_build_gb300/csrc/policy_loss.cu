@@ -259,8 +259,8 @@ __global__ void __launch_bounds__(kRowThreads) policy_short_kernel(const PolicyP
   }
 }
 
-// Forward (LSE), backward (GRAD) or both.  MANY: several blocks per row.  FOUR: a step's rows are small enough
-// for as many blocks on an SM as a pass has.
+// Forward (LSE), backward (GRAD) or both.  MANY: several blocks per row.  FOUR: a
+// step's rows are small enough for as many blocks on an SM as a pass has.
 template <typename T, bool LSE, bool GRAD, bool MANY, bool FOUR = false>
 __global__ void __launch_bounds__(kRowThreads, LSE && GRAD && !FOUR ? kStepBlocks : kPassBlocks)
     policy_kernel(const PolicyParams p) {
