@@ -564,7 +564,7 @@ extern "C" stp_status stp_embed_fwd(const stp_embed_desc* desc, const void* tabl
   EmbedParams p = embed_params(desc, d_token_ids, d_ws);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // One block checks all tokens, 4096 of them a round trip to memory, and saves the
-  // word's clearing (5 us beside a forward of 28); from rows of 1 KB on it ends before the others do.
+  // word's clearing (16384 x 4096 bf16: 36.2 -> 34.6 us); from rows of 1 KB on it ends before the others do.
   p.check = p.N > 0 && (p.N <= 4096 || p.C * (desc->dtype == STP_BF16 ? 2 : 4) >= 1024);
   p.table = table;
   p.out = out;
