@@ -735,7 +735,12 @@ stp_status stp_distill_step(const stp_distill_desc* desc, const void* logits, co
  *   d_logits_v = d_loss[n] scale (g ([v = target] - p_v) + entropy_coef p_v (ln p_v + H))
  * A negative target is a row that is not read: zeros in every output.  A row
  * whose target has probability 0 (logprob -inf) has a gradient of zeros; a row
- * that holds NaN or +inf gives NaN.  All sums are float32 in a fixed order.
+ * that holds NaN or +inf gives NaN.  A logit of probability 0 (-inf, or the
+ * type's lowest value beside others) has a gradient of 0, as long as d_loss[n]
+ * scale entropy_coef stays below 2^119 in magnitude.  Where an r A that is not
+ * clipped or exp(ref_logprob[n] - lp) leaves float32's range, the loss is
+ * infinite and d_loss[n] scale g is held at bf16's largest number.
+ * All sums are float32 in a fixed order.
  */
 typedef struct {
   int32_t n_rows;     /* N >= 0                                                  */

@@ -140,15 +140,21 @@ __device__ __forceinline__ void put_unread(const PolicyParams& p, int n, int tar
   if (!p.check && target >= p.V) atomicOr(p.err, kErrBadList);
 }
 
+// An infinite factor of a gradient (a ratio beyond float32's range) is held at
+// the largest number that bf16 has, too, so that 0 times it is 0.
+__device__ __forceinline__ float held(float x) { return isinf(x) ? copysignf(0x1.fep127f, x) : x; }
+
 // dz = p (h ln p + c), and g more for the token itself.  LSE: from the row's
-// maximum and sum (whose inverse is in h2 and c), else from lse alone.
+// maximum and sum (whose inverse is in h2 and c), else from lse alone.  Where ln p
+// lies below kLowest p is 0 already, and ln p is held there, so that its product
+// with a large weight stays finite.
 template <bool LSE>
 struct RowGrad {
   float scale, sl2, sub, up, shift, h2, c, g;
   __device__ __forceinline__ RowGrad(const PolicyParams& p, int n, const Row& r, const Terms& term) {
-    const float w = p.w[n] * p.scale, h = w * p.gamma, inv = LSE ? r.inv : 1.f;
-    g = w * term.g;
-    c = (p.gamma != 0.f ? fmaf(h, r.ent, -g) : -g) * inv;
+    const float w = p.w[n] * p.scale, h = held(w * p.gamma), inv = LSE ? r.inv : 1.f;
+    g = held(w * term.g);
+    c = held((p.gamma != 0.f ? fmaf(h, r.ent, -g) : -g) * inv);
     h2 = h * kLn2T * inv;
     scale = p.scale;
     sl2 = p.sl2;
@@ -159,7 +165,7 @@ struct RowGrad {
   __device__ __forceinline__ float operator()(float x) const {
     const float d = LSE ? (x + sub) * sl2 : fmaf(x, scale, up) * kLog2eT;
     const float l2 = LSE ? d + shift : d;   // ln p in units of ln 2
-    return ex2(d) * fmaf(h2, fmaxf(l2, -1e30f), c);
+    return ex2(d) * fmaf(h2, fmaxf(l2, kLowest), c);
   }
   // Two by two, as the pass issues more than it may; without an entropy term p times one number.
   template <bool ENT, int N>
@@ -177,7 +183,7 @@ struct RowGrad {
         float2 term = make_float2(c, c);
         if constexpr (ENT) {
           const float2 l = LSE ? __fadd2_rn(d, make_float2(shift, shift)) : d;
-          term = __ffma2_rn(make_float2(h2, h2), make_float2(fmaxf(l.x, -1e30f), fmaxf(l.y, -1e30f)), term);
+          term = __ffma2_rn(make_float2(h2, h2), make_float2(fmaxf(l.x, kLowest), fmaxf(l.y, kLowest)), term);
         }
         const float2 p2 = __fmul2_rn(make_float2(ex2(d.x), ex2(d.y)), term);
         z[e] = p2.x;
