@@ -320,7 +320,8 @@ __global__ void __launch_bounds__(kRowThreads, kPassBlocks) stats_bwd_kernel(con
 #pragma unroll
     for (int e = 0; e < N(); ++e) {
       const float lp = fmaf(z[e], scale, -lse);
-      zt = -ex2(lp * kLog2eT) * fmaf(h, fmaxf(lp, -1e30f), c);
+      // below kLowest p is 0, and ln p is held there, so that its product with a large h stays finite
+      zt = -ex2(lp * kLog2eT) * fmaf(h, fmaxf(lp, kLowest), c);
       z[e] = id + e == target ? zt + g : zt;
     }
   });
