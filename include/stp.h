@@ -817,8 +817,9 @@ stp_status stp_embed_workspace_size(const stp_embed_desc* desc, size_t* ws_bytes
  *   table         device [V, C];  out, d_out  device [N, C], rows stride apart
  *   d_token_ids   device int32 [N]
  *   accumulate    0: d_table is written in full, zeros for tokens that do not
- *                 occur; else the sums are added to it, and rows of tokens that
- *                 do not occur are not touched
+ *                 occur; else the sums are added to it (numbers below the smallest
+ *                 normal one count), and rows of tokens that do not occur are not
+ *                 touched; calls that add to the same table must not overlap
  *   d_table       device float32 [V, C]
  *   d_ws          device, 256-byte aligned; its first word is the device error
  *                 word: a token >= V sets it, and counts as negative
