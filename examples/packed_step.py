@@ -28,8 +28,8 @@ from sft_trie_build_gb300 import workloads as W  # noqa: E402
 
 @dataclass
 class Config:
-    vocab: int = 512
-    width: int = 256
+    vocab: int = 512   # with ckpt8 a multiple of 8, as every width of a gradient there
+    width: int = 256   # a multiple of 8: token vectors are whole 16 bytes
     n_q_heads: int = 4
     n_kv_heads: int = 2
     head_dim: int = 128

@@ -794,9 +794,9 @@ stp_status stp_policy_step(const stp_policy_desc* desc, const void* logits, cons
  * materialization section: rows carry token ids, pads the id 0):
  *   out[n] = scale table[token[n]],
  *   d_table[v] (+)= scale sum over n with token[n] = v of d_out[n].
- * A negative token has a vector of zeros and no gradient.  Each output is
- * rounded once; the gradient's sums are float32 in a fixed order (repeated
- * calls give the same bits).
+ * A negative token has a vector of zeros and no gradient.  A vector is a float32
+ * product, rounded to its type; the gradient's sums are float32 in a fixed order
+ * (repeated calls give the same bits), then scaled, and added where they are added.
  */
 typedef struct {
   int32_t n_tokens; /* N in [0, 2^28] (rows of a batch back to back)          */

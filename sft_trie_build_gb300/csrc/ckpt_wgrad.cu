@@ -24,9 +24,10 @@
 // tensor core waits for the reading of TMEM alone; results leave for memory
 // while it works on.
 //
-// Measured: 16384 tokens, 4096 x 6144: 451 us in a short run, 1829 TFLOP/s, 0.95 of the
-// measured bf16 burst, and 524 us in a longer one, 1573 TFLOP/s, 0.92 of the
-// sustained rate; taking the sums out costs about 20.  Tiles narrower than 256
+// Measured: 16384 tokens, 4096 x 6144: 506-524 us in a long run, 1573-1630 TFLOP/s, 0.92-0.95 of the
+// measured sustained bf16 rate, and 451-464 us in runs of a few calls, up to 1829 TFLOP/s, 0.95 of the
+// burst rate; taking the sums out costs about 20.  Adding to dW costs 42 us
+// more, and 23 more for 65531 tokens, 1000 x 523.  Tiles narrower than 256
 // columns are bound by the conversion, 0.55-0.65 us a stage whatever their width:
 // 65531 tokens, 1000 x 523: 66 us.  The warp that multiplies walks its loop as a
 // whole, so that descriptors stay in uniform registers (one lane alone took 650

@@ -16,6 +16,12 @@
 //                 another one goes to the workspace
 //   embed_join_kernel   those tokens: the sums of their pieces, in order
 // Every row of d_out is read once and every row of dE written once.  Sums are float32.
+//
+// Ranges are of equal length, so the call waits for the one with the most
+// entries.  Measured, frequent tokens all over the vocabulary and at its
+// beginning: 16384 x 4096 bf16 over 32000 tokens 127 / 130 us (the zeros hide it),
+// 65531 x 1000 float32 over 32003 95 / 148 us.  Tokens that are none are entries
+// of the last range: with 9 of 10 of them none, 191 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
